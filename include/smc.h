@@ -60,7 +60,7 @@ typedef enum { SMC_POOL_MAX = 0, SMC_POOL_MEAN = 1 } smc_pool;
 enum {
   SMC_OK = 0,
   SMC_E_ARG = -1,       /* null pointer, negative size, bad ksize/orientation/dtype value */
-  SMC_E_RANGE = -2,     /* a coordinate outside [0,batch) x [0,Z) x [0,Y) x [0,X) */
+  SMC_E_RANGE = -2,     /* a coordinate outside [0,batch) x [0,Z) x [0,Y) x [0,X); item offsets out of range */
   SMC_E_DUPLICATE = -3, /* the same (b,z,y,x) appears twice */
   SMC_E_DTYPE = -4,     /* unsupported dtype for this call */
   SMC_E_SHAPE = -5,     /* channel count or N does not match the map / limits */
@@ -320,6 +320,139 @@ SMC_API int smc_group_norm(const void* x, int64_t n, int64_t c, const int32_t* c
                    int32_t groups, const double* stats, const void* gamma, const void* beta, float eps,
                    int32_t act, void* out, int32_t dtype, void* stream);
 
+/*
+ * smc_layer_norm -- layer norm over each row's c channels and an activation
+ * (the norms of the sparse ResBlocks and transformer blocks, with or without
+ * affine parameters: shared sparse-core commit log; LATO.2 MLX port README
+ * "Status"):
+ *   out = round(act(gamma * (x - mean) * rstd + beta))
+ * with the row's mean and rstd = 1 / sqrt(var + eps) (biased variance), all in
+ * fp32.
+ *
+ * x     : device [n, c] row-major, dtype `dtype`.
+ * gamma, beta : device [c] in dtype, or NULL (1 and 0).
+ * eps   : finite, >= 0.
+ * act   : SMC_ACT_*.
+ * out   : device [n, c]; may be x itself, must not overlap anything else.
+ * stats : device fp32 [n, 2], 8-byte aligned, or NULL: receives (mean, rstd)
+ *         of each row, what smc_layer_norm_backward takes.
+ * Rows and parameters that are 16-byte aligned, with c * sizeof(dtype) a
+ * multiple of 16, move as 16-byte accesses; every other shape runs too.
+ * Asynchronous on `stream`; n == 0 does nothing.  Errors: SMC_E_ARG,
+ * SMC_E_DTYPE, SMC_E_SHAPE (c above 2^24), SMC_E_ALIGN, SMC_E_ALIAS,
+ * SMC_E_CUDA.
+ */
+SMC_API int smc_layer_norm(const void* x, int64_t n, int64_t c, const void* gamma, const void* beta, float eps,
+                   int32_t act, void* out, float* stats, int32_t dtype, void* stream);
+
+/*
+ * smc_layer_norm_backward -- the gradients of smc_layer_norm:
+ *   dz = dy * act'(z),  g = dz * gamma,  xh = (x - mean) * rstd
+ *   dx = rstd * (g - mean_c(g) - xh * mean_c(g * xh))
+ *   dgamma = sum over rows of dz * xh,  dbeta = sum over rows of dz
+ * dy, x : device [n, c]; stats: the forward call's [n, 2]; gamma, beta, act as
+ * in the forward call.  dx: device [n, c]; may be dy or x itself.  dgamma,
+ * dbeta: device [c] in dtype, overwritten, or NULL (either alone, or both
+ * left out).  Sums in fp32, and over the rows in a fixed order: the same call
+ * gives the same bits.  Scratch comes from the library's stream-ordered pool.
+ * n == 0 zeroes dgamma and dbeta.  Asynchronous on `stream`.  Errors as
+ * smc_layer_norm, and SMC_E_OOM.
+ */
+SMC_API int smc_layer_norm_backward(const void* dy, const void* x, int64_t n, int64_t c, const float* stats,
+                            const void* gamma, const void* beta, int32_t act, void* dx, void* dgamma, void* dbeta,
+                            int32_t dtype, void* stream);
+
+/* Which channels of a head smc_rotary turns together: (2p, 2p + 1), or
+ * (p, P + p) with P = axes * nfreq. */
+typedef enum { SMC_ROTARY_INTERLEAVED = 0, SMC_ROTARY_HALF = 1 } smc_rotary_layout;
+
+/*
+ * smc_rotary -- rotary positions (rope phases from voxel coordinates: Pixal3D
+ * commit log; shared sparse-core commit log).  Pair p = a * nfreq + f of every
+ * head of row n is turned by positions[n, a] * freqs[a, f] and multiplied by
+ * `scale`:
+ *   (u, v) -> scale * (u cos - v sin, u sin + v cos)
+ * The first 2 * axes * nfreq channels of a head are turned, the others copied.
+ * inverse = 1 turns by the negative angle: with the same scale, the gradient
+ * of the forward call.  Stretched contexts are a matter of freqs and scale.
+ *
+ * x          : device [n, heads, dim], the last axis dense; x_stride (host,
+ *              elements) = (row, head), or NULL (dense).
+ * positions  : device int32 [n, axes] with pos_stride (row, axis), or NULL
+ *              (dense); any int32 value.
+ * freqs      : device fp64 [axes, nfreq], radians per step.  Angles are formed
+ *              and reduced in fp64: exact to fp32 rounding at any position.
+ * out        : device [n, heads, dim] with out_stride; may be x itself with
+ *              x's strides, must not overlap anything otherwise, nor itself.
+ * Asynchronous on `stream`; n == 0 does nothing.  Errors: SMC_E_ARG (also a
+ * negative stride or a scale that is not finite), SMC_E_DTYPE, SMC_E_SHAPE
+ * (2 * axes * nfreq above dim), SMC_E_ALIGN, SMC_E_ALIAS, SMC_E_CUDA.
+ */
+SMC_API int smc_rotary(const void* x, const int64_t x_stride[2], int64_t n, int32_t heads, int32_t dim,
+               const int32_t* positions, const int64_t pos_stride[2], const double* freqs, int32_t axes,
+               int32_t nfreq, int32_t layout, float scale, int32_t inverse, void* out, const int64_t out_stride[2],
+               int32_t dtype, void* stream);
+
+/*
+ * smc_attention -- attention of each item's queries over the item's keys (the
+ * transformer blocks over the voxels of a batch: full self-attention, windows
+ * as items, and attention over conditioning tokens; Pixal3D working notes and
+ * MLX README "Status"):
+ *   out = softmax(scale * q k^T) v,  lse = log sum exp of the scaled scores
+ *
+ * q          : device [n, heads, dim], k and v: device [m, kv_heads, dim], the
+ *              last axis dense, strides (host, elements) = (row, head) or NULL
+ *              (dense); zero strides are fine.  Query head h reads key/value
+ *              head h / (heads / kv_heads).
+ * q_offsets, k_offsets : device int32 [items + 1], ascending: item i has the
+ *              queries q_offsets[i] .. q_offsets[i + 1] - 1 and the keys
+ *              k_offsets[i] .. k_offsets[i + 1] - 1.  They may be the same
+ *              array.  Either side of an item may be empty.  Rows outside
+ *              every item are left as they were.
+ * scale      : finite, > 0.
+ * causal     : 1: query i of an item sees its keys j <= i + keys - queries (the
+ *              last query sees every key); 0: all of them.
+ * out        : device [n, heads, dim] dense; must not overlap any input.  A
+ *              query that sees no key gets zeros and lse = -infinity.
+ * lse        : device fp32 [n, heads] or NULL.
+ * Scores, softmax and sums are fp32; bf16 / fp16 inputs round the (unnormalised)
+ * probabilities to the input type for the product with v.  Keys outside an
+ * item never reach its rows, whatever they hold.  A key that only the causal
+ * mask hides from a query must be finite, as in any product by zero.
+ * Offsets that descend or leave [0, n] / [0, m] are cut to the buffers and
+ * reported by smc_status as SMC_E_RANGE; the results are then undefined.
+ * Asynchronous on `stream`.  Errors: SMC_E_ARG, SMC_E_DTYPE, SMC_E_SHAPE (dim
+ * above 128, heads not a multiple of kv_heads or over 64 of them sharing one,
+ * rows beyond 2^31), SMC_E_ALIGN, SMC_E_ALIAS, SMC_E_OOM, SMC_E_CUDA.
+ */
+SMC_API int smc_attention(const void* q, const int64_t q_stride[2], const void* k, const int64_t k_stride[2],
+                  const void* v, const int64_t v_stride[2], const int32_t* q_offsets, const int32_t* k_offsets,
+                  int32_t items, int64_t n, int64_t m, int32_t heads, int32_t kv_heads, int32_t dim, float scale,
+                  int32_t causal, void* out, float* lse, int32_t dtype, void* stream);
+
+/*
+ * smc_attention_backward -- the gradients of smc_attention, with the
+ * probabilities recomputed from the saved lse:
+ *   P = exp(scale * q k^T - lse),  dv = P^T dout,
+ *   dS = P * (dout v^T - rowsum(dout * out)),  dq = scale dS k,  dk = scale dS^T q
+ * The gradients of shared key/value heads are summed over their query heads.
+ * out (dense) and lse as smc_attention wrote them; the other arguments as
+ * there.  dout: device [n, heads, dim] with dout_stride.  dq: device [n, heads, dim], dk and dv:
+ * device [m, kv_heads, dim], each with its strides (views of one packed
+ * buffer may interleave); they must not overlap the inputs.  Gradients of
+ * queries and keys that nothing pairs with are zero; rows outside every item
+ * are left as they were.  No atomics: the same call gives the same bits.
+ * Scratch (fp32 [n, heads]) comes from the library's stream-ordered pool.
+ * Asynchronous on `stream`.  Errors as smc_attention.
+ */
+SMC_API int smc_attention_backward(const void* dout, const int64_t dout_stride[2], const void* q,
+                           const int64_t q_stride[2], const void* k, const int64_t k_stride[2], const void* v,
+                           const int64_t v_stride[2], const void* out, const float* lse, const int32_t* q_offsets,
+                           const int32_t* k_offsets, int32_t items, int64_t n, int64_t m, int32_t heads,
+                           int32_t kv_heads, int32_t dim, float scale, int32_t causal, void* dq,
+                           const int64_t dq_stride[2], void* dk, const int64_t dk_stride[2], void* dv,
+                           const int64_t dv_stride[2], int32_t dtype, void* stream);
+
 /* n and the per-offset pair counts counts[27] (host) of a map: the hit
  * counts of the indice map's 27 offsets (LATO.2 MLX port README, "Correctness":
  * indice-map hit rates). */
@@ -368,7 +501,9 @@ SMC_API int smc_set_schedule_segment(int64_t rows);
 SMC_API int smc_free_map(smc_map* map);
 
 /* Synchronise `stream`, then return and clear the device-side error word
- * (SMC_E_TIMEOUT if a bounded wait in a conv kernel ran out), or SMC_OK. */
+ * (SMC_E_TIMEOUT if a bounded wait in a conv or attention kernel ran out,
+ * SMC_E_RANGE if an attention call met item offsets out of order or range),
+ * or SMC_OK. */
 SMC_API int smc_status(void* stream);
 
 /* Static description of an error code. */

@@ -14,3 +14,6 @@ from ._binding import (  # noqa: F401
     downsample, upsample, POOL_MODES, set_conv_epilogue, set_alloc_fail_after, set_wait_limit_ns, set_scan_hold,
     set_schedule_segment, set_conv_priority,
 )
+from ._tokens import (  # noqa: F401
+    ROTARY_LAYOUTS, attention, attention_backward, layer_norm, layer_norm_backward, rotary, rotary_freqs,
+)

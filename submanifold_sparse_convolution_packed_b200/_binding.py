@@ -33,7 +33,8 @@ EXPORTS = [
     "smc_set_map_lookup", "smc_map_stream_wait", "smc_subdivide", "smc_conv_ex", "smc_group_stats",
     "smc_group_norm", "smc_downsample", "smc_upsample", "smc_set_conv_epilogue",
     "smc_set_alloc_fail_after", "smc_set_wait_limit_ns", "smc_set_scan_hold", "smc_set_schedule_segment",
-    "smc_set_conv_priority",
+    "smc_set_conv_priority", "smc_layer_norm", "smc_layer_norm_backward", "smc_rotary", "smc_attention",
+    "smc_attention_backward",
 ]
 
 
@@ -90,6 +91,12 @@ def lib() -> ctypes.CDLL:
         L.smc_set_scan_hold.argtypes = [i64]
         L.smc_set_schedule_segment.argtypes = [i64]
         L.smc_set_conv_priority.argtypes = [i32]
+        f32 = ctypes.c_float
+        L.smc_layer_norm.argtypes = [P, i64, i64, P, P, f32, i32, P, P, i32, P]
+        L.smc_layer_norm_backward.argtypes = [P, P, i64, i64, P, P, P, i32, P, P, P, i32, P]
+        L.smc_rotary.argtypes = [P, P, i64, i32, i32, P, P, P, i32, i32, i32, f32, i32, P, P, i32, P]
+        L.smc_attention.argtypes = [P] * 8 + [i32, i64, i64, i32, i32, i32, f32, i32, P, P, i32, P]
+        L.smc_attention_backward.argtypes = [P] * 12 + [i32, i64, i64, i32, i32, i32, f32, i32] + [P] * 6 + [i32, P]
         for name in EXPORTS:
             if name != "smc_strerror":
                 getattr(L, name).restype = ctypes.c_int
@@ -489,7 +496,8 @@ def group_norm(x: torch.Tensor, coords: torch.Tensor, batch: int, groups: int, s
 
 
 def status(stream=None) -> None:
-    """Synchronise the stream and raise if a conv kernel reported a timeout."""
+    """Synchronise the stream and raise if a conv or attention kernel reported
+    a timeout, or an attention call met item offsets out of order or range."""
     _check(lib().smc_status(_stream(stream)), "smc_status")
 
 

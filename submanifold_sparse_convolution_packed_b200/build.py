@@ -16,7 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsmc.so")
 SOURCES = ["api.cu", "map_build.cu", "conv_simt.cu", "conv_tc.cu", "conv_offsets.cu", "norm.cu", "resample.cu",
-           "noalloc.cu"]
+           "noalloc.cu", "layer_norm.cu", "rotary.cu", "attn_simt.cu", "api_tokens.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -41,7 +41,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-           "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",
+           "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr", "--threads", "0",
            "-I", os.path.join(HERE, "..", "include")]
     if verbose:
         cmd += ["-Xptxas", "-v"]

@@ -70,7 +70,8 @@ constexpr double kOccMinSites = 8388608.0;
 
 constexpr int kMaxDevices = 64;
 
-// Per-device error word of the conv kernels (bounded-wait timeouts).
+// Per-device error word of the conv and attention kernels (bounded-wait
+// timeouts, item offsets out of range).
 uint32_t* g_status[kMaxDevices] = {};
 // Per-device stream-ordered memory pool that keeps its memory between builds
 // (the default pool returns memory to the driver at every synchronisation,
@@ -568,6 +569,11 @@ namespace smc {
 void count_launches(int k) { g_launches.fetch_add(k, std::memory_order_relaxed); }
 uint64_t scan_wait_limit_ns() { return static_cast<uint64_t>(g_wait_limit_ns.load()); }
 int64_t scan_hold_ticket() { return g_scan_hold.load(); }
+uint32_t* status_word(int dev) { return device_status(dev); }
+int pending_error() { return pending_cuda_error(); }
+cudaError_t scratch_alloc(void** p, size_t bytes, int dev, cudaStream_t s) {
+  return pool_alloc(p, bytes, device_pool(dev), s);
+}
 }  // namespace smc
 
 extern "C" {
@@ -576,7 +582,7 @@ const char* smc_strerror(int code) {
   switch (code) {
     case SMC_OK: return "ok";
     case SMC_E_ARG: return "invalid argument";
-    case SMC_E_RANGE: return "coordinate outside the grid or batch range";
+    case SMC_E_RANGE: return "coordinate outside the grid or batch range, or item offsets out of order or range";
     case SMC_E_DUPLICATE: return "duplicate coordinate";
     case SMC_E_DTYPE: return "unsupported dtype";
     case SMC_E_SHAPE: return "shape mismatch";
@@ -1192,6 +1198,7 @@ int smc_status(void* stream) {
   uint32_t h = 0;
   if (cudaMemcpy(&h, st, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return SMC_E_CUDA;
   if (h) cudaMemset(st, 0, sizeof(uint32_t));
+  if (h & smc::kErrRange) return SMC_E_RANGE;
   return (h & smc::kErrTimeout) ? SMC_E_TIMEOUT : SMC_OK;
 }
 

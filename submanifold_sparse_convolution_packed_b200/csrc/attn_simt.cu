@@ -1,0 +1,392 @@
+// Attention within each item and its gradients, in fp32 FMA: every type, every
+// head width up to 128, every stride (the transformer blocks' attention of the
+// pages, Pixal3D MLX README "Status" and working notes, over the voxels of one
+// item).  The tensor-core kernels take the bf16 / fp16 shapes they can.
+//
+//   S = scale Q K^T,  P = softmax(S),  O = P V,  lse = log sum exp S
+//   dP = dO V^T,  delta = rowsum(dO * O),  dS = P * (dP - delta)
+//   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO,  P = exp(S - lse)
+//
+// The heads that share a key/value head are packed into the rows of one tile
+// (row = query * G + head of the group), so a tile's keys and values are
+// loaded once for all of them, and the gradients of shared heads add up in one
+// accumulator.  One pass over the keys with a running maximum and sum; the
+// backward pass recomputes P from the saved lse in two kernels, one tile of
+// queries (dQ) or of keys (dK, dV) per block, so nothing is added with atomics
+// and a call gives the same bits every time.
+//
+// 64 x 64 tiles, 256 threads, each with 4 x 4 scores and 4 rows of the
+// accumulator; operands are fp32 in shared memory, rows padded by 16 bytes so
+// that the float4 reads along a row meet no bank twice.
+#include "kernels.h"
+#include "tokens.cuh"
+
+namespace smc {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 64;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// kTile rows of one operand into shared memory as fp32, zero behind `rows` and
+// behind `dim`.  Row r is packed row first + r: source row (first + r) / group
+// of the item, head `head` + (first + r) % group.
+template <typename T, int DP>
+__device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t row_stride, int64_t head_stride, int head,
+                                          int group, int32_t first, int rows, int dim) {
+  for (int i = threadIdx.x; i < kTile * DP; i += kThreads) {
+    const int r = i / DP, c = i % DP;
+    float v = 0.f;
+    if (r < rows && c < dim) {
+      const int pr = first + r;
+      v = to_f(src[static_cast<int64_t>(pr / group) * row_stride + (head + pr % group) * head_stride + c]);
+    }
+    dst[r * (DP + 4) + c] = v;
+  }
+}
+
+// acc[i][j] = A[4 ty + i] . B[tx + 16 j]
+template <int DP>
+__device__ __forceinline__ void mm_nt(const float* A, const float* B, int ty, int tx, float (&acc)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+  for (int d = 0; d < DP; d += 4) {
+    float4 a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * (DP + 4) + d);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * (DP + 4) + d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = fmaf(a[i].w, b[j].w, fmaf(a[i].z, b[j].z, fmaf(a[i].y, b[j].y, fmaf(a[i].x, b[j].x, acc[i][j]))));
+  }
+}
+
+// Column of the accumulator's element j of thread tx: runs of up to 4.
+template <int DP>
+__device__ __forceinline__ int col_of(int tx, int j) {
+  constexpr int kRun = DP / 16 < 4 ? DP / 16 : 4;
+  return j / kRun * 16 * kRun + tx * kRun + j % kRun;
+}
+
+// acc[i][j] += sum_k P[4 ty + i][k] * B[k][col_of(tx, j)]
+template <int DP>
+__device__ __forceinline__ void mm_nn(const float* P, const float* B, int ty, int tx, float (&acc)[4][DP / 16]) {
+  constexpr int W = DP / 16, kRun = W < 4 ? W : 4;
+#pragma unroll 2
+  for (int k = 0; k < kTile; k += 4) {
+    float4 p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(P + (4 * ty + i) * (kTile + 4) + k);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      float b[W];
+#pragma unroll
+      for (int j = 0; j < W; j += kRun) {
+        const float* at = B + (k + kk) * (DP + 4) + col_of<DP>(tx, j);
+        if constexpr (kRun == 4) {
+          const float4 t = *reinterpret_cast<const float4*>(at);
+          b[j] = t.x, b[j + 1] = t.y, b[j + 2] = t.z, b[j + 3] = t.w;
+        } else {
+          const float2 t = *reinterpret_cast<const float2*>(at);
+          b[j] = t.x, b[j + 1] = t.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float s = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+#pragma unroll
+        for (int j = 0; j < W; ++j) acc[i][j] = fmaf(s, b[j], acc[i][j]);
+      }
+    }
+  }
+}
+
+// Keys that query `qi` of an item sees: the first `seen` ones.
+__device__ __forceinline__ int32_t keys_seen(const Unit& u, int32_t qi, bool causal) {
+  if (!causal) return u.k.count;
+  const int64_t s = static_cast<int64_t>(qi) + u.k.count - u.q.count + 1;
+  return s < 0 ? 0 : (s > u.k.count ? u.k.count : static_cast<int32_t>(s));
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a) {
+  extern __shared__ float sm[];
+  __shared__ Unit unit;
+  constexpr int LD = DP + 4, W = DP / 16;
+  float *sq = sm, *sk = sq + kTile * LD, *sv = sk + kTile * LD, *sp = sv + kTile * LD;
+  const int group = a.heads / a.kv_heads, per_tile = kTile / group;
+  find_unit<kThreads>(a.q_off, a.k_off, a.items, a.n, a.m, per_tile, 0, false, blockIdx.x, &unit, a.err);
+  if (unit.item < 0) return;
+  const Unit u = unit;
+  const int hk = blockIdx.y, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int32_t q0 = u.tile * per_tile, queries = u.q.count - q0 < per_tile ? u.q.count - q0 : per_tile;
+  const int rows = queries * group;
+  const T* q = static_cast<const T*>(a.q) + u.q.begin * a.q_stride[0];
+  const T* k = static_cast<const T*>(a.k) + u.k.begin * a.k_stride[0] + hk * a.k_stride[1];
+  const T* v = static_cast<const T*>(a.v) + u.k.begin * a.v_stride[0] + hk * a.v_stride[1];
+  load_tile<T, DP>(sq, q, a.q_stride[0], a.q_stride[1], hk * group, group, q0 * group, rows, a.dim);
+  const float c = a.scale * kLog2e;
+  int32_t seen[4];
+  float top[4], sum[4], o[4][W];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * ty + i;
+    seen[i] = r < rows ? keys_seen(u, q0 + r / group, a.causal) : 0;
+    top[i] = -INFINITY;
+    sum[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) o[i][j] = 0.f;
+  }
+  const int32_t last = keys_seen(u, q0 + queries - 1, a.causal);
+  for (int32_t k0 = 0; k0 < last; k0 += kTile) {
+    const int kr = u.k.count - k0 < kTile ? u.k.count - k0 : kTile;
+    __syncthreads();
+    load_tile<T, DP>(sk, k, a.k_stride[0], 0, 0, 1, k0, kr, a.dim);
+    load_tile<T, DP>(sv, v, a.v_stride[0], 0, 0, 1, k0, kr, a.dim);
+    __syncthreads();
+    float s[4][4];
+    mm_nt<DP>(sq, sk, ty, tx, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (k0 + tx + 16 * j >= seen[i]) s[i][j] = -INFINITY;
+        m = fmaxf(m, s[i][j]);
+      }
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+      // top is the rounded product with c, so that an unchanged maximum keeps
+      // the sums by exactly 1 (a fused difference would be off by an ulp of
+      // the product, tile after tile)
+      m = fmaxf(__fmul_rn(m, c), top[i]);
+      const float base = m == -INFINITY ? 0.f : m;  // nothing seen yet: every term is exp2(-inf) = 0
+      const float keep = exp2f(top[i] - base);
+      float t = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = exp2f(fmaf(s[i][j], c, -base));
+        t += s[i][j];
+      }
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
+      sum[i] = sum[i] * keep + t;
+      top[i] = m;
+#pragma unroll
+      for (int j = 0; j < W; ++j) o[i][j] *= keep;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sp[(4 * ty + i) * (kTile + 4) + tx + 16 * j] = s[i][j];
+    }
+    __syncwarp();  // a warp reads back its own rows of P only
+    mm_nn<DP>(sp, sv, ty, tx, o);
+  }
+  T* out = static_cast<T*>(a.out_w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * ty + i;
+    if (r >= rows) continue;
+    const int64_t at = static_cast<int64_t>(u.q.begin + q0 + r / group) * a.heads + hk * group + r % group;
+    const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const int cc = col_of<DP>(tx, j);
+      if (cc < a.dim) out[at * a.dim + cc] = from_f<T>(o[i][j] * inv);
+    }
+    if (a.lse_w && tx == 0) a.lse_w[at] = sum[i] == 0.f ? -INFINITY : (top[i] + log2f(sum[i])) * kLn2;
+  }
+}
+
+// kDQ: a tile of packed queries against all its keys -> dQ.  Otherwise a tile
+// of keys against all its packed queries -> dK, dV.  A1, A2 stay; B1, B2 pass.
+template <typename T, int DP, bool kDQ>
+__global__ void __launch_bounds__(kThreads) k_attn_bwd(const AttnArgs a) {
+  extern __shared__ float sm[];
+  __shared__ Unit unit;
+  __shared__ float s_lse[kTile], s_delta[kTile];
+  constexpr int LD = DP + 4, W = DP / 16;
+  float *a1 = sm, *a2 = a1 + kTile * LD, *b1 = a2 + kTile * LD, *b2 = b1 + kTile * LD, *sp = b2 + kTile * LD;
+  const int group = a.heads / a.kv_heads, per_tile = kTile / group;
+  find_unit<kThreads>(a.q_off, a.k_off, a.items, a.n, a.m, kDQ ? per_tile : kTile, 0, !kDQ, blockIdx.x, &unit, a.err);
+  if (unit.item < 0) return;
+  const Unit u = unit;
+  const int hk = blockIdx.y, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const T* q = static_cast<const T*>(a.q) + u.q.begin * a.q_stride[0];
+  const T* dout = static_cast<const T*>(a.dout) + u.q.begin * a.dout_stride[0];
+  const T* k = static_cast<const T*>(a.k) + u.k.begin * a.k_stride[0] + hk * a.k_stride[1];
+  const T* v = static_cast<const T*>(a.v) + u.k.begin * a.v_stride[0] + hk * a.v_stride[1];
+  const float c = a.scale * kLog2e;
+  auto load_q = [&](float* d1, float* d2, int32_t first, int rows) {
+    load_tile<T, DP>(d1, q, a.q_stride[0], a.q_stride[1], hk * group, group, first, rows, a.dim);
+    load_tile<T, DP>(d2, dout, a.dout_stride[0], a.dout_stride[1], hk * group, group, first, rows, a.dim);
+    if (threadIdx.x < kTile) {
+      const int r = threadIdx.x;
+      float l = INFINITY, e = 0.f;  // exp2(s - inf) = 0: rows that are not there, or saw no key
+      if (r < rows) {
+        const int64_t at = static_cast<int64_t>(u.q.begin + (first + r) / group) * a.heads + hk * group + (first + r) % group;
+        l = a.lse[at] == -INFINITY ? INFINITY : a.lse[at] * kLog2e;
+        e = a.delta[at];
+      }
+      s_lse[r] = l;
+      s_delta[r] = e;
+    }
+  };
+  auto load_k = [&](float* d1, float* d2, int32_t first) {
+    const int rows = u.k.count - first < kTile ? u.k.count - first : kTile;
+    load_tile<T, DP>(d1, k, a.k_stride[0], 0, 0, 1, first, rows, a.dim);
+    load_tile<T, DP>(d2, v, a.v_stride[0], 0, 0, 1, first, rows, a.dim);
+  };
+  float acc1[4][W], acc2[4][W];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < W; ++j) acc1[i][j] = acc2[i][j] = 0.f;
+  const int32_t all = u.q.count * group;  // packed rows of the item
+  int32_t t0, t1, first;                  // the tile's first row, and the range of what passes
+  int rows;
+  if constexpr (kDQ) {
+    t0 = u.tile * per_tile * group;
+    rows = all - t0 < per_tile * group ? all - t0 : per_tile * group;
+    load_q(a1, a2, t0, rows);
+    first = 0;
+    t1 = keys_seen(u, (t0 + rows - 1) / group, a.causal);
+  } else {
+    t0 = u.tile * kTile;
+    rows = u.k.count - t0 < kTile ? u.k.count - t0 : kTile;
+    load_k(a1, a2, t0);
+    // the first query that sees key t0
+    const int64_t f = a.causal ? static_cast<int64_t>(t0) + u.q.count - u.k.count : 0;
+    first = (f < 0 ? 0 : static_cast<int32_t>(f)) * group;
+    t1 = all;
+  }
+  for (int32_t b0 = first; b0 < t1; b0 += kTile) {
+    __syncthreads();
+    if constexpr (kDQ) load_k(b1, b2, b0);
+    else load_q(b1, b2, b0, all - b0 < kTile ? all - b0 : kTile);
+    __syncthreads();
+    float s[4][4], dp[4][4];
+    mm_nt<DP>(a1, b1, ty, tx, s);
+    mm_nt<DP>(a2, b2, ty, tx, dp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 4 * ty + i, x = tx + 16 * j;
+        const int lr = kDQ ? r : x;  // the query's place in the tile
+        const int32_t pq = (kDQ ? t0 + r : b0 + x), key = kDQ ? b0 + x : t0 + r;
+        const bool see = pq < all && key < keys_seen(u, pq / group, a.causal);
+        const float p = see ? exp2f(s[i][j] * c - s_lse[lr]) : 0.f;
+        s[i][j] = p;
+        dp[i][j] = see ? p * (dp[i][j] - s_delta[lr]) : 0.f;
+      }
+    }
+    if constexpr (!kDQ) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sp[(4 * ty + i) * (kTile + 4) + tx + 16 * j] = s[i][j];
+      __syncwarp();
+      mm_nn<DP>(sp, b2, ty, tx, acc2);
+      __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sp[(4 * ty + i) * (kTile + 4) + tx + 16 * j] = dp[i][j];
+    __syncwarp();
+    mm_nn<DP>(sp, b1, ty, tx, acc1);
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * ty + i;
+    if (r >= rows) continue;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const int cc = col_of<DP>(tx, j);
+      if (cc >= a.dim) continue;
+      if constexpr (kDQ) {
+        const int pr = t0 + r;
+        static_cast<T*>(a.dq)[static_cast<int64_t>(u.q.begin + pr / group) * a.dq_stride[0] +
+                              (hk * group + pr % group) * a.dq_stride[1] + cc] = from_f<T>(acc1[i][j] * a.scale);
+      } else {
+        const int64_t row = static_cast<int64_t>(u.k.begin) + t0 + r;
+        static_cast<T*>(a.dk)[row * a.dk_stride[0] + hk * a.dk_stride[1] + cc] = from_f<T>(acc1[i][j] * a.scale);
+        static_cast<T*>(a.dv)[row * a.dv_stride[0] + hk * a.dv_stride[1] + cc] = from_f<T>(acc2[i][j]);
+      }
+    }
+  }
+}
+
+// delta[row, head] = sum of dO * O over the head, one warp each.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_attn_delta(const AttnArgs a) {
+  const int64_t total = a.n * a.heads;
+  const int lane = threadIdx.x & 31;
+  for (int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5; w < total;
+       w += static_cast<int64_t>(gridDim.x) * (kThreads / 32)) {
+    const int64_t row = w / a.heads;
+    const T* o = static_cast<const T*>(a.out) + w * a.dim;
+    const T* d = static_cast<const T*>(a.dout) + row * a.dout_stride[0] + (w - row * a.heads) * a.dout_stride[1];
+    float s = 0.f;
+    for (int j = lane; j < a.dim; j += 32) s += to_f(o[j]) * to_f(d[j]);
+    s = group_sum<32>(s);
+    if (lane == 0) a.delta[w] = s;
+  }
+}
+
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+}
+
+template <typename T, int DP>
+cudaError_t launch_dim(const AttnArgs& a, bool backward, cudaStream_t s) {
+  const int per_tile = kTile / (a.heads / a.kv_heads);
+  const dim3 qgrid(static_cast<unsigned>(a.n / per_tile + a.items), a.kv_heads);
+  const size_t tile = kTile * (DP + 4) * sizeof(float), extra = kTile * (kTile + 4) * sizeof(float);
+  cudaError_t e;
+  if (!backward) {
+    if ((e = allow_smem(k_attn<T, DP>, 3 * tile + extra)) != cudaSuccess) return e;
+    k_attn<T, DP><<<qgrid, kThreads, 3 * tile + extra, s>>>(a);
+    count_launches(1);
+    return cudaGetLastError();
+  }
+  if ((e = allow_smem(k_attn_bwd<T, DP, true>, 4 * tile + extra)) != cudaSuccess) return e;
+  if ((e = allow_smem(k_attn_bwd<T, DP, false>, 4 * tile + extra)) != cudaSuccess) return e;
+  const int64_t warps = a.n * a.heads, want = (warps + 7) / 8;
+  if (a.n > 0) {
+    k_attn_delta<T><<<static_cast<unsigned>(want < 4096 ? want : 4096), kThreads, 0, s>>>(a);
+    k_attn_bwd<T, DP, true><<<qgrid, kThreads, 4 * tile + extra, s>>>(a);
+    count_launches(2);
+  }
+  if (a.m > 0) {
+    const dim3 kgrid(static_cast<unsigned>(a.m / kTile + a.items), a.kv_heads);
+    k_attn_bwd<T, DP, false><<<kgrid, kThreads, 4 * tile + extra, s>>>(a);
+    count_launches(1);
+  }
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_typed(const AttnArgs& a, bool backward, cudaStream_t s) {
+  if (a.dim <= 32) return launch_dim<T, 32>(a, backward, s);
+  if (a.dim <= 64) return launch_dim<T, 64>(a, backward, s);
+  return launch_dim<T, 128>(a, backward, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_simt(const AttnArgs& a, bool backward, cudaStream_t s) {
+  if (a.dtype == kF32) return launch_typed<float>(a, backward, s);
+  if (a.dtype == kBF16) return launch_typed<__nv_bfloat16>(a, backward, s);
+  return launch_typed<__half>(a, backward, s);
+}
+
+}  // namespace smc

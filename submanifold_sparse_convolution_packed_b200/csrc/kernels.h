@@ -157,6 +157,68 @@ cudaError_t launch_group_norm(const void* x, int64_t n, int c, const int32_t* co
                               const double* stats, const void* gamma, const void* beta, float eps, int act,
                               void* out, int dtype, cudaStream_t s);
 
+// Shared with the C ABI's other file (api.cu): the device's error word, a
+// pending CUDA error as SMC_E_CUDA, and scratch from the device's
+// stream-ordered pool (freed with cudaFreeAsync on the same stream).
+uint32_t* status_word(int dev);
+int pending_error();
+cudaError_t scratch_alloc(void** p, size_t bytes, int dev, cudaStream_t s);
+
+// Layer norm over each row's channels (layer_norm.cu).  dy null: out = act(
+// gamma * (x - mean) * rstd + beta), stats (mean, rstd) written when given.
+// dy given: out = dx from the stats; with part ([layer_norm_parts, 2, c]
+// fp32 scratch) the channel sums go to dgamma / dbeta.
+struct LayerNormArgs {
+  const void *x, *dy, *gamma, *beta;
+  float* stats;  // [n, 2]
+  void *out, *dgamma, *dbeta;
+  float* part;
+  int64_t n;
+  int c, act, dtype;
+  float eps;
+};
+int64_t layer_norm_parts(const LayerNormArgs& a, int sms);
+cudaError_t launch_layer_norm(const LayerNormArgs& a, int sms, cudaStream_t s);
+
+// Rotary positions (rotary.cu); strides in elements.
+struct RotaryArgs {
+  const void* x;
+  void* out;
+  int64_t x_stride[2], out_stride[2];  // row, head
+  const int32_t* positions;
+  int64_t pos_stride[2];  // row, axis
+  const double* freqs;    // [axes, nfreq]
+  int64_t n;
+  int heads, dim, axes, nfreq, dtype;
+  float scale;
+  bool half, inverse;
+};
+cudaError_t launch_rotary(const RotaryArgs& a, int sms, cudaStream_t s);
+
+// Attention within items (attn_simt.cu); strides (row, head) in elements.
+struct AttnArgs {
+  const void *q, *k, *v;
+  int64_t q_stride[2], k_stride[2], v_stride[2];
+  const int32_t *q_off, *k_off;  // [items + 1]
+  int64_t n, m;                  // rows of q, rows of k and v
+  int items, heads, kv_heads, dim, dtype;
+  float scale;
+  bool causal;
+  uint32_t* err;
+  // forward
+  void* out_w;    // [n, heads, dim]
+  float* lse_w;   // [n, heads] or null
+  // backward
+  const void *out, *dout;  // out [n, heads, dim]
+  int64_t dout_stride[2];
+  const float* lse;
+  float* delta;  // [n, heads] scratch
+  void *dq, *dk, *dv;
+  int64_t dq_stride[2], dk_stride[2], dv_stride[2];
+};
+// FMA kernels: every dtype, dim <= 128, heads / kv_heads <= 64.
+cudaError_t launch_attn_simt(const AttnArgs& a, bool backward, cudaStream_t s);
+
 // dtype codes as in smc.h
 enum DType : int { kF32 = 0, kBF16 = 1, kF16 = 2 };
 
@@ -197,6 +259,5 @@ int conv_variant();
 // Per-offset gather-GEMM-scatter over the map's pair lists (bf16/fp16 on the
 // tensor-core shapes, k = 3); acc is [n, cout] fp32 scratch.
 cudaError_t launch_conv_offsets(const ConvArgs& a, float* acc, cudaStream_t s);
-
 
 }  // namespace smc
