@@ -269,7 +269,17 @@ int smc_attention(const void* q, const int64_t q_stride[2], const void* k, const
   if (!a.err) return SMC_E_OOM;
   a.out_w = out;
   a.lse_w = lse;
-  return outcome(smc::launch_attn_simt(a, false, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!smc::attn_tc_supported(a)) return outcome(smc::launch_attn_simt(a, false, s));
+  void* scratch = nullptr;
+  const int64_t bytes = smc::attn_tc_scratch(a, dev.sms);
+  if (bytes > 0 && smc::scratch_alloc(&scratch, static_cast<size_t>(bytes), dev.id, s) != cudaSuccess) {
+    cudaGetLastError();
+    return SMC_E_OOM;
+  }
+  const cudaError_t e = smc::launch_attn_tc(a, scratch, dev.sms, s);
+  if (scratch) cudaFreeAsync(scratch, s);
+  return outcome(e);
 }
 
 int smc_attention_backward(const void* dout, const int64_t dout_stride[2], const void* q, const int64_t q_stride[2],

@@ -1,0 +1,513 @@
+// Attention within each item on the tensor cores (bf16 / fp16, sm_100a).
+//
+//   S = scale Q K^T,  P = exp2(S log2e - top),  O = sum P V / sum P
+//
+// One CTA holds two tiles of 128 packed rows (row = query * G + head of the
+// group, so the heads that share keys share the tile) of one key/value head
+// against a run of the item's keys, 128 at a time:
+//   warp 9     TMA: both Q tiles once, then K and V tiles into a ring;
+//   warp 8     tcgen05.mma: S = Q K^T (both from shared memory), then
+//              O += P V with P in TMEM and V read MN-major as it lies;
+//   warps 0-3, 4-7  the softmax of the first and second tile: one thread per
+//              row, 128 scores in registers, running maximum and sum in fp32,
+//              P rounded to the input type into the columns its scores came
+//              from.
+// While one tile's scores are exponentiated, the tensor cores work on the
+// other tile.  The accumulator is rescaled in TMEM only when a row's maximum
+// has grown by more than 2^8 (P stays below 256, far inside fp16's range);
+// the sums use the unrounded P.  Keys behind the item's end are masked, and V
+// rows there are zeroed in shared memory, since P = 0 does not undo a NaN.
+// With few queries over many keys the keys are split between CTAs; each writes
+// its unnormalised fp32 O, maximum and sum, and k_attn_join adds them up in
+// order.
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "kernels.h"
+#include "tcgen05_attn.cuh"
+#include "tokens.cuh"
+
+namespace smc {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kRows = 128;       // rows of a tile, keys of a step
+constexpr int kFwdThreads = 320;
+constexpr uint32_t kPanel = kRows * 128;  // 128 rows of 64 16-bit channels
+
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+struct FwdParams {
+  const int32_t *q_off, *k_off;
+  int64_t n, m;
+  int items, heads, kv_heads, dim, group, qpt;  // qpt: queries of a tile
+  int chunk;                                     // keys of a split (0: no split)
+  int slot_rows;                                 // rows of a split's partial results
+  float c;                                       // scale * log2 e
+  bool causal;
+  void* out;
+  float* lse;
+  float *part_o, *part_ml;  // [units, kv_heads, slot_rows, dim] and [.., 2]
+  uint32_t* err;
+  uint64_t wait_ns;
+};
+
+__device__ __forceinline__ int32_t keys_seen(const Unit& u, int64_t qi, bool causal) {
+  if (!causal) return u.k.count;
+  const int64_t s = qi + u.k.count - u.q.count + 1;
+  return s < 0 ? 0 : (s > u.k.count ? u.k.count : static_cast<int32_t>(s));
+}
+
+template <int DP> struct FwdLayout {
+  static constexpr uint32_t kTileBytes = DP / 64 * kPanel;
+  static constexpr int kSlots = DP == 64 ? 8 : 4;
+  static constexpr uint32_t kQ = 0, kKv = 2 * kTileBytes, kBar = kKv + kSlots * kTileBytes;
+  // barriers: q, kv full[kSlots], kv empty[kSlots], s full[2], p ready[2], o full[2], tail
+  static constexpr uint32_t kMisc = kBar + 8 * (2 * kSlots + 8), kTotal = kMisc + 32 + 1024;
+};
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    k_attn_fwd_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap, const FwdParams p) {
+  using L = FwdLayout<DP>;
+  constexpr int kSlots = L::kSlots, kPanels = DP / 64;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Unit s_unit;
+  const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  volatile uint32_t* s_misc = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);  // [0] tmem, [1] abort
+  const uint32_t bar_q = sbase + L::kBar, bar_full = bar_q + 8, bar_empty = bar_full + 8 * kSlots;
+  const uint32_t bar_s = bar_empty + 8 * kSlots, bar_p = bar_s + 16, bar_o = bar_p + 16, bar_tail = bar_o + 16;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  find_unit<kFwdThreads>(p.q_off, p.k_off, p.items, p.n, p.m, 2 * p.qpt, p.chunk, false, blockIdx.x, &s_unit, p.err);
+  if (s_unit.item < 0) return;
+  const Unit u = s_unit;
+  const int hk = blockIdx.y;
+  const int32_t q0 = u.tile * 2 * p.qpt;
+  const int32_t left = u.q.count - q0;
+  const int32_t k_lo = u.split * p.chunk;
+  const int32_t k_hi = u.splits > 1 && u.k.count - k_lo > p.chunk ? k_lo + p.chunk : u.k.count;
+  int queries[2], steps[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int32_t rest = left - t * p.qpt;
+    queries[t] = rest < 0 ? 0 : (rest < p.qpt ? rest : p.qpt);
+    const int32_t seen = queries[t] > 0 ? keys_seen(u, q0 + t * p.qpt + queries[t] - 1, p.causal) : 0;
+    const int32_t hi = seen < k_hi ? seen : k_hi;
+    steps[t] = hi > k_lo ? (hi - k_lo + kRows - 1) / kRows : 0;
+  }
+  const int nsteps = steps[0] > steps[1] ? steps[0] : steps[1];
+
+  if (tid == 0) {
+    prefetch_tmap(&qmap);
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
+    mbar_init(bar_q, 1);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar_s + 8 * t, 1);
+      mbar_init(bar_p + 8 * t, 4);
+      mbar_init(bar_o + 8 * t, 1);
+    }
+    mbar_init(bar_tail, 1);
+    s_misc[1] = 0;
+    fence_mbarrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(const_cast<uint32_t*>(&s_misc[0])), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_misc[0];
+
+  if (warp == 9) {
+    // ------------------------------------------------------------- TMA loads
+    // 2 * nsteps tiles in the order they are used: K0 V0 K1 V1 ...
+    if (nsteps > 0) {
+      if (elect_one()) {
+        const int tiles = queries[1] > 0 ? 2 : 1;
+        mbar_arrive_expect_tx(bar_q, static_cast<uint32_t>(tiles * kPanels * p.group * p.qpt) * 128u);
+        for (int t = 0; t < tiles; ++t)
+          for (int c = 0; c < kPanels; ++c)
+            tma_load_3d(sbase + L::kQ + t * L::kTileBytes + c * kPanel, &qmap, bar_q, c * 64, hk * p.group,
+                        u.q.begin + q0 + t * p.qpt);
+      }
+      __syncwarp();
+      for (int i = 0; i < 2 * nsteps; ++i) {
+        const int slot = i % kSlots;
+        int ok = 1;
+        if (lane == 0)
+          ok = mbar_wait_bounded(bar_empty + 8 * slot, ((i / kSlots) & 1) ^ 1, p.err, p.wait_ns) && !s_misc[1];
+        if (!__shfl_sync(0xffffffffu, ok, 0)) {
+          if (lane == 0) s_misc[1] = 1;
+          break;
+        }
+        const int32_t key = k_lo + (i >> 1) * kRows;
+        const int rows = u.k.count - key;  // V rows behind the item's end are zeroed below
+        const bool tail = (i & 1) && rows < kRows;
+        const uint32_t dst = sbase + L::kKv + slot * L::kTileBytes, bar = tail ? bar_tail : bar_full + 8 * slot;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar, L::kTileBytes);
+          for (int c = 0; c < kPanels; ++c)
+            tma_load_3d(dst + c * kPanel, (i & 1) ? &vmap : &kmap, bar, c * 64, hk, u.k.begin + key);
+        }
+        __syncwarp();
+        if (tail) {  // once, at the last step
+          ok = mbar_wait_bounded(bar_tail, 0, p.err, p.wait_ns);
+          if (!__all_sync(0xffffffffu, ok)) {
+            if (lane == 0) s_misc[1] = 1;
+            break;
+          }
+          uint4* base = reinterpret_cast<uint4*>(smem + L::kKv + slot * L::kTileBytes);
+          for (int c = 0; c < kPanels; ++c)
+            for (int j = rows * 8 + lane; j < kRows * 8; j += 32) base[c * (kPanel / 16) + j] = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_full + 8 * slot);
+        }
+      }
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------- MMA issue
+    const uint32_t ab = kBf16 ? 1u : 0u;
+    const int ks = (p.dim + 15) / 16;
+    const uint32_t idesc_s = idesc_f16(ab, kRows), idesc_o = idesc_f16(ab, static_cast<uint32_t>(ks * 16)) | kIdescBMn;
+    bool ok = nsteps > 0;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      const bool w = mbar_wait_bounded(bar, parity, p.err, p.wait_ns);
+      if (!__all_sync(0xffffffffu, w && !s_misc[1])) {
+        if (lane == 0) s_misc[1] = 1;
+        ok = false;
+      }
+      tc_fence_after();
+    };
+    auto scores = [&](int t, int slot) {
+      const uint32_t a = sbase + L::kQ + t * L::kTileBytes, b = sbase + L::kKv + slot * L::kTileBytes;
+      for (int k = 0; k < ks; ++k) {
+        const uint64_t off = 2 * (k & 3);
+        umma_f16_elect(tmem + t * kRows, kmajor_desc(a + (k >> 2) * kPanel, 128) + off,
+                       kmajor_desc(b + (k >> 2) * kPanel, 128) + off, idesc_s, k > 0);
+      }
+      umma_commit_elect(bar_s + 8 * t);
+    };
+    if (ok) wait(bar_q, 0);
+    if (ok) wait(bar_full, 0);
+    if (ok) {
+      for (int t = 0; t < 2; ++t)
+        if (steps[t] > 0) scores(t, 0);
+      if (kSlots < 2 * nsteps) umma_commit_elect(bar_empty);
+    }
+    for (int j = 0; j < nsteps && ok; ++j) {
+      const int iv = 2 * j + 1, ik = 2 * j + 2, sv = iv % kSlots, sk = ik % kSlots;
+      bool next = false;  // K of the next step awaited
+      wait(bar_full + 8 * sv, (iv / kSlots) & 1);
+      for (int t = 0; t < 2 && ok; ++t) {
+        if (j >= steps[t]) continue;
+        wait(bar_p + 8 * t, j & 1);
+        if (!ok) break;
+        const uint64_t b = mnmajor_desc(sbase + L::kKv + sv * L::kTileBytes, kPanel);
+#pragma unroll
+        for (int k = 0; k < kRows / 16; ++k)
+          umma_f16_ts_elect(tmem + 2 * kRows + t * DP, tmem + t * kRows + k * 8, b + 128 * k, idesc_o, j > 0 || k > 0);
+        if (j + 1 < steps[t]) {
+          if (!next) wait(bar_full + 8 * sk, (ik / kSlots) & 1);
+          next = true;
+          if (ok) scores(t, sk);
+        } else {
+          umma_commit_elect(bar_o + 8 * t);
+        }
+      }
+      // only for slots that are loaded again: no arrival is left under way at the end
+      if (iv + kSlots < 2 * nsteps) umma_commit_elect(bar_empty + 8 * sv);
+      if (next && ik + kSlots < 2 * nsteps) umma_commit_elect(bar_empty + 8 * sk);
+    }
+  } else {
+    // --------------------------------------------------------------- softmax
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + t * kRows, to = tmem + lanes + 2 * kRows + t * DP;
+    const int32_t qi = r / p.group;  // query in the tile
+    const bool row = qi < queries[t];
+    int32_t lim = row ? keys_seen(u, q0 + t * p.qpt + qi, p.causal) : 0;  // keys [0, lim) are seen
+    lim = lim < k_hi ? lim : k_hi;
+    float top = -INFINITY, sum = 0.f;  // top: the rounded product with c the sums refer to
+    bool ok = true;
+    for (int j = 0; j < steps[t]; ++j) {
+      ok = mbar_wait_bounded(bar_s + 8 * t, j & 1, p.err, p.wait_ns);
+      if (!__all_sync(0xffffffffu, ok && !s_misc[1])) {
+        s_misc[1] = 1;
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float x[kRows];
+      tmem_ld(ts, x);
+      const int32_t seen = lim - (k_lo + j * kRows);
+      if (__any_sync(0xffffffffu, seen < kRows)) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+          if (i >= seen) x[i] = -INFINITY;
+      }
+      float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
+#pragma unroll
+      for (int i = 4; i < kRows; i += 4) {
+        m0 = fmaxf(m0, x[i]);
+        m1 = fmaxf(m1, x[i + 1]);
+        m2 = fmaxf(m2, x[i + 2]);
+        m3 = fmaxf(m3, x[i + 3]);
+      }
+      const float m = __fmul_rn(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), p.c);
+      const bool grown = m > top + 8.f || (top == -INFINITY && m > -INFINITY);
+      if (__any_sync(0xffffffffu, grown)) {
+        const float keep = grown ? exp2_fast(top - m) : 1.f;
+        if (grown) {
+          sum *= keep;
+          top = m;
+        }
+        if (j > 0) {  // this tile's products so far are complete: its S came after them
+          for (int c0 = 0; c0 < DP; c0 += 32) {
+            float o[32];
+            uint32_t b[32];
+            tmem_ld(to + c0, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) b[i] = __float_as_uint(o[i] * keep);
+            tmem_st(to + c0, b);
+          }
+        }
+      }
+      const float base = top == -INFINITY ? 0.f : top;
+      float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const int e = h * 64 + 2 * i;
+          const float a0 = exp2_fast(fmaf(x[e], p.c, -base)), a1 = exp2_fast(fmaf(x[e + 1], p.c, -base));
+          const float a2 = exp2_fast(fmaf(x[e + 2], p.c, -base)), a3 = exp2_fast(fmaf(x[e + 3], p.c, -base));
+          s0 += a0;
+          s1 += a1;
+          s2 += a2;
+          s3 += a3;
+          w[i] = pack2<T>(a0, a1);
+          w[i + 1] = pack2<T>(a2, a3);
+        }
+        tmem_st(ts + h * 32, w);
+      }
+      sum += (s0 + s1) + (s2 + s3);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_p + 8 * t);
+    }
+    // --------------------------------------------------------------- results
+    if (ok && steps[t] > 0) {
+      ok = mbar_wait_bounded(bar_o + 8 * t, 0, p.err, p.wait_ns);
+      ok = __all_sync(0xffffffffu, ok && !s_misc[1]);
+      tc_fence_after();
+    }
+    if (ok) {
+      const int64_t at = static_cast<int64_t>(u.q.begin + q0 + t * p.qpt + qi) * p.heads + hk * p.group + r % p.group;
+      const bool split = p.part_o != nullptr;
+      const int64_t slot =
+          (static_cast<int64_t>(blockIdx.x) * p.kv_heads + hk) * p.slot_rows + t * p.qpt * p.group + r;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+      for (int c0 = 0; c0 < DP; c0 += 32) {
+        if (c0 >= p.dim) break;
+        float o[32];
+        if (steps[t] > 0) {
+          tmem_ld(to + c0, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        }
+        if (!row) continue;
+        if (split) {
+          float4* d = reinterpret_cast<float4*>(p.part_o + slot * p.dim + c0);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c0 + 4 * i < p.dim) d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else {
+          uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * p.dim + c0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c0 + 8 * i < p.dim)
+              d[i] = make_uint4(pack2<T>(o[8 * i] * inv, o[8 * i + 1] * inv), pack2<T>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                pack2<T>(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack2<T>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+        }
+      }
+      if (row) {
+        if (split) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(top, sum);
+        else if (p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// Joins the splits of one tile, in order: O = sum 2^(top_s - top) O_s / sum ...
+template <typename T>
+__global__ void __launch_bounds__(256) k_attn_join(const FwdParams p) {
+  __shared__ Unit s_unit;
+  find_unit<256>(p.q_off, p.k_off, p.items, p.n, p.m, 2 * p.qpt, p.chunk, false, blockIdx.x, &s_unit, p.err);
+  const Unit u = s_unit;
+  if (u.item < 0 || u.split != 0) return;
+  const int hk = blockIdx.y, lane = threadIdx.x & 31;
+  const int32_t q0 = u.tile * 2 * p.qpt;
+  const int32_t queries = u.q.count - q0 < 2 * p.qpt ? u.q.count - q0 : 2 * p.qpt;
+  for (int r = threadIdx.x >> 5; r < queries * p.group; r += 8) {
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * p.kv_heads + hk) * p.slot_rows + r;
+    const int64_t step = static_cast<int64_t>(p.kv_heads) * p.slot_rows;
+    float top = -INFINITY;
+    for (int s = lane; s < u.splits; s += 32) top = fmaxf(top, p.part_ml[2 * (first + s * step)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    const bool mine = 4 * lane < p.dim;
+    for (int s = 0; s < u.splits; ++s) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (first + s * step));
+      if (ml.x == -INFINITY) continue;  // this split's keys are hidden from the row
+      const float w = exp2f(ml.x - top);
+      sum += w * ml.y;
+      if (mine) {
+        const float4 v = *reinterpret_cast<const float4*>(p.part_o + (first + s * step) * p.dim + 4 * lane);
+        o[0] += w * v.x, o[1] += w * v.y, o[2] += w * v.z, o[3] += w * v.w;
+      }
+    }
+    const int64_t at = static_cast<int64_t>(u.q.begin + q0 + r / p.group) * p.heads + hk * p.group + r % p.group;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (mine)
+      *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at * p.dim + 4 * lane) =
+          make_uint2(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv));
+    if (lane == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  }
+}
+
+// A [rows, heads, dim] tensor as boxes of 64 channels x `bh` heads x `br` rows.
+bool make_map(CUtensorMap* map, const void* p, int dtype, int64_t rows, int heads, int dim, const int64_t st[2], int bh,
+              int br) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(st[1]) * 2, static_cast<cuuint64_t>(st[0]) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(bh), static_cast<cuuint32_t>(br)};
+  const cuuint32_t es[3] = {1, 1, 1};
+  const CUtensorMapDataType dt = dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return encode_fn()(map, dt, 3, const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool map_fits(const void* p, const int64_t st[2]) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && st[0] > 0 && st[1] > 0 && st[0] % 8 == 0 && st[1] % 8 == 0 &&
+         st[0] < (int64_t{1} << 38) && st[1] < (int64_t{1} << 38);
+}
+
+struct SplitPlan {
+  int64_t units;  // blocks along x
+  int chunk, slot_rows;
+};
+
+// Splits the keys when the tiles alone leave more than half of the SMs idle:
+// into runs of about (keys x tiles) / (2 x SMs), at least 256 keys.
+SplitPlan split_plan(const AttnArgs& a, int sms) {
+  const int group = a.heads / a.kv_heads, per = 2 * (kRows / group);
+  const int64_t tiles = a.n / per + a.items;  // upper bound
+  SplitPlan s = {tiles, 0, 0};
+  if (2 * tiles * a.kv_heads > sms) return s;
+  const int64_t most = a.n / per + 1;  // tiles of one item, upper bound
+  int64_t chunk = a.m * most * a.kv_heads / (2 * sms);
+  chunk = (chunk < 256 ? 256 : chunk + kRows - 1) / kRows * kRows;
+  if (a.m <= chunk) return s;  // no item is longer than one run
+  s.chunk = static_cast<int>(chunk);
+  s.units = tiles + most * (a.m / chunk);
+  const int64_t rows = a.n * group;
+  s.slot_rows = static_cast<int>(rows < per * group ? rows : per * group);
+  return s;
+}
+
+template <typename T, int DP>
+cudaError_t launch_fwd(const AttnArgs& a, const FwdParams& p, const SplitPlan& s, const CUtensorMap& qm,
+                       const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+  auto kern = k_attn_fwd_tc<T, DP>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(FwdLayout<DP>::kTotal));
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(s.units), a.kv_heads);
+  kern<<<grid, kFwdThreads, FwdLayout<DP>::kTotal, st>>>(qm, km, vm, p);
+  if (s.chunk) k_attn_join<T><<<grid, 256, 0, st>>>(p);
+  count_launches(s.chunk ? 2 : 1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool attn_tc_supported(const AttnArgs& a) {
+  return a.dtype != kF32 && a.dim % 8 == 0 && a.m > 0 && map_fits(a.q, a.q_stride) && map_fits(a.k, a.k_stride) &&
+         map_fits(a.v, a.v_stride) && (reinterpret_cast<uintptr_t>(a.out_w) & 15u) == 0 && encode_fn() != nullptr;
+}
+
+int64_t attn_tc_scratch(const AttnArgs& a, int sms) {
+  const SplitPlan s = split_plan(a, sms);
+  return s.chunk ? s.units * a.kv_heads * s.slot_rows * (a.dim + 2) * static_cast<int64_t>(sizeof(float)) : 0;
+}
+
+cudaError_t launch_attn_tc(const AttnArgs& a, void* scratch, int sms, cudaStream_t st) {
+  const int group = a.heads / a.kv_heads, qpt = kRows / group;
+  const SplitPlan s = split_plan(a, sms);
+  CUtensorMap qm, km, vm;
+  if (!make_map(&qm, a.q, a.dtype, a.n, a.heads, a.dim, a.q_stride, group, qpt) ||
+      !make_map(&km, a.k, a.dtype, a.m, a.kv_heads, a.dim, a.k_stride, 1, kRows) ||
+      !make_map(&vm, a.v, a.dtype, a.m, a.kv_heads, a.dim, a.v_stride, 1, kRows))
+    return cudaErrorInvalidValue;
+  FwdParams p = {};
+  p.q_off = a.q_off;
+  p.k_off = a.k_off;
+  p.n = a.n;
+  p.m = a.m;
+  p.items = a.items;
+  p.heads = a.heads;
+  p.kv_heads = a.kv_heads;
+  p.dim = a.dim;
+  p.group = group;
+  p.qpt = qpt;
+  p.chunk = s.chunk;
+  p.slot_rows = s.slot_rows;
+  p.c = a.scale * kLog2e;
+  p.causal = a.causal;
+  p.out = a.out_w;
+  p.lse = a.lse_w;
+  if (s.chunk) {
+    p.part_o = static_cast<float*>(scratch);
+    p.part_ml = p.part_o + s.units * a.kv_heads * s.slot_rows * a.dim;
+  }
+  p.err = a.err;
+  // never below 100 ms, so that no CTA leaves with its loads in flight
+  p.wait_ns = scan_wait_limit_ns() > 100000000ull ? scan_wait_limit_ns() : 100000000ull;
+  if (a.dtype == kBF16)
+    return a.dim <= 64 ? launch_fwd<__nv_bfloat16, 64>(a, p, s, qm, km, vm, st)
+                       : launch_fwd<__nv_bfloat16, 128>(a, p, s, qm, km, vm, st);
+  return a.dim <= 64 ? launch_fwd<__half, 64>(a, p, s, qm, km, vm, st) : launch_fwd<__half, 128>(a, p, s, qm, km, vm, st);
+}
+
+}  // namespace smc

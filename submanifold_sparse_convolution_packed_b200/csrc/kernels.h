@@ -219,6 +219,12 @@ struct AttnArgs {
 // FMA kernels: every dtype, dim <= 128, heads / kv_heads <= 64.
 cudaError_t launch_attn_simt(const AttnArgs& a, bool backward, cudaStream_t s);
 
+// tcgen05 kernels (attn_tc.cu): bf16 / fp16, dim a multiple of 8, 16-byte
+// aligned tensors and strides; scratch of attn_tc_scratch bytes.
+bool attn_tc_supported(const AttnArgs& a);
+int64_t attn_tc_scratch(const AttnArgs& a, int sms);
+cudaError_t launch_attn_tc(const AttnArgs& a, void* scratch, int sms, cudaStream_t s);
+
 // dtype codes as in smc.h
 enum DType : int { kF32 = 0, kBF16 = 1, kF16 = 2 };
 

@@ -85,27 +85,28 @@ template <int kThreads>
 __device__ __forceinline__ void find_unit(const int32_t* q_off, const int32_t* k_off, int items, int64_t n, int64_t m,
                                           int per_tile, int chunk, bool tile_k, int64_t u, Unit* out, uint32_t* err) {
   static_assert(kThreads % 32 == 0, "whole warps");
-  __shared__ int32_t s_warp[kThreads / 32];
+  __shared__ int64_t s_warp[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (items + kThreads - 1) / kThreads;
   const int i0 = tid * run < items ? tid * run : items, i1 = i0 + run < items ? i0 + run : items;
   if (tid == 0) out->item = -1;
-  int32_t mine = 0, sp;
+  int64_t mine = 0;
+  int32_t sp;
   bool bad = false;
   for (int i = i0; i < i1; ++i)
     mine += units_of(item_span(q_off, i, n, &bad), item_span(k_off, i, m, &bad), per_tile, chunk, tile_k, &sp);
-  int32_t incl = mine;
+  int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
   if (lane == 31) s_warp[warp] = incl;
   __syncthreads();
-  int32_t before = incl - mine;
+  int64_t before = incl - mine;
   for (int w = 0; w < warp; ++w) before += s_warp[w];
   if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(err, kErrRange);
-  if (u >= before && u < static_cast<int64_t>(before) + mine) {
+  if (u >= before && u < before + mine) {
     int64_t at = before;
     for (int i = i0; i < i1; ++i) {
       const Span q = item_span(q_off, i, n, &bad), k = item_span(k_off, i, m, &bad);
