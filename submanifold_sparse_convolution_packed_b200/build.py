@@ -16,7 +16,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsmc.so")
 SOURCES = ["api.cu", "map_build.cu", "conv_simt.cu", "conv_tc.cu", "conv_offsets.cu", "norm.cu", "resample.cu",
-           "noalloc.cu", "layer_norm.cu", "rotary.cu", "attn_simt.cu", "attn_tc.cu", "api_tokens.cu"]
+           "noalloc.cu", "layer_norm.cu", "rotary.cu", "attn_simt.cu", "attn_tc.cu", "attn_bwd_tc.cu",
+           "api_tokens.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -20,32 +20,17 @@
 // With few queries over many keys the keys are split between CTAs; each writes
 // its unnormalised fp32 O, maximum and sum, and k_attn_join adds them up in
 // order.
-#include <cuda.h>
-
 #include <type_traits>
 
-#include "kernels.h"
-#include "tcgen05_attn.cuh"
-#include "tokens.cuh"
+#include "attn_tc.cuh"
 
 namespace smc {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kRows = 128;       // rows of a tile, keys of a step
-constexpr int kFwdThreads = 320;
-constexpr uint32_t kPanel = kRows * 128;  // 128 rows of 64 16-bit channels
+using namespace attn;
 
-template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
-template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
+constexpr int kFwdThreads = 320;
 
 struct FwdParams {
   const int32_t *q_off, *k_off;
@@ -61,12 +46,6 @@ struct FwdParams {
   uint32_t* err;
   uint64_t wait_ns;
 };
-
-__device__ __forceinline__ int32_t keys_seen(const Unit& u, int64_t qi, bool causal) {
-  if (!causal) return u.k.count;
-  const int64_t s = qi + u.k.count - u.q.count + 1;
-  return s < 0 ? 0 : (s > u.k.count ? u.k.count : static_cast<int32_t>(s));
-}
 
 template <int DP> struct FwdLayout {
   static constexpr uint32_t kTileBytes = DP / 64 * kPanel;
@@ -92,7 +71,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const uint32_t bar_s = bar_empty + 8 * kSlots, bar_p = bar_s + 16, bar_o = bar_p + 16, bar_tail = bar_o + 16;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  find_unit<kFwdThreads>(p.q_off, p.k_off, p.items, p.n, p.m, 2 * p.qpt, p.chunk, false, blockIdx.x, &s_unit, p.err);
+  // causal: the tiles with the most keys come last in an item and start first
+  const int64_t ux = p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+  find_unit<kFwdThreads>(p.q_off, p.k_off, p.items, p.n, p.m, 2 * p.qpt, p.chunk, false, ux, &s_unit, p.err);
   if (s_unit.item < 0) return;
   const Unit u = s_unit;
   const int hk = blockIdx.y;
@@ -329,7 +310,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const int64_t at = static_cast<int64_t>(u.q.begin + q0 + t * p.qpt + qi) * p.heads + hk * p.group + r % p.group;
       const bool split = p.part_o != nullptr;
       const int64_t slot =
-          (static_cast<int64_t>(blockIdx.x) * p.kv_heads + hk) * p.slot_rows + t * p.qpt * p.group + r;
+          (ux * p.kv_heads + hk) * p.slot_rows + t * p.qpt * p.group + r;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll 1
       for (int c0 = 0; c0 < DP; c0 += 32) {
@@ -403,24 +384,6 @@ __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p) {
           make_uint2(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv));
     if (lane == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
   }
-}
-
-// A [rows, heads, dim] tensor as boxes of 64 channels x `bh` heads x `br` rows.
-bool make_map(CUtensorMap* map, const void* p, int dtype, int64_t rows, int heads, int dim, const int64_t st[2], int bh,
-              int br) {
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(st[1]) * 2, static_cast<cuuint64_t>(st[0]) * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(bh), static_cast<cuuint32_t>(br)};
-  const cuuint32_t es[3] = {1, 1, 1};
-  const CUtensorMapDataType dt = dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  return encode_fn()(map, dt, 3, const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool map_fits(const void* p, const int64_t st[2]) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && st[0] > 0 && st[1] > 0 && st[0] % 8 == 0 && st[1] % 8 == 0 &&
-         st[0] < (int64_t{1} << 38) && st[1] < (int64_t{1} << 38);
 }
 
 struct SplitPlan {

@@ -1,0 +1,56 @@
+// Shared by the tensor-core attention kernels: packing of fp32 pairs, the
+// causal limit, the TMA maps of [rows, heads, dim] tensors.
+#pragma once
+
+#include <cuda.h>
+
+#include <cstdint>
+
+#include "kernels.h"
+#include "tcgen05_attn.cuh"
+#include "tokens.cuh"
+
+namespace smc {
+namespace attn {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kRows = 128;                // rows of a resident tile
+constexpr uint32_t kPanel = kRows * 128;  // 128 rows of 64 16-bit channels
+
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Keys that query `qi` of an item sees: the first ones, this many.
+__device__ __forceinline__ int32_t keys_seen(const Unit& u, int64_t qi, bool causal) {
+  if (!causal) return u.k.count;
+  const int64_t s = qi + u.k.count - u.q.count + 1;
+  return s < 0 ? 0 : (s > u.k.count ? u.k.count : static_cast<int32_t>(s));
+}
+
+// A [rows, heads, dim] tensor as boxes of 64 channels x `bh` heads x `br` rows.
+inline bool make_map(CUtensorMap* map, const void* p, int dtype, int64_t rows, int heads, int dim, const int64_t st[2], int bh,
+              int br) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(st[1]) * 2, static_cast<cuuint64_t>(st[0]) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(bh), static_cast<cuuint32_t>(br)};
+  const cuuint32_t es[3] = {1, 1, 1};
+  const CUtensorMapDataType dt = dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return encode_fn()(map, dt, 3, const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+inline bool map_fits(const void* p, const int64_t st[2]) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && st[0] > 0 && st[1] > 0 && st[0] % 8 == 0 && st[1] % 8 == 0 &&
+         st[0] < (int64_t{1} << 38) && st[1] < (int64_t{1} << 38);
+}
+
+}  // namespace attn
+}  // namespace smc
