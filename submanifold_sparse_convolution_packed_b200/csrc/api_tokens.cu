@@ -330,16 +330,17 @@ int smc_attention_backward(const void* dout, const int64_t dout_stride[2], const
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  // scratch: delta [n, heads] and two words
+  // scratch: delta and the scaled lse, [n, heads] each, and two words
   void* scratch = nullptr;
   const size_t count = static_cast<size_t>(n) * heads;
-  if (n > 0 && smc::scratch_alloc(&scratch, (count + 2) * sizeof(float), dev.id, s) != cudaSuccess) {
+  if (n > 0 && smc::scratch_alloc(&scratch, (2 * count + 2) * sizeof(float), dev.id, s) != cudaSuccess) {
     cudaGetLastError();
     return SMC_E_OOM;
   }
   a.delta = static_cast<float*>(scratch);
   const cudaError_t e = smc::attn_bwd_tc_supported(a)
-                            ? smc::launch_attn_bwd_tc(a, reinterpret_cast<uint32_t*>(a.delta + count), dev.sms, s)
+                            ? smc::launch_attn_bwd_tc(a, a.delta + count, reinterpret_cast<uint32_t*>(a.delta + 2 * count),
+                                                      dev.sms, s)
                             : smc::launch_attn_simt(a, true, s);
   if (scratch) cudaFreeAsync(scratch, s);
   return outcome(e);

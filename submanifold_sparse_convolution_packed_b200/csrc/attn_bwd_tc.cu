@@ -13,11 +13,12 @@
 // transposed (keys are the rows), so that P^T and dS^T, written to TMEM by the
 // threads that hold their rows, are the A operands of the products as they
 // lie; Q, dO, K are read a second time from the same shared memory, MN-major.
-//   warp 9     TMA: the resident tiles once, then the passing ones, with the
-//              lse and delta of their rows (dK / dV);
-//   warp 8     tcgen05.mma: S and dP of step j + 1 are issued before the
-//              products of step j, into the other of two TMEM buffers;
-//   warps 0-3, 4-7  P and dS of even and odd steps, one thread per row.
+//   warp 17    TMA: the resident tiles once, then the passing ones, with the
+//              lse and delta of their rows (dK / dV, cp.async);
+//   warp 16    tcgen05.mma: S and dP of step j + 1 are issued before
+//              the products of step j, into the other of two TMEM buffers;
+//   warps 0-15 P and dS, one thread per row and half of the step's columns:
+//              eight warps each for even and odd steps.
 // fp16: P carries a factor 2^14 and dS a power of two taken from the largest
 // norms of dO and V rows (|dP|, |delta| <= |dO| |V|), undone on the fp32
 // accumulators, so that the P of a long context do not fall below fp16's
@@ -32,7 +33,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 576;
 constexpr int kStep = 64;                       // passing rows of a step
 constexpr uint32_t kStepPanel = kStep * 128;
 
@@ -43,7 +44,7 @@ struct BwdParams {
   int qpt, qps;  // queries of a resident tile, of a step
   float scale;
   bool causal;
-  const float *lse, *delta;
+  const float *lse, *delta;  // as k_attn_delta_tc leaves them: lse log2e (+inf for a row that saw no key), delta
   const uint32_t* norms;  // fp16: bits of max |dO|^2, max |V|^2
   void *d1, *d2;          // dQ, -- or dK, dV
   int64_t s1[2], s2[2];
@@ -83,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Unit s_unit;
   const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - raw);
-  volatile uint32_t* s_misc = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);  // [0] tmem, [1] abort
+  volatile uint32_t* s_misc = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);  // [0] tmem
   const uint32_t bar_a = sbase + L::kBar, bar_full = bar_a + 8, bar_empty = bar_full + 8 * kSlots;
   const uint32_t bar_s = bar_empty + 8 * kSlots, bar_p = bar_s + 16, bar_o = bar_p + 16, bar_tail = bar_o + 8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -118,16 +119,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&b2map);
     mbar_init(bar_a, 1);
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(bar_full + 8 * s, kDQ ? 1 : 2);
+      mbar_init(bar_full + 8 * s, kDQ ? 1 : 33);
       mbar_init(bar_empty + 8 * s, 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar_s + 8 * t, 1);
-      mbar_init(bar_p + 8 * t, 4);
+      mbar_init(bar_p + 8 * t, 8);
     }
     mbar_init(bar_o, 1);
     mbar_init(bar_tail, 1);
-    s_misc[1] = 0;
     fence_mbarrier_init();
   }
   const int rows_step = kDQ ? kStep : p.qps * p.group;  // rows of a step that the TMA writes
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   fence_proxy_async_smem();
-  if (warp == 8) {
+  if (warp == 16) {
     tmem_alloc(smem_u32(const_cast<uint32_t*>(&s_misc[0])), 512);
     tmem_relinquish();
   }
@@ -147,11 +147,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_misc[0];
 
-  if (warp == 9) {
+  // Every wait is bounded; a role that gives up leaves its loop, and the others
+  // then run out of their own waits.
+  if (warp == 17) {
     // ------------------------------------------------------------- TMA loads
     if (nsteps > 0) {
-      const float f = kDQ ? 1.f : ds_factor(p.norms) * exp2f(-kShift);
-      if (elect_one()) {
+      if (lane == 0) {
         const uint32_t rows = kDQ ? p.group * p.qpt : kRows;
         mbar_arrive_expect_tx(bar_a, 2 * kPanels * rows * 128u);
         const int head = kDQ ? hk * p.group : hk, row = (kDQ ? u.q.begin : u.k.begin) + r0;
@@ -161,65 +162,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      // lse and delta of the step's rows, fetched a step ahead
-      float l[2], e[2];
-      auto fetch = [&](int j) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = lane + 32 * h, qi = b_lo + j * per_step + r / p.group;
-          l[h] = INFINITY;  // exp2(s - inf) = 0: rows that are not there, or saw no key
-          e[h] = 0.f;
-          if (r < rows_step && qi < b_hi) {
-            const int64_t at = static_cast<int64_t>(u.q.begin + qi) * p.heads + hk * p.group + r % p.group;
-            const float v = __ldg(p.lse + at);
-            if (v != -INFINITY) {
-              l[h] = v * kLog2e - kShift;
-              e[h] = p.delta[at] * f;
-            }
-          }
-        }
-      };
-      if (!kDQ) fetch(0);
+      int slot = 0;
+      uint32_t parity = 1;
+      const int head = kDQ ? hk : hk * p.group, base_row = kDQ ? u.k.begin : u.q.begin;
       for (int j = 0; j < nsteps; ++j) {
-        const int slot = j % kSlots;
-        int ok = 1;
-        if (lane == 0)
-          ok = mbar_wait_bounded(bar_empty + 8 * slot, ((j / kSlots) & 1) ^ 1, p.err, p.wait_ns) && !s_misc[1];
-        if (!__shfl_sync(0xffffffffu, ok, 0)) {
-          if (lane == 0) s_misc[1] = 1;
-          break;
-        }
+        if (!__all_sync(0xffffffffu, mbar_wait_short(bar_empty + 8 * slot, parity, p.err, p.wait_ns))) break;
         const int32_t b0 = b_lo + j * per_step;
         const int rows = (b_hi - b0 < per_step ? b_hi - b0 : per_step) * (kDQ ? 1 : p.group);
         // in the dQ launch b_hi may be the causal limit: rows behind it are the item's own, but not seen
         const bool tail = rows < rows_step;
         const uint32_t dst = sbase + L::kB + slot * 2 * L::kPass, bar = tail ? bar_tail : bar_full + 8 * slot;
-        if (elect_one()) {
+        if (lane == 0) {
           mbar_arrive_expect_tx(bar, 2 * kPanels * static_cast<uint32_t>(rows_step) * 128u);
-          const int head = kDQ ? hk : hk * p.group, row = (kDQ ? u.k.begin : u.q.begin) + b0;
           for (int c = 0; c < kPanels; ++c) {
-            tma_load_3d(dst + c * kStepPanel, &b1map, bar, c * 64, head, row);
-            tma_load_3d(dst + L::kPass + c * kStepPanel, &b2map, bar, c * 64, head, row);
+            tma_load_3d(dst + c * kStepPanel, &b1map, bar, c * 64, head, base_row + b0);
+            tma_load_3d(dst + L::kPass + c * kStepPanel, &b2map, bar, c * 64, head, base_row + b0);
           }
         }
-        __syncwarp();
-        if (!kDQ) {
-          float* vals = reinterpret_cast<float*>(smem + L::kRowVals) + slot * 2 * kStep;
+        if (!kDQ) {  // rows that are not there get 0: their S, dP and dO are 0 too, so they add nothing
+          const uint32_t vals = sbase + L::kRowVals + slot * 8 * kStep;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            vals[lane + 32 * h] = l[h];
-            vals[kStep + lane + 32 * h] = e[h];
+            const int r = lane + 32 * h;
+            const bool there = r < rows;
+            const int64_t at =
+                there ? static_cast<int64_t>(base_row + b0 + r / p.group) * p.heads + head + r % p.group : 0;
+            cp_async4(vals + 4 * r, p.lse + at, there);
+            cp_async4(vals + 4 * (kStep + r), p.delta + at, there);
           }
-          if (j + 1 < nsteps) fetch(j + 1);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_full + 8 * slot);
+          cp_async_arrive(bar_full + 8 * slot);
         }
         if (tail) {  // once, at the last step: rows that are not the item's may hold NaN
-          ok = mbar_wait_bounded(bar_tail, 0, p.err, p.wait_ns);
-          if (!__all_sync(0xffffffffu, ok)) {
-            if (lane == 0) s_misc[1] = 1;
-            break;
-          }
+          if (!__all_sync(0xffffffffu, mbar_wait_short(bar_tail, 0, p.err, p.wait_ns))) break;
           for (int c = 0; c < 2 * kPanels; ++c) {
             uint4* base = reinterpret_cast<uint4*>(smem + L::kB + slot * 2 * L::kPass + c * kStepPanel);
             for (int i = rows * 8 + lane; i < rows_step * 8; i += 32) base[i] = make_uint4(0, 0, 0, 0);
@@ -228,151 +202,174 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_full + 8 * slot);
         }
+        if (++slot == kSlots) {
+          slot = 0;
+          parity ^= 1;
+        }
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == 16) {
     // ------------------------------------------------------------- MMA issue
+    // The whole warp runs the loop; one elected lane issues each batch, with
+    // the descriptors advanced by additions only (computing them anew made
+    // each MMA cost about 120 clocks of this warp's time, and a step twice as
+    // long).
     const uint32_t ab = kBf16 ? 1u : 0u;
     const int ks = (p.dim + 15) / 16;
     const uint32_t idesc_s = idesc_f16(ab, kStep), idesc_o = idesc_f16(ab, static_cast<uint32_t>(ks * 16)) | kIdescBMn;
-    bool ok = nsteps > 0;
+    const uint64_t a1 = kmajor_desc(sbase + L::kA, 128);
+    const uint64_t b1 = kmajor_desc(sbase + L::kB, 128), n1 = mnmajor_desc(sbase + L::kB, kStepPanel);
+    constexpr uint64_t kSecondA = L::kResident >> 4, kSecond = L::kPass >> 4, kSlot = 2 * kSecond;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-      const bool w = mbar_wait_bounded(bar, parity, p.err, p.wait_ns);
-      if (!__all_sync(0xffffffffu, w && !s_misc[1])) {
-        if (lane == 0) s_misc[1] = 1;
-        ok = false;
-      }
+      const bool w = __all_sync(0xffffffffu, mbar_wait_short(bar, parity, p.err, p.wait_ns));
       tc_fence_after();
+      return w;
     };
-    auto scores = [&](int j) {  // S and dP of step j
-      const uint32_t b = sbase + L::kB + (j % kSlots) * 2 * L::kPass, d = tmem + (j & 1) * 2 * kStep;
+    auto scores = [&](uint32_t d, uint64_t b, uint32_t bar) {  // S and dP of a step
+      if (elect_one()) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-        for (int k = 0; k < ks; ++k) {
-          const uint64_t off = 2 * (k & 3);
-          umma_f16_elect(d + x * kStep, kmajor_desc(sbase + L::kA + x * L::kResident + (k >> 2) * kPanel, 128) + off,
-                         kmajor_desc(b + x * L::kPass + (k >> 2) * kStepPanel, 128) + off, idesc_s, k > 0);
-        }
-      umma_commit_elect(bar_s + 8 * (j & 1));
-    };
-    if (ok) wait(bar_a, 0);
-    if (ok) wait(bar_full, 0);
-    if (ok) scores(0);
-    for (int j = 0; j < nsteps && ok; ++j) {
-      const int slot = j % kSlots;
-      if (j + 1 < nsteps) {
-        wait(bar_full + 8 * ((j + 1) % kSlots), ((j + 1) / kSlots) & 1);
-        if (!ok) break;
-        scores(j + 1);
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k)
+            if (k < ks)
+              umma_f16(d + x * kStep, a1 + x * kSecondA + (k >> 2) * (kPanel >> 4) + 2 * (k & 3),
+                       b + x * kSecond + (k >> 2) * (kStepPanel >> 4) + 2 * (k & 3), idesc_s, k > 0);
+        umma_commit(bar);
       }
-      wait(bar_p + 8 * (j & 1), (j >> 1) & 1);
-      if (!ok) break;
-      const uint32_t b = sbase + L::kB + slot * 2 * L::kPass, d = tmem + (j & 1) * 2 * kStep;
-      if (!kDQ) {
+      __syncwarp();
+    };
+    bool ok = nsteps > 0 && wait(bar_a, 0) && wait(bar_full, 0);
+    if (ok) scores(tmem, b1, bar_s);
+    int slot = 0, nslot = 1;
+    uint32_t nparity = 0;
+    for (int j = 0; j < nsteps && ok; ++j) {
+      const uint32_t b = j & 1, d = tmem + b * 2 * kStep;
+      if (j + 1 < nsteps) {
+        if (!wait(bar_full + 8 * nslot, nparity)) break;
+        scores(tmem + (b ^ 1) * 2 * kStep, b1 + nslot * kSlot, bar_s + 8 * (b ^ 1));
+      }
+      if (!wait(bar_p + 8 * b, (j >> 1) & 1)) break;
+      const uint64_t at = n1 + slot * kSlot;
+      if (elect_one()) {
+        if (!kDQ) {
+#pragma unroll
+          for (int k = 0; k < kStep / 16; ++k)
+            umma_f16_ts(tmem + 4 * kStep + DP, d + 8 * k + 16 * (k >> 1), at + kSecond + 128 * k, idesc_o, j > 0 || k > 0);
+        }
 #pragma unroll
         for (int k = 0; k < kStep / 16; ++k)
-          umma_f16_ts_elect(tmem + 4 * kStep + DP, d + 8 * k, mnmajor_desc(b + L::kPass, kStepPanel) + 128 * k, idesc_o,
-                            j > 0 || k > 0);
+          umma_f16_ts(tmem + 4 * kStep, d + kStep + 8 * k + 16 * (k >> 1), at + 128 * k, idesc_o, j > 0 || k > 0);
+        if (j + kSlots < nsteps) umma_commit(bar_empty + 8 * slot);
+        if (j + 1 == nsteps) umma_commit(bar_o);
       }
-#pragma unroll
-      for (int k = 0; k < kStep / 16; ++k)
-        umma_f16_ts_elect(tmem + 4 * kStep, d + kStep + 8 * k, mnmajor_desc(b, kStepPanel) + 128 * k, idesc_o,
-                          j > 0 || k > 0);
-      if (j + kSlots < nsteps) umma_commit_elect(bar_empty + 8 * slot);
+      __syncwarp();
+      slot = nslot;
+      if (++nslot == kSlots) {
+        nslot = 0;
+        nparity ^= 1;
+      }
     }
-    if (ok) umma_commit_elect(bar_o);
   } else {
     // ---------------------------------------------------------------- P, dS
-    const int w = warp >> 2, r = (warp & 3) * 32 + lane;
+    // w & 1: even or odd steps; w >> 1: columns 0-31 or 32-63 of them
+    const int w = warp >> 2, r = (warp & 3) * 32 + lane, par = w & 1, half = w >> 1;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t buf = tmem + lanes + w * 2 * kStep;
-    const float c = p.scale * kLog2e, factor = ds_factor(p.norms), f = factor * exp2f(-kShift);
+    const uint32_t buf = tmem + lanes + par * 2 * kStep;
+    const float factor = ds_factor(p.norms);
+    const float2 c2 = make_float2(p.scale * kLog2e, p.scale * kLog2e);
+    const float2 f2 = make_float2(factor * exp2f(-kShift), factor * exp2f(-kShift));
     const int32_t qi = kDQ ? r / p.group : 0;
     const bool row = kDQ ? qi < count : r < count;
-    float l = INFINITY, e = 0.f;  // dQ: of this thread's query
-    int32_t lim = 0;              // dQ: keys [0, lim) are seen; dK / dV: packed query rows [lim, ..) of the item see the key
+    float l = -INFINITY, e = 0.f;  // dQ: minus those of this thread's query; exp2(s - inf) = 0
+    int32_t lim = 0;               // dQ: keys [0, lim) are seen; dK / dV: packed query rows [lim, ..) of the item see the key
     if (kDQ) {
       if (row) {
         const int64_t at = static_cast<int64_t>(u.q.begin + r0 + qi) * p.heads + hk * p.group + r % p.group;
-        const float v = __ldg(p.lse + at);
-        if (v != -INFINITY) {
-          l = v * kLog2e;
-          e = p.delta[at] * f;
-        }
+        l = -p.lse[at];
+        e = -p.delta[at];
         lim = keys_seen(u, r0 + qi, p.causal);
       }
     } else if (p.causal) {
       const int64_t first = static_cast<int64_t>(r0) + r + u.q.count - u.k.count;  // the first query that sees this key
       lim = first < 0 ? 0 : static_cast<int32_t>(first < u.q.count ? first : u.q.count) * p.group;
     }
+    int slot = par % kSlots;
+    uint32_t fparity = 0, sparity = 0;
     bool ok = true;
-    for (int j = w; j < nsteps; j += 2) {
-      const int slot = j % kSlots;
-      if (!kDQ) ok = mbar_wait_bounded(bar_full + 8 * slot, (j / kSlots) & 1, p.err, p.wait_ns);  // the row values
-      ok = ok && mbar_wait_bounded(bar_s + 8 * w, (j >> 1) & 1, p.err, p.wait_ns);
-      if (!__all_sync(0xffffffffu, ok && !s_misc[1])) {
-        s_misc[1] = 1;
+    for (int j = par; j < nsteps; j += 2) {
+      if (!kDQ) ok = mbar_wait_short(bar_full + 8 * slot, fparity, p.err, p.wait_ns);  // the rows' values
+      ok = ok && mbar_wait_short(bar_s + 8 * par, sparity, p.err, p.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      float s[kStep], d[kStep];
-      tmem_ld(buf, s);
-      tmem_ld(buf + kStep, d);
-      uint32_t wp[kStep / 2], ws[kStep / 2];
+      float s[32], d[32];
+      tmem_ld(buf + 32 * half, s);
+      tmem_ld(buf + kStep + 32 * half, d);
+      uint32_t wp[16], ws[16];
       const int32_t b0 = b_lo + j * per_step;
-      // columns [from, to) of this row count
-      const int from = kDQ ? 0 : lim - b0 * p.group, to = kDQ ? lim - b0 : kStep;
-      const bool whole = __all_sync(0xffffffffu, from <= 0 && to >= kStep);
-      const float4* vl = reinterpret_cast<const float4*>(smem + L::kRowVals) + slot * 2 * (kStep / 4);
+      // columns [from, to) of this thread's 32 count
+      const int from = kDQ ? 0 : lim - b0 * p.group - 32 * half, to = kDQ ? lim - b0 - 32 * half : 32;
+      const bool whole = __all_sync(0xffffffffu, from <= 0 && to >= 32);
+      const float4* vl = reinterpret_cast<const float4*>(smem + L::kRowVals + slot * 8 * kStep) + 8 * half;
 #pragma unroll
-      for (int i = 0; i < kStep; i += 4) {
+      for (int i = 0; i < 32; i += 4) {
         float4 l4 = make_float4(l, l, l, l), e4 = make_float4(e, e, e, e);
         if (!kDQ) {
-          l4 = vl[i / 4];
-          e4 = vl[kStep / 4 + i / 4];
+          const float4 a = vl[i / 4], b = vl[kStep / 4 + i / 4];
+          l4 = make_float4(kShift - a.x, kShift - a.y, kShift - a.z, kShift - a.w);
+          e4 = make_float4(-b.x, -b.y, -b.z, -b.w);
         }
-        float pv[4], dv[4];
-        pv[0] = exp2_fast(fmaf(s[i], c, -l4.x));
-        pv[1] = exp2_fast(fmaf(s[i + 1], c, -l4.y));
-        pv[2] = exp2_fast(fmaf(s[i + 2], c, -l4.z));
-        pv[3] = exp2_fast(fmaf(s[i + 3], c, -l4.w));
-        dv[0] = pv[0] * fmaf(d[i], f, -e4.x);
-        dv[1] = pv[1] * fmaf(d[i + 1], f, -e4.y);
-        dv[2] = pv[2] * fmaf(d[i + 2], f, -e4.z);
-        dv[3] = pv[3] * fmaf(d[i + 3], f, -e4.w);
+        const float2 x0 = fma2(make_float2(s[i], s[i + 1]), c2, make_float2(l4.x, l4.y));
+        const float2 x1 = fma2(make_float2(s[i + 2], s[i + 3]), c2, make_float2(l4.z, l4.w));
+        float2 p0 = make_float2(exp2_fast(x0.x), exp2_fast(x0.y)), p1 = make_float2(exp2_fast(x1.x), exp2_fast(x1.y));
+        float2 d0 = add2(make_float2(d[i], d[i + 1]), make_float2(e4.x, e4.y));
+        float2 d1 = add2(make_float2(d[i + 2], d[i + 3]), make_float2(e4.z, e4.w));
+        if (!kBf16) {  // exact: a power of two
+          d0 = mul2(d0, f2);
+          d1 = mul2(d1, f2);
+        }
+        d0 = mul2(p0, d0);
+        d1 = mul2(p1, d1);
         if (!whole) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const bool see = i + x >= from && i + x < to;
-            pv[x] = see ? pv[x] : 0.f;
-            dv[x] = see ? dv[x] : 0.f;
-          }
+          auto keep = [&](int x, float v) { return i + x >= from && i + x < to ? v : 0.f; };
+          p0 = make_float2(keep(0, p0.x), keep(1, p0.y));
+          p1 = make_float2(keep(2, p1.x), keep(3, p1.y));
+          d0 = make_float2(keep(0, d0.x), keep(1, d0.y));
+          d1 = make_float2(keep(2, d1.x), keep(3, d1.y));
         }
         if (!kDQ) {
-          wp[i / 2] = pack2<T>(pv[0], pv[1]);
-          wp[i / 2 + 1] = pack2<T>(pv[2], pv[3]);
+          wp[i / 2] = pack2<T>(p0.x, p0.y);
+          wp[i / 2 + 1] = pack2<T>(p1.x, p1.y);
         }
-        ws[i / 2] = pack2<T>(dv[0], dv[1]);
-        ws[i / 2 + 1] = pack2<T>(dv[2], dv[3]);
+        ws[i / 2] = pack2<T>(d0.x, d0.y);
+        ws[i / 2 + 1] = pack2<T>(d1.x, d1.y);
       }
-      if (!kDQ) tmem_st(buf, wp);
-      tmem_st(buf + kStep, ws);
+      // over this thread's own scores: the other half's may not be read yet
+      if (!kDQ) tmem_st(buf + 32 * half, wp);
+      tmem_st(buf + kStep + 32 * half, ws);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_p + 8 * w);
+      if (lane == 0) mbar_arrive(bar_p + 8 * par);
+      __syncwarp();
+      sparity ^= 1;
+      if ((slot += 2) >= kSlots) {
+        slot -= kSlots;
+        fparity ^= 1;
+      }
     }
     // --------------------------------------------------------------- results
     if (ok && nsteps > 0) {
-      ok = mbar_wait_bounded(bar_o, 0, p.err, p.wait_ns);
-      ok = __all_sync(0xffffffffu, ok && !s_misc[1]);
+      ok = __all_sync(0xffffffffu, mbar_wait_short(bar_o, 0, p.err, p.wait_ns));
       tc_fence_after();
     }
     if (ok) {
-      // dQ: the warps of the two halves take half of the columns each; dK / dV: one of the two each
-      const int c_lo = kDQ ? w * (DP / 2) : 0, c_hi = kDQ ? c_lo + DP / 2 : DP;
-      const bool second = !kDQ && w == 1;
+      // dQ: 32 columns each (64 channels: the first two groups); dK: groups 0
+      // and 2, dV: 1 and 3, half of the columns each
+      const int c_lo = kDQ ? 32 * w : half * (DP / 2), c_hi = kDQ ? (c_lo + 32 < DP ? c_lo + 32 : DP) : c_lo + DP / 2;
+      const bool second = !kDQ && par == 1;
       const uint32_t acc = tmem + lanes + 4 * kStep + (second ? DP : 0);
       const float mul = second ? exp2f(-kShift) : p.scale / factor;
       const int64_t out_row = kDQ ? static_cast<int64_t>(u.q.begin) + r0 + qi : static_cast<int64_t>(u.k.begin) + r0 + r;
@@ -389,27 +386,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
         }
-        if (!row) continue;
         uint4* d = reinterpret_cast<uint4*>(to + c0);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (c0 + 8 * i < p.dim)
+          if (row && c0 + 8 * i < p.dim)
             d[i] = make_uint4(pack2<T>(o[8 * i] * mul, o[8 * i + 1] * mul), pack2<T>(o[8 * i + 2] * mul, o[8 * i + 3] * mul),
                               pack2<T>(o[8 * i + 4] * mul, o[8 * i + 5] * mul),
                               pack2<T>(o[8 * i + 6] * mul, o[8 * i + 7] * mul));
+        __syncwarp();  // the warp reads TMEM together
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
-// delta[row, head] = sum of dO * O; fp16: also the largest squared norms of
+// delta[row, head] = sum of dO * O, and lse2 = lse log2e, or +infinity for a
+// row that saw no key, whose P = exp2(S - lse2) is then 0; fp16: also the largest squared norms of
 // the rows of dO and of V that belong to items (as bits: they are not
 // negative).  LPR lanes hold a row of up to 8 LPR channels.
 template <typename T, int LPR>
-__global__ void __launch_bounds__(256) k_attn_delta_tc(const AttnArgs a, uint32_t* norms) {
+__global__ void __launch_bounds__(256) k_attn_delta_tc(const AttnArgs a, float* lse2, uint32_t* norms) {
   using C = Chunk<T, 8>;
   const int l = threadIdx.x % LPR;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * (256 / LPR), first = static_cast<int64_t>(blockIdx.x) * (256 / LPR);
@@ -440,7 +438,10 @@ __global__ void __launch_bounds__(256) k_attn_delta_tc(const AttnArgs a, uint32_
       }
     }
     s = group_sum<LPR>(s);
-    if (there && l == 0) a.delta[i] = s;
+    if (there && l == 0) {
+      a.delta[i] = s;
+      lse2[i] = a.lse[i] == -INFINITY ? INFINITY : a.lse[i] * kLog2e;
+    }
     if (norms) top = fmaxf(top, group_sum<LPR>(q));
   }
   if (!norms) return;
@@ -467,8 +468,8 @@ __global__ void __launch_bounds__(256) k_attn_delta_tc(const AttnArgs a, uint32_
 }
 
 template <typename T, int DP>
-cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const CUtensorMap* maps, int sms, uint32_t* norms,
-                         cudaStream_t st) {
+cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const CUtensorMap* maps, int sms, float* lse2,
+                         uint32_t* norms, cudaStream_t st) {
   const int64_t rows = a.n * a.heads, per = DP == 64 ? 32 : 16;
   int64_t blocks = (rows + per - 1) / per;
   blocks = blocks < 8ll * sms ? (blocks < 1 ? 1 : blocks) : 8ll * sms;
@@ -476,7 +477,7 @@ cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const CUtensorMap* maps
     const cudaError_t e = cudaMemsetAsync(norms, 0, 2 * sizeof(uint32_t), st);
     if (e != cudaSuccess) return e;
   }
-  k_attn_delta_tc<T, DP / 8><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, norms);
+  k_attn_delta_tc<T, DP / 8><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, lse2, norms);
   constexpr int kSmem = static_cast<int>(BwdLayout<DP>::kTotal);
   auto kq = k_attn_bwd_tc<T, DP, true>;
   auto kk = k_attn_bwd_tc<T, DP, false>;
@@ -512,7 +513,7 @@ bool attn_bwd_tc_supported(const AttnArgs& a) {
          (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && encode_fn() != nullptr;
 }
 
-cudaError_t launch_attn_bwd_tc(const AttnArgs& a, uint32_t* norms, int sms, cudaStream_t st) {
+cudaError_t launch_attn_bwd_tc(const AttnArgs& a, float* lse2, uint32_t* norms, int sms, cudaStream_t st) {
   const int group = a.heads / a.kv_heads;
   BwdParams p = {};
   p.qpt = kRows / group;
@@ -540,7 +541,7 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs& a, uint32_t* norms, int sms, cuda
   p.group = group;
   p.scale = a.scale;
   p.causal = a.causal;
-  p.lse = a.lse;
+  p.lse = lse2;
   p.delta = a.delta;
   if (a.dtype != kF16) norms = nullptr;
   p.norms = norms;
@@ -548,10 +549,10 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs& a, uint32_t* norms, int sms, cuda
   // never below 100 ms, so that no CTA leaves with its loads in flight
   p.wait_ns = scan_wait_limit_ns() > 100000000ull ? scan_wait_limit_ns() : 100000000ull;
   if (a.dtype == kBF16)
-    return a.dim <= 64 ? launch_typed<__nv_bfloat16, 64>(a, p, maps, sms, norms, st)
-                       : launch_typed<__nv_bfloat16, 128>(a, p, maps, sms, norms, st);
-  return a.dim <= 64 ? launch_typed<__half, 64>(a, p, maps, sms, norms, st)
-                     : launch_typed<__half, 128>(a, p, maps, sms, norms, st);
+    return a.dim <= 64 ? launch_typed<__nv_bfloat16, 64>(a, p, maps, sms, lse2, norms, st)
+                       : launch_typed<__nv_bfloat16, 128>(a, p, maps, sms, lse2, norms, st);
+  return a.dim <= 64 ? launch_typed<__half, 64>(a, p, maps, sms, lse2, norms, st)
+                     : launch_typed<__half, 128>(a, p, maps, sms, lse2, norms, st);
 }
 
 }  // namespace smc

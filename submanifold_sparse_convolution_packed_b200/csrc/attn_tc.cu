@@ -51,7 +51,7 @@ template <int DP> struct FwdLayout {
   static constexpr uint32_t kTileBytes = DP / 64 * kPanel;
   static constexpr int kSlots = DP == 64 ? 8 : 4;
   static constexpr uint32_t kQ = 0, kKv = 2 * kTileBytes, kBar = kKv + kSlots * kTileBytes;
-  // barriers: q, kv full[kSlots], kv empty[kSlots], s full[2], p ready[2], o full[2], tail
+  // barriers: q, kv full[kSlots], kv empty[kSlots], s full[2], p ready[2], o done[2], tail
   static constexpr uint32_t kMisc = kBar + 8 * (2 * kSlots + 8), kTotal = kMisc + 32 + 1024;
 };
 
@@ -66,9 +66,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   __shared__ Unit s_unit;
   const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - raw);
-  volatile uint32_t* s_misc = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);  // [0] tmem, [1] abort
+  volatile uint32_t* s_misc = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);  // [0] tmem
   const uint32_t bar_q = sbase + L::kBar, bar_full = bar_q + 8, bar_empty = bar_full + 8 * kSlots;
-  const uint32_t bar_s = bar_empty + 8 * kSlots, bar_p = bar_s + 16, bar_o = bar_p + 16, bar_tail = bar_o + 16;
+  const uint32_t bar_s = bar_empty + 8 * kSlots, bar_p = bar_s + 16, bar_o = bar_p + 16;
+  const uint32_t bar_tail = bar_o + 16;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // causal: the tiles with the most keys come last in an item and start first
@@ -107,7 +108,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mbar_init(bar_o + 8 * t, 1);
     }
     mbar_init(bar_tail, 1);
-    s_misc[1] = 0;
     fence_mbarrier_init();
     fence_proxy_async_smem();
   }
@@ -133,15 +133,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         u.q.begin + q0 + t * p.qpt);
       }
       __syncwarp();
+      int slot = 0;
+      uint32_t parity = 1;
       for (int i = 0; i < 2 * nsteps; ++i) {
-        const int slot = i % kSlots;
-        int ok = 1;
-        if (lane == 0)
-          ok = mbar_wait_bounded(bar_empty + 8 * slot, ((i / kSlots) & 1) ^ 1, p.err, p.wait_ns) && !s_misc[1];
-        if (!__shfl_sync(0xffffffffu, ok, 0)) {
-          if (lane == 0) s_misc[1] = 1;
-          break;
-        }
+        if (!__all_sync(0xffffffffu, mbar_wait_short(bar_empty + 8 * slot, parity, p.err, p.wait_ns))) break;
         const int32_t key = k_lo + (i >> 1) * kRows;
         const int rows = u.k.count - key;  // V rows behind the item's end are zeroed below
         const bool tail = (i & 1) && rows < kRows;
@@ -153,11 +148,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         __syncwarp();
         if (tail) {  // once, at the last step
-          ok = mbar_wait_bounded(bar_tail, 0, p.err, p.wait_ns);
-          if (!__all_sync(0xffffffffu, ok)) {
-            if (lane == 0) s_misc[1] = 1;
-            break;
-          }
+          if (!__all_sync(0xffffffffu, mbar_wait_short(bar_tail, 0, p.err, p.wait_ns))) break;
           uint4* base = reinterpret_cast<uint4*>(smem + L::kKv + slot * L::kTileBytes);
           for (int c = 0; c < kPanels; ++c)
             for (int j = rows * 8 + lane; j < kRows * 8; j += 32) base[c * (kPanel / 16) + j] = make_uint4(0, 0, 0, 0);
@@ -165,61 +156,81 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_full + 8 * slot);
         }
+        if (++slot == kSlots) {
+          slot = 0;
+          parity ^= 1;
+        }
       }
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------- MMA issue
+    // The whole warp runs the loop; one elected lane issues each batch, with
+    // the descriptors advanced by additions only (computing them anew made
+    // each MMA cost about 120 clocks of this warp's time).
     const uint32_t ab = kBf16 ? 1u : 0u;
     const int ks = (p.dim + 15) / 16;
     const uint32_t idesc_s = idesc_f16(ab, kRows), idesc_o = idesc_f16(ab, static_cast<uint32_t>(ks * 16)) | kIdescBMn;
-    bool ok = nsteps > 0;
+    const uint64_t q = kmajor_desc(sbase + L::kQ, 128), kd = kmajor_desc(sbase + L::kKv, 128);
+    const uint64_t vd = mnmajor_desc(sbase + L::kKv, kPanel);
+    constexpr uint64_t kTile = L::kTileBytes >> 4;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-      const bool w = mbar_wait_bounded(bar, parity, p.err, p.wait_ns);
-      if (!__all_sync(0xffffffffu, w && !s_misc[1])) {
-        if (lane == 0) s_misc[1] = 1;
-        ok = false;
-      }
+      const bool w = __all_sync(0xffffffffu, mbar_wait_short(bar, parity, p.err, p.wait_ns));
       tc_fence_after();
+      return w;
     };
-    auto scores = [&](int t, int slot) {
-      const uint32_t a = sbase + L::kQ + t * L::kTileBytes, b = sbase + L::kKv + slot * L::kTileBytes;
-      for (int k = 0; k < ks; ++k) {
-        const uint64_t off = 2 * (k & 3);
-        umma_f16_elect(tmem + t * kRows, kmajor_desc(a + (k >> 2) * kPanel, 128) + off,
-                       kmajor_desc(b + (k >> 2) * kPanel, 128) + off, idesc_s, k > 0);
+    auto scores = [&](int t, uint64_t k0) {
+      if (elect_one()) {
+        const uint64_t a0 = q + t * kTile;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k)
+          if (k < ks)
+            umma_f16(tmem + t * kRows, a0 + (k >> 2) * (kPanel >> 4) + 2 * (k & 3),
+                     k0 + (k >> 2) * (kPanel >> 4) + 2 * (k & 3), idesc_s, k > 0);
+        umma_commit(bar_s + 8 * t);
       }
-      umma_commit_elect(bar_s + 8 * t);
+      __syncwarp();
     };
-    if (ok) wait(bar_q, 0);
-    if (ok) wait(bar_full, 0);
+    bool ok = nsteps > 0 && wait(bar_q, 0) && wait(bar_full, 0);
     if (ok) {
-      for (int t = 0; t < 2; ++t)
-        if (steps[t] > 0) scores(t, 0);
+      if (steps[0] > 0) scores(0, kd);
+      if (steps[1] > 0) scores(1, kd);
       if (kSlots < 2 * nsteps) umma_commit_elect(bar_empty);
     }
+    int sv = 1, sk = 2 % kSlots;  // slots of V of this step, of K of the next
+    uint32_t pv = 0, pk = 0;
     for (int j = 0; j < nsteps && ok; ++j) {
-      const int iv = 2 * j + 1, ik = 2 * j + 2, sv = iv % kSlots, sk = ik % kSlots;
       bool next = false;  // K of the next step awaited
-      wait(bar_full + 8 * sv, (iv / kSlots) & 1);
+      ok = wait(bar_full + 8 * sv, pv);
+      const uint64_t v0 = vd + sv * kTile, k0 = kd + sk * kTile;
       for (int t = 0; t < 2 && ok; ++t) {
         if (j >= steps[t]) continue;
-        wait(bar_p + 8 * t, j & 1);
+        ok = wait(bar_p + 8 * t, j & 1);
         if (!ok) break;
-        const uint64_t b = mnmajor_desc(sbase + L::kKv + sv * L::kTileBytes, kPanel);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kRows / 16; ++k)
-          umma_f16_ts_elect(tmem + 2 * kRows + t * DP, tmem + t * kRows + k * 8, b + 128 * k, idesc_o, j > 0 || k > 0);
+          for (int k = 0; k < kRows / 16; ++k)
+            umma_f16_ts(tmem + 2 * kRows + t * DP, tmem + t * kRows + k * 8, v0 + 128 * k, idesc_o, j > 0 || k > 0);
+          if (j + 1 == steps[t]) umma_commit(bar_o + 8 * t);
+        }
+        __syncwarp();
         if (j + 1 < steps[t]) {
-          if (!next) wait(bar_full + 8 * sk, (ik / kSlots) & 1);
+          ok = next || wait(bar_full + 8 * sk, pk);
           next = true;
-          if (ok) scores(t, sk);
-        } else {
-          umma_commit_elect(bar_o + 8 * t);
+          if (ok) scores(t, k0);
         }
       }
+      if (!ok) break;
       // only for slots that are loaded again: no arrival is left under way at the end
-      if (iv + kSlots < 2 * nsteps) umma_commit_elect(bar_empty + 8 * sv);
-      if (next && ik + kSlots < 2 * nsteps) umma_commit_elect(bar_empty + 8 * sk);
+      if (2 * j + 1 + kSlots < 2 * nsteps) umma_commit_elect(bar_empty + 8 * sv);
+      if (next && 2 * j + 2 + kSlots < 2 * nsteps) umma_commit_elect(bar_empty + 8 * sk);
+      if ((sv += 2) >= kSlots) {
+        sv -= kSlots;
+        pv ^= 1;
+      }
+      if ((sk += 2) >= kSlots) {
+        sk -= kSlots;
+        pk ^= 1;
+      }
     }
   } else {
     // --------------------------------------------------------------- softmax
@@ -233,12 +244,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     float top = -INFINITY, sum = 0.f;  // top: the rounded product with c the sums refer to
     bool ok = true;
     for (int j = 0; j < steps[t]; ++j) {
-      ok = mbar_wait_bounded(bar_s + 8 * t, j & 1, p.err, p.wait_ns);
-      if (!__all_sync(0xffffffffu, ok && !s_misc[1])) {
-        s_misc[1] = 1;
-        ok = false;
-        break;
-      }
+      ok = __all_sync(0xffffffffu, mbar_wait_short(bar_s + 8 * t, j & 1, p.err, p.wait_ns));
+      if (!ok) break;
       tc_fence_after();
       float x[kRows];
       tmem_ld(ts, x);
@@ -264,7 +271,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           sum *= keep;
           top = m;
         }
-        if (j > 0) {  // this tile's products so far are complete: its S came after them
+        if (j > 0) {  // this tile's products so far are complete: its scores came after them
           for (int c0 = 0; c0 < DP; c0 += 32) {
             float o[32];
             uint32_t b[32];
@@ -276,34 +283,33 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
       }
       const float base = top == -INFINITY ? 0.f : top;
-      float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+      float2 sa = make_float2(0.f, 0.f), sb = sa;
+      const float2 c2 = make_float2(p.c, p.c), b2 = make_float2(-base, -base);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t w[32];
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
           const int e = h * 64 + 2 * i;
-          const float a0 = exp2_fast(fmaf(x[e], p.c, -base)), a1 = exp2_fast(fmaf(x[e + 1], p.c, -base));
-          const float a2 = exp2_fast(fmaf(x[e + 2], p.c, -base)), a3 = exp2_fast(fmaf(x[e + 3], p.c, -base));
-          s0 += a0;
-          s1 += a1;
-          s2 += a2;
-          s3 += a3;
-          w[i] = pack2<T>(a0, a1);
-          w[i + 1] = pack2<T>(a2, a3);
+          const float2 y0 = fma2(make_float2(x[e], x[e + 1]), c2, b2), y1 = fma2(make_float2(x[e + 2], x[e + 3]), c2, b2);
+          const float2 e0 = make_float2(exp2_fast(y0.x), exp2_fast(y0.y)), e1 = make_float2(exp2_fast(y1.x), exp2_fast(y1.y));
+          sa = add2(sa, e0);
+          sb = add2(sb, e1);
+          w[i] = pack2<T>(e0.x, e0.y);
+          w[i + 1] = pack2<T>(e1.x, e1.y);
         }
         tmem_st(ts + h * 32, w);
       }
-      sum += (s0 + s1) + (s2 + s3);
+      sum += (sa.x + sa.y) + (sb.x + sb.y);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_p + 8 * t);
+      __syncwarp();
     }
     // --------------------------------------------------------------- results
     if (ok && steps[t] > 0) {
-      ok = mbar_wait_bounded(bar_o + 8 * t, 0, p.err, p.wait_ns);
-      ok = __all_sync(0xffffffffu, ok && !s_misc[1]);
+      ok = __all_sync(0xffffffffu, mbar_wait_short(bar_o + 8 * t, 0, p.err, p.wait_ns));
       tc_fence_after();
     }
     if (ok) {
@@ -322,8 +328,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
         }
-        if (!row) continue;
-        if (split) {
+        if (!row) {
+          // nothing to store; the warp reads TMEM together
+        } else if (split) {
           float4* d = reinterpret_cast<float4*>(p.part_o + slot * p.dim + c0);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -336,6 +343,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               d[i] = make_uint4(pack2<T>(o[8 * i] * inv, o[8 * i + 1] * inv), pack2<T>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
                                 pack2<T>(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack2<T>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
         }
+        __syncwarp();
       }
       if (row) {
         if (split) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(top, sum);

@@ -225,9 +225,9 @@ bool attn_tc_supported(const AttnArgs& a);
 int64_t attn_tc_scratch(const AttnArgs& a, int sms);
 cudaError_t launch_attn_tc(const AttnArgs& a, void* scratch, int sms, cudaStream_t s);
 // Backward pass (attn_bwd_tc.cu): the same shapes, gradients and dout aligned
-// too; norms: two words of scratch.
+// too; scratch: lse2 [n, heads], norms two words.
 bool attn_bwd_tc_supported(const AttnArgs& a);
-cudaError_t launch_attn_bwd_tc(const AttnArgs& a, uint32_t* norms, int sms, cudaStream_t s);
+cudaError_t launch_attn_bwd_tc(const AttnArgs& a, float* lse2, uint32_t* norms, int sms, cudaStream_t s);
 
 // dtype codes as in smc.h
 enum DType : int { kF32 = 0, kBF16 = 1, kF16 = 2 };
