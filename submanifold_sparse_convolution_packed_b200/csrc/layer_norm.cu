@@ -27,27 +27,89 @@ namespace smc {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f;
 
-// The exponential is the accurate one for fp32 rows and the fast one (an
-// error of a few fp32 ulp, far below the rounding of the result) otherwise.
-template <typename T> __device__ __forceinline__ float exp_for(float x) {
-  return std::is_same<T, float>::value ? expf(x) : __expf(x);
+// 1 / (1 + exp(-z)).  fp32 rows take the accurate exponential and a division;
+// the others the fast exponential (an error of a few fp32 ulp, far below the
+// rounding of the result).
+template <typename T> __device__ __forceinline__ float sigmoid(float z) {
+  return std::is_same<T, float>::value ? 1.f / (1.f + expf(-z)) : __fdividef(1.f, 1.f + exp2_fast(z * -kLog2e));
+}
+
+// Two of them with one reciprocal: 1/a = b * 1/(ab).  The special-function unit
+// otherwise bounds 16-bit rows (an exponential and a reciprocal for each value
+// at 16 lanes a clock).  The exponent is cut at 62 (z = -43), so that ab stays
+// in range; what is behind it is below 1e-17 either way.  A NaN passes the cut
+// and comes back with the product by z.
+template <typename T> __device__ __forceinline__ void sigmoid2(float z0, float z1, float* s0, float* s1) {
+  if (std::is_same<T, float>::value) {
+    *s0 = sigmoid<T>(z0);
+    *s1 = sigmoid<T>(z1);
+    return;
+  }
+  const float2 t = mul2(make_float2(z0, z1), make_float2(-kLog2e, -kLog2e));
+  const float a = 1.f + exp2_fast(fminf(t.x, 62.f)), b = 1.f + exp2_fast(fminf(t.y, 62.f));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
+  *s0 = r * b;
+  *s1 = r * a;
 }
 
 template <typename T> __device__ __forceinline__ float act_value(float z, int act) {
-  if (act == kActRelu) return z > 0.f ? z : (z != z ? z : 0.f);
-  if (act == kActSilu) return z / (1.f + exp_for<T>(-z));
+  if (act == kActRelu) return z < 0.f ? 0.f : z;  // a NaN stays
+  if (act == kActSilu) return z * sigmoid<T>(z);
   return z;
 }
 
 template <typename T> __device__ __forceinline__ float act_slope(float z, int act) {
   if (act == kActRelu) return z > 0.f ? 1.f : 0.f;
   if (act == kActSilu) {
-    const float s = 1.f / (1.f + exp_for<T>(-z));
+    const float s = sigmoid<T>(z);
     return s * (1.f + z * (1.f - s));
   }
   return 1.f;
 }
+
+// act over a lane's values, and its slopes there.
+template <typename T, int N> __device__ __forceinline__ void act_values(float (&z)[N], int act) {
+  if (act == kActNone) return;
+  if (act == kActSilu && N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i + 1 < N; i += 2) {
+      float2 s;
+      sigmoid2<T>(z[i], z[i + 1], &s.x, &s.y);
+      s = mul2(make_float2(z[i], z[i + 1]), s);
+      z[i] = s.x;
+      z[i + 1] = s.y;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) z[i] = act_value<T>(z[i], act);
+}
+
+template <typename T, int N> __device__ __forceinline__ void act_slopes(float (&z)[N], int act) {
+  if (act == kActSilu && N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i + 1 < N; i += 2) {
+      float2 s;
+      sigmoid2<T>(z[i], z[i + 1], &s.x, &s.y);
+      const float2 zz = make_float2(z[i], z[i + 1]), one = make_float2(1.f, 1.f);
+      // s (1 + z (1 - s))
+      const float2 t = mul2(s, fma2(zz, add2(one, make_float2(-s.x, -s.y)), one));
+      z[i] = t.x;
+      z[i + 1] = t.y;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) z[i] = act_slope<T>(z[i], act);
+}
+
+// Blocks that an SM should hold, by the elements a lane holds: more rows in
+// flight for short rows, registers for long ones.
+constexpr int fwd_blocks(int elems) { return elems <= 8 ? 4 : elems <= 16 ? 2 : 1; }
+constexpr int bwd_blocks(int elems) { return elems <= 8 ? 2 : elems <= 16 ? 2 : 1; }
 
 template <typename T>
 struct NormArgs {
@@ -60,194 +122,290 @@ struct NormArgs {
   float eps;
 };
 
-template <typename T, int EPC, int NCH, int TPR>
-__global__ void __launch_bounds__(kThreads) k_layer_norm(const NormArgs<T> a) {
-  using C = Chunk<T, EPC>;
-  constexpr int kRows = kThreads / TPR;
-  const int l = threadIdx.x % TPR, chunks = a.c / EPC;
-  const C* x = reinterpret_cast<const C*>(a.x);
-  C* y = reinterpret_cast<C*>(a.out);
-  C gam[NCH], bet[NCH], cur[NCH], nxt[NCH];
-  float f[EPC];
+// Elementwise steps over a lane's values, two to an instruction.
+template <int N> __device__ __forceinline__ float sum_of(const float (&x)[N]) {
+  if constexpr (N % 2 == 0) {
+    float2 s = make_float2(x[0], x[1]);
 #pragma unroll
-  for (int i = 0; i < EPC; ++i) f[i] = 1.f;
-  const C one = pack<T, EPC>(f);
-#pragma unroll
-  for (int i = 0; i < EPC; ++i) f[i] = 0.f;
-  const C zero = pack<T, EPC>(f);
-#pragma unroll
-  for (int k = 0; k < NCH; ++k) {
-    const int j = k * TPR + l;
-    gam[k] = a.gamma && j < chunks ? reinterpret_cast<const C*>(a.gamma)[j] : one;
-    bet[k] = a.beta && j < chunks ? reinterpret_cast<const C*>(a.beta)[j] : zero;
+    for (int i = 2; i < N; i += 2) s = add2(s, make_float2(x[i], x[i + 1]));
+    return s.x + s.y;
   }
-  const float inv = static_cast<float>(a.c);
-  auto fetch = [&](int64_t row, C(&to)[NCH]) {
+  float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      const int j = k * TPR + l;
-      to[k] = row < a.n && j < chunks ? x[row * chunks + j] : zero;
+  for (int i = 0; i < N; ++i) s += x[i];
+  return s;
+}
+
+template <int N> __device__ __forceinline__ float dot_of(const float (&x)[N], const float (&y)[N]) {
+  if constexpr (N % 2 == 0) {
+    float2 s = mul2(make_float2(x[0], x[1]), make_float2(y[0], y[1]));
+#pragma unroll
+    for (int i = 2; i < N; i += 2) s = fma2(make_float2(x[i], x[i + 1]), make_float2(y[i], y[i + 1]), s);
+    return s.x + s.y;
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) s += x[i] * y[i];
+  return s;
+}
+
+// z = x * y + w, elementwise (z may be any of them).
+template <int N>
+__device__ __forceinline__ void fma_all(const float (&x)[N], const float (&y)[N], const float (&w)[N], float (&z)[N]) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 t = fma2(make_float2(x[i], x[i + 1]), make_float2(y[i], y[i + 1]), make_float2(w[i], w[i + 1]));
+      z[i] = t.x;
+      z[i + 1] = t.y;
     }
-  };
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
-  int64_t base = static_cast<int64_t>(blockIdx.x) * kRows;
-  fetch(base + threadIdx.x / TPR, cur);
-  for (; base < a.n; base += step) {
-    const int64_t row = base + threadIdx.x / TPR;
-    fetch(row + step, nxt);
-    float s = 0.f;
+  } else {
 #pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      unpack(cur[k], f);
-#pragma unroll
-      for (int i = 0; i < EPC; ++i) s += f[i];
-    }
-    const float mean = group_sum<TPR>(s) / inv;
-    s = 0.f;
-#pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      unpack(cur[k], f);
-      const bool there = k * TPR + l < chunks;
-#pragma unroll
-      for (int i = 0; i < EPC; ++i) s += there ? (f[i] - mean) * (f[i] - mean) : 0.f;
-    }
-    const float rstd = 1.f / sqrtf(group_sum<TPR>(s) / inv + a.eps);
-    if (row < a.n) {
-#pragma unroll
-      for (int k = 0; k < NCH; ++k) {
-        const int j = k * TPR + l;
-        float g[EPC], b[EPC];
-        unpack(cur[k], f);
-        unpack(gam[k], g);
-        unpack(bet[k], b);
-#pragma unroll
-        for (int i = 0; i < EPC; ++i) f[i] = act_value<T>((f[i] - mean) * rstd * g[i] + b[i], a.act);
-        if (j < chunks) y[row * chunks + j] = pack<T, EPC>(f);
-      }
-      if (a.stats && l == 0) {
-        a.stats[2 * row] = mean;
-        a.stats[2 * row + 1] = rstd;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < NCH; ++k) cur[k] = nxt[k];
+    for (int i = 0; i < N; ++i) z[i] = fmaf(x[i], y[i], w[i]);
   }
 }
 
-template <typename T, int EPC, int NCH, int TPR>
-__global__ void __launch_bounds__(kThreads) k_layer_norm_bwd(const NormArgs<T> a) {
+template <int N> __device__ __forceinline__ void mul_all(float (&z)[N], const float (&x)[N]) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 t = mul2(make_float2(z[i], z[i + 1]), make_float2(x[i], x[i + 1]));
+      z[i] = t.x;
+      z[i + 1] = t.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] *= x[i];
+  }
+}
+
+// z = (z + a) * m
+template <int N> __device__ __forceinline__ void shift_scale(float (&z)[N], float a, float m) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 t = mul2(add2(make_float2(z[i], z[i + 1]), make_float2(a, a)), make_float2(m, m));
+      z[i] = t.x;
+      z[i + 1] = t.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = (z[i] + a) * m;
+  }
+}
+
+// A lane's chunks of a row: chunk k * TPR + l of each of its NCH (kWhole: the
+// row has all of them).
+template <typename T, int EPC, int NCH, int TPR, bool kWhole>
+struct Row {
   using C = Chunk<T, EPC>;
-  constexpr int kRows = kThreads / TPR;
-  extern __shared__ float s_sum[];  // [2, c]
+  C c[NCH];
+  __device__ __forceinline__ void load(const C* p, int l, int chunks, bool there) {
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int j = k * TPR + l;
+      if (there && (kWhole || j < chunks)) {
+        c[k] = p[j];
+      } else {
+        float f[EPC];
+#pragma unroll
+        for (int i = 0; i < EPC; ++i) f[i] = 0.f;
+        c[k] = pack<T, EPC>(f);
+      }
+    }
+  }
+  __device__ __forceinline__ void values(float (&f)[NCH * EPC]) const {
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      float t[EPC];
+      unpack(c[k], t);
+#pragma unroll
+      for (int i = 0; i < EPC; ++i) f[k * EPC + i] = t[i];
+    }
+  }
+  static __device__ __forceinline__ void store(C* p, const float (&f)[NCH * EPC], int l, int chunks) {
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int j = k * TPR + l;
+      float t[EPC];
+#pragma unroll
+      for (int i = 0; i < EPC; ++i) t[i] = f[k * EPC + i];
+      if (kWhole || j < chunks) p[j] = pack<T, EPC>(t);
+    }
+  }
+};
+
+// gamma (or 1) and beta (or 0) of a lane's channels.
+template <typename T, int EPC, int NCH, int TPR, bool kWhole>
+__device__ __forceinline__ void parameter(const T* p, float otherwise, int l, int chunks, float (&f)[NCH * EPC]) {
+  if (p) {
+    Row<T, EPC, NCH, TPR, kWhole> r;
+    r.load(reinterpret_cast<const Chunk<T, EPC>*>(p), l, chunks, true);
+    r.values(f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NCH * EPC; ++i) f[i] = otherwise;
+  }
+}
+
+template <typename T, int EPC, int NCH, int TPR, bool kWhole>
+__global__ void __launch_bounds__(kThreads, fwd_blocks(EPC* NCH)) k_layer_norm(const NormArgs<T> a) {
+  using C = Chunk<T, EPC>;
+  constexpr int kRows = kThreads / TPR, N = NCH * EPC;
+  const int l = threadIdx.x % TPR, chunks = a.c / EPC;
+  const C* x = reinterpret_cast<const C*>(a.x);
+  C* y = reinterpret_cast<C*>(a.out);
+  float gam[N], bet[N], f[N];
+  parameter<T, EPC, NCH, TPR, kWhole>(a.gamma, 1.f, l, chunks, gam);
+  parameter<T, EPC, NCH, TPR, kWhole>(a.beta, 0.f, l, chunks, bet);
+  const float inv = 1.f / static_cast<float>(a.c);
+  // channels a lane holds beyond the row's, as zeros
+  bool pad = false;
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) pad = pad || (!kWhole && k * TPR + l >= chunks);
+  Row<T, EPC, NCH, TPR, kWhole> cur;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+  int64_t base = static_cast<int64_t>(blockIdx.x) * kRows, row = base + threadIdx.x / TPR;
+  const int64_t jump = step * chunks;
+  x += row * chunks;
+  y += row * chunks;
+  cur.load(x, l, chunks, row < a.n);
+  for (; base < a.n; base += step, row += step, y += jump) {
+    cur.values(f);
+    x += jump;
+    cur.load(x, l, chunks, row + step < a.n);  // the next row
+    const float mean = group_sum<TPR>(sum_of(f)) * inv;
+    shift_scale(f, -mean, 1.f);
+    float s = dot_of(f, f);
+    if (pad) {  // a padded channel's 0 - mean does not count
+#pragma unroll
+      for (int k = 0; k < NCH; ++k)
+        if (k * TPR + l >= chunks) {
+#pragma unroll
+          for (int i = 0; i < EPC; ++i) f[k * EPC + i] = 0.f;
+        }
+      s = dot_of(f, f);
+    }
+    const float rstd = rsqrtf(group_sum<TPR>(s) * inv + a.eps);
+    shift_scale(f, 0.f, rstd);
+    fma_all(f, gam, bet, f);
+    act_values<T, N>(f, a.act);
+    if (row < a.n) {
+      Row<T, EPC, NCH, TPR, kWhole>::store(y, f, l, chunks);
+      if (a.stats && l == 0) reinterpret_cast<float2*>(a.stats)[row] = make_float2(mean, rstd);
+    }
+  }
+}
+
+template <typename T, int EPC, int NCH, int TPR, bool kWhole>
+__global__ void __launch_bounds__(kThreads, bwd_blocks(EPC* NCH)) k_layer_norm_bwd(const NormArgs<T> a) {
+  using C = Chunk<T, EPC>;
+  constexpr int kRows = kThreads / TPR, N = NCH * EPC;
+  constexpr bool kAhead = N <= 8;  // the next row is fetched before this one is worked on
+  extern __shared__ float s_sum[];  // [warps, c]
   const int l = threadIdx.x % TPR, chunks = a.c / EPC;
   const C* x = reinterpret_cast<const C*>(a.x);
   const C* dy = reinterpret_cast<const C*>(a.dy);
   C* dx = reinterpret_cast<C*>(a.out);
   const float2* st = reinterpret_cast<const float2*>(a.stats_in);
-  C gam[NCH], bet[NCH], cx[NCH], cd[NCH], nx[NCH], nd[NCH];
-  float f[EPC];
+  float dg[N], db[N], xh[N], g[N];
 #pragma unroll
-  for (int i = 0; i < EPC; ++i) f[i] = 1.f;
-  const C one = pack<T, EPC>(f);
-#pragma unroll
-  for (int i = 0; i < EPC; ++i) f[i] = 0.f;
-  const C zero = pack<T, EPC>(f);
-  float dg[NCH * EPC], db[NCH * EPC];
-#pragma unroll
-  for (int k = 0; k < NCH; ++k) {
-    const int j = k * TPR + l;
-    gam[k] = a.gamma && j < chunks ? reinterpret_cast<const C*>(a.gamma)[j] : one;
-    bet[k] = a.beta && j < chunks ? reinterpret_cast<const C*>(a.beta)[j] : zero;
-#pragma unroll
-    for (int i = 0; i < EPC; ++i) dg[k * EPC + i] = db[k * EPC + i] = 0.f;
-  }
-  const float width = static_cast<float>(a.c);
-  float2 cs, ns;
-  auto fetch = [&](int64_t row, C(&tx)[NCH], C(&td)[NCH], float2& ts) {
-    const bool in = row < a.n;
-    ts = in ? st[row] : make_float2(0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      const int j = k * TPR + l;
-      tx[k] = in && j < chunks ? x[row * chunks + j] : zero;
-      td[k] = in && j < chunks ? dy[row * chunks + j] : zero;
-    }
-  };
+  for (int i = 0; i < N; ++i) dg[i] = db[i] = 0.f;
+  const float inv = 1.f / static_cast<float>(a.c);
+  Row<T, EPC, NCH, TPR, kWhole> cx, cd;
+  float2 cs;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
-  int64_t base = static_cast<int64_t>(blockIdx.x) * kRows;
-  fetch(base + threadIdx.x / TPR, cx, cd, cs);
-  for (; base < a.n; base += step) {
-    const int64_t row = base + threadIdx.x / TPR;
-    fetch(row + step, nx, nd, ns);
+  int64_t base = static_cast<int64_t>(blockIdx.x) * kRows, row = base + threadIdx.x / TPR;
+  const int64_t jump = step * chunks;
+  int64_t at = row * chunks;  // of the row to fetch
+  auto fetch = [&](int64_t r) {
+    cx.load(x + at, l, chunks, r < a.n);
+    cd.load(dy + at, l, chunks, r < a.n);
+    cs = r < a.n ? st[r] : make_float2(0.f, 0.f);
+    at += jump;
+  };
+  dx += row * chunks;
+  if (kAhead) fetch(row);
+  for (; base < a.n; base += step, row += step, dx += jump) {
+    if (!kAhead) fetch(row);
+    cx.values(xh);
+    cd.values(g);
+    const float mean = cs.x, rstd = cs.y;
+    if (kAhead) fetch(row + step);
+    shift_scale(xh, -mean, rstd);
+    float gam[N];  // gamma and beta come from the cache each time: registers are scarcer
+    parameter<T, EPC, NCH, TPR, kWhole>(a.gamma, 1.f, l, chunks, gam);
     // rows and chunks that are not there have dy = 0, so they add nothing
-    float s1 = 0.f, s2 = 0.f;
-    float g[NCH * EPC], xh[NCH * EPC];
+    if (a.act != kActNone) {
+      float z[N];
+      parameter<T, EPC, NCH, TPR, kWhole>(a.beta, 0.f, l, chunks, z);
+      fma_all(xh, gam, z, z);
+      act_slopes<T, N>(z, a.act);
+      mul_all(g, z);
+    }
+    fma_all(g, xh, dg, dg);
 #pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      float fx[EPC], fd[EPC], fg[EPC], fb[EPC];
-      unpack(cx[k], fx);
-      unpack(cd[k], fd);
-      unpack(gam[k], fg);
-      unpack(bet[k], fb);
-#pragma unroll
-      for (int i = 0; i < EPC; ++i) {
-        const int e = k * EPC + i;
-        xh[e] = (fx[i] - cs.x) * cs.y;
-        const float dz = a.act == kActNone ? fd[i] : fd[i] * act_slope<T>(xh[e] * fg[i] + fb[i], a.act);
-        dg[e] += dz * xh[e];
-        db[e] += dz;
-        g[e] = dz * fg[i];
-        s1 += g[e];
-        s2 += g[e] * xh[e];
+    for (int i = 0; i < N; i += (N % 2 ? 1 : 2)) {
+      if constexpr (N % 2 == 0) {
+        const float2 t = add2(make_float2(db[i], db[i + 1]), make_float2(g[i], g[i + 1]));
+        db[i] = t.x;
+        db[i + 1] = t.y;
+      } else {
+        db[i] += g[i];
       }
     }
-    s1 = group_sum<TPR>(s1) / width;
-    s2 = group_sum<TPR>(s2) / width;
+    mul_all(g, gam);
+    const float s1 = group_sum<TPR>(sum_of(g)) * inv;
+    const float s2 = group_sum<TPR>(dot_of(g, xh)) * -inv;
     if (row < a.n) {
+      // (g - s1 - xh * mean(g xh)) * rstd
 #pragma unroll
-      for (int k = 0; k < NCH; ++k) {
-        const int j = k * TPR + l;
-#pragma unroll
-        for (int i = 0; i < EPC; ++i) f[i] = (g[k * EPC + i] - s1 - xh[k * EPC + i] * s2) * cs.y;
-        if (j < chunks) dx[row * chunks + j] = pack<T, EPC>(f);
+      for (int i = 0; i < N; i += (N % 2 ? 1 : 2)) {
+        if constexpr (N % 2 == 0) {
+          const float2 t = fma2(make_float2(xh[i], xh[i + 1]), make_float2(s2, s2), make_float2(g[i], g[i + 1]));
+          g[i] = t.x;
+          g[i + 1] = t.y;
+        } else {
+          g[i] = fmaf(xh[i], s2, g[i]);
+        }
       }
+      shift_scale(g, -s1, rstd);
+      Row<T, EPC, NCH, TPR, kWhole>::store(dx, g, l, chunks);
     }
-#pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      cx[k] = nx[k];
-      cd[k] = nd[k];
-    }
-    cs = ns;
   }
   if (!a.part) return;
-  // the block's channel sums: across the row groups of each warp, then warp
-  // after warp
+  // the block's channel sums: across the row groups of each warp, then over the
+  // warps in order
 #pragma unroll
-  for (int e = 0; e < NCH * EPC; ++e) {
+  for (int e = 0; e < N; ++e) {
 #pragma unroll
     for (int o = TPR; o < 32; o <<= 1) {
       dg[e] += __shfl_xor_sync(0xffffffffu, dg[e], o);
       db[e] += __shfl_xor_sync(0xffffffffu, db[e], o);
     }
   }
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (static_cast<int>(threadIdx.x >> 5) == w && (threadIdx.x & 31) < TPR) {
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.c;
+  const int warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    if (which) __syncthreads();
+    if ((threadIdx.x & 31) < TPR) {
 #pragma unroll
       for (int k = 0; k < NCH; ++k) {
         const int j = k * TPR + l;
         if (j >= chunks) continue;
 #pragma unroll
-        for (int i = 0; i < EPC; ++i) {
-          float* at = s_sum + j * EPC + i;
-          at[0] = (w ? at[0] : 0.f) + dg[k * EPC + i];
-          at[a.c] = (w ? at[a.c] : 0.f) + db[k * EPC + i];
-        }
+        for (int i = 0; i < EPC; ++i) s_sum[warp * a.c + j * EPC + i] = which ? db[k * EPC + i] : dg[k * EPC + i];
       }
     }
     __syncthreads();
+    for (int i = threadIdx.x; i < a.c; i += kThreads) {
+      float t = 0.f;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) t += s_sum[w * a.c + i];
+      part[which * a.c + i] = t;
+    }
   }
-  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.c;
-  for (int i = threadIdx.x; i < 2 * a.c; i += kThreads) part[i] = s_sum[i];
 }
 
 // Rows too long for registers: one block per row, which reads it again for
@@ -332,34 +490,42 @@ __global__ void __launch_bounds__(kThreads) k_layer_norm_long_bwd(const NormArgs
 }
 
 // dgamma[j], dbeta[j] = the partial rows added up in fp64, in a fixed order:
-// 32 channels x 8 runs of partials per block.
+// 32 channels x 32 runs of partials per block, so that the few hundred
+// dependent loads of a channel are spread over 32 warps.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_ln_fold(const float* part, int parts, int c, T* dgamma, T* dbeta) {
-  __shared__ double s_run[8][33];
-  const int j = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
+__global__ void __launch_bounds__(1024) k_ln_fold(const float* part, int parts, int c, T* dgamma, T* dbeta) {
+  __shared__ double s_run[32][33];
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, j = blockIdx.x * 32 + lane;
   double s = 0.0;
   if (j < 2 * c)
 #pragma unroll 8
-    for (int p = run; p < parts; p += 8) s += part[static_cast<int64_t>(p) * 2 * c + j];
-  s_run[run][threadIdx.x & 31] = s;
+    for (int p = run; p < parts; p += 32) s += part[static_cast<int64_t>(p) * 2 * c + j];
+  s_run[run][lane] = s;
   __syncthreads();
-  if (run == 0 && j < 2 * c) {
+  // warp `run` adds up channel `run` of the 32
+  s = s_run[lane][run];
 #pragma unroll
-    for (int r = 1; r < 8; ++r) s += s_run[r][threadIdx.x & 31];
-    T* to = j < c ? dgamma : dbeta;
-    if (to) to[j < c ? j : j - c] = from_f<T>(static_cast<float>(s));
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int jj = blockIdx.x * 32 + run;
+  if (lane == 0 && jj < 2 * c) {
+    T* to = jj < c ? dgamma : dbeta;
+    if (to) to[jj < c ? jj : jj - c] = from_f<T>(static_cast<float>(s));
   }
 }
 
-constexpr int kBlocksPerSm = 4;
 constexpr int kMaxElems = 32;  // elements of a row that one lane holds
 
 template <typename T, int EPC, int NCH, int TPR>
 void launch_one(const NormArgs<T>& a, bool backward, int blocks, cudaStream_t s) {
-  if (backward)
-    k_layer_norm_bwd<T, EPC, NCH, TPR><<<blocks, kThreads, a.part ? 2 * a.c * sizeof(float) : 0, s>>>(a);
-  else
-    k_layer_norm<T, EPC, NCH, TPR><<<blocks, kThreads, 0, s>>>(a);
+  const size_t sums = a.part ? kThreads / 32 * a.c * sizeof(float) : 0;
+  // the common widths (every lane's chunks full) without the checks of the others
+  if (EPC > 1 && a.c == EPC * NCH * TPR) {
+    if (backward) k_layer_norm_bwd<T, EPC, NCH, TPR, (EPC > 1)><<<blocks, kThreads, sums, s>>>(a);
+    else k_layer_norm<T, EPC, NCH, TPR, (EPC > 1)><<<blocks, kThreads, 0, s>>>(a);
+    return;
+  }
+  if (backward) k_layer_norm_bwd<T, EPC, NCH, TPR, false><<<blocks, kThreads, sums, s>>>(a);
+  else k_layer_norm<T, EPC, NCH, TPR, false><<<blocks, kThreads, 0, s>>>(a);
 }
 
 // Lanes per row: as many as it has chunks, up to a warp, then more chunks per
@@ -384,7 +550,7 @@ struct NormPlan {
   int epc, tpr, blocks;  // epc 0: the long-row kernels
 };
 
-NormPlan plan(int64_t n, int c, size_t esz, bool aligned, int sms) {
+NormPlan plan(int64_t n, int c, size_t esz, bool aligned, bool backward, int sms) {
   NormPlan p;
   const int wide = static_cast<int>(16 / esz);
   p.epc = aligned && c % wide == 0 ? wide : 1;
@@ -397,7 +563,9 @@ NormPlan plan(int64_t n, int c, size_t esz, bool aligned, int sms) {
   p.tpr = 1;
   while (p.tpr < 32 && p.tpr * p.epc < c) p.tpr *= 2;
   const int64_t need = (n + kThreads / p.tpr - 1) / (kThreads / p.tpr);
-  p.blocks = static_cast<int>(need < static_cast<int64_t>(kBlocksPerSm) * sms ? need : kBlocksPerSm * sms);
+  const int elems = (c + p.tpr - 1) / p.tpr;
+  const int64_t most = static_cast<int64_t>(backward ? bwd_blocks(elems) : fwd_blocks(elems)) * sms;
+  p.blocks = static_cast<int>(need < most ? need : most);
   return p;
 }
 
@@ -428,7 +596,7 @@ cudaError_t launch_typed(const LayerNormArgs& b, int sms, cudaStream_t s) {
   a.act = b.act;
   a.eps = b.eps;
   const bool backward = b.dy != nullptr;
-  const NormPlan p = plan(b.n, b.c, sizeof(T), aligned_to_chunks(b), sms);
+  const NormPlan p = plan(b.n, b.c, sizeof(T), aligned_to_chunks(b), backward, sms);
   int parts = p.blocks, launches = 1;
   if (p.epc == 0) {
     if (!backward) {
@@ -447,7 +615,7 @@ cudaError_t launch_typed(const LayerNormArgs& b, int sms, cudaStream_t s) {
     launch_width<T, 16 / sizeof(T)>(a, backward, p.blocks, p.tpr, s);
   }
   if (backward && a.part) {
-    k_ln_fold<T><<<(2 * b.c + 31) / 32, kThreads, 0, s>>>(a.part, parts, b.c, a.dgamma, a.dbeta);
+    k_ln_fold<T><<<(2 * b.c + 31) / 32, 1024, 0, s>>>(a.part, parts, b.c, a.dgamma, a.dbeta);
     ++launches;
   }
   count_launches(launches);
@@ -457,7 +625,7 @@ cudaError_t launch_typed(const LayerNormArgs& b, int sms, cudaStream_t s) {
 }  // namespace
 
 int64_t layer_norm_parts(const LayerNormArgs& a, int sms) {
-  const NormPlan p = plan(a.n, a.c, a.dtype == kF32 ? 4 : 2, aligned_to_chunks(a), sms);
+  const NormPlan p = plan(a.n, a.c, a.dtype == kF32 ? 4 : 2, aligned_to_chunks(a), a.dy != nullptr, sms);
   return p.epc == 0 ? (a.n < kLongSlices ? a.n : kLongSlices) : p.blocks;
 }
 

@@ -66,11 +66,19 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const RotArgs<T> a) {
   const int64_t total = a.n * per_row * runs;
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; u < total;
        u += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t rest = u / per_row, row = rest / runs;
+    int64_t rest, row;
+    if (total < (int64_t{1} << 31)) {  // a 64-bit division takes longer than the turn of a chunk
+      rest = static_cast<uint32_t>(u) / static_cast<uint32_t>(per_row);
+      row = static_cast<uint32_t>(rest) / static_cast<uint32_t>(runs);
+    } else {
+      rest = u / per_row;
+      row = rest / runs;
+    }
     const int ch = static_cast<int>(u - rest * per_row), h0 = static_cast<int>(rest - row * runs) * a.run;
     const int h1 = h0 + a.run < a.heads ? h0 + a.run : a.heads;
     const T* x = a.x + row * a.xs_row + h0 * a.xs_head;
     T* y = a.out + row * a.os_row + h0 * a.os_head;
+    const int count = h1 - h0;
     float2 cs[kPairs];
     if constexpr (kHalf) {
       const bool two = ch < paired;
@@ -79,14 +87,16 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const RotArgs<T> a) {
 #pragma unroll
         for (int i = 0; i < EPC; ++i) cs[i] = turn_of(a, row, lo + i);
       }
+      x += lo;
+      y += lo;
 #pragma unroll 2
-      for (int h = h0; h < h1; ++h, x += a.xs_head, y += a.os_head) {
-        const C cu = *reinterpret_cast<const C*>(x + lo);
+      for (int h = 0; h < count; ++h, x += a.xs_head, y += a.os_head) {
+        const C cu = *reinterpret_cast<const C*>(x);
         if (!two) {
-          *reinterpret_cast<C*>(y + lo) = cu;
+          *reinterpret_cast<C*>(y) = cu;
           continue;
         }
-        const C cv = *reinterpret_cast<const C*>(x + lo + pairs);
+        const C cv = *reinterpret_cast<const C*>(x + pairs);
         float fu[EPC], fv[EPC], ru[EPC], rv[EPC];
         unpack(cu, fu);
         unpack(cv, fv);
@@ -95,39 +105,43 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const RotArgs<T> a) {
           ru[i] = fu[i] * cs[i].x - fv[i] * cs[i].y;
           rv[i] = fu[i] * cs[i].y + fv[i] * cs[i].x;
         }
-        *reinterpret_cast<C*>(y + lo) = pack<T, EPC>(ru);
-        *reinterpret_cast<C*>(y + lo + pairs) = pack<T, EPC>(rv);
+        *reinterpret_cast<C*>(y) = pack<T, EPC>(ru);
+        *reinterpret_cast<C*>(y + pairs) = pack<T, EPC>(rv);
+      }
+    } else if constexpr (EPC == 1) {
+      const int lo = ch * kElems;
+      const bool two = lo / 2 < pairs, both = lo + 1 < a.dim;
+      if (two) cs[0] = turn_of(a, row, lo / 2);
+      for (int h = 0; h < count; ++h, x += a.xs_head, y += a.os_head) {
+        const T u0 = x[lo], v0 = both ? x[lo + 1] : u0;
+        const float fu = to_f(u0), fv = to_f(v0);
+        y[lo] = two ? from_f<T>(fu * cs[0].x - fv * cs[0].y) : u0;
+        if (both) y[lo + 1] = two ? from_f<T>(fu * cs[0].y + fv * cs[0].x) : v0;
       }
     } else {
       const int lo = ch * kElems;
 #pragma unroll
       for (int i = 0; i < kPairs; ++i)
         cs[i] = lo / 2 + i < pairs ? turn_of(a, row, lo / 2 + i) : make_float2(1.f, 0.f);
-      if constexpr (EPC == 1) {
-        const bool two = lo / 2 < pairs, both = lo + 1 < a.dim;
-        for (int h = h0; h < h1; ++h, x += a.xs_head, y += a.os_head) {
-          const T u0 = x[lo], v0 = both ? x[lo + 1] : u0;
-          const float fu = to_f(u0), fv = to_f(v0);
-          y[lo] = two ? from_f<T>(fu * cs[0].x - fv * cs[0].y) : u0;
-          if (both) y[lo + 1] = two ? from_f<T>(fu * cs[0].y + fv * cs[0].x) : v0;
-        }
-      } else {
+      x += lo;
+      y += lo;
 #pragma unroll 4
-        for (int h = h0; h < h1; ++h, x += a.xs_head, y += a.os_head) {
-          const C c = *reinterpret_cast<const C*>(x + lo);
-          float f[EPC], r[EPC];
-          unpack(c, f);
+      for (int h = 0; h < count; ++h, x += a.xs_head, y += a.os_head) {
+        const C c = *reinterpret_cast<const C*>(x);
+        float f[EPC], r[EPC];
+        unpack(c, f);
 #pragma unroll
-          for (int i = 0; i < EPC / 2; ++i) {
-            r[2 * i] = f[2 * i] * cs[i].x - f[2 * i + 1] * cs[i].y;
-            r[2 * i + 1] = f[2 * i] * cs[i].y + f[2 * i + 1] * cs[i].x;
-          }
-          C o = pack<T, EPC>(r);
-#pragma unroll
-          for (int i = 0; i < EPC; ++i)  // channels behind the pairs keep their bits
-            if (lo / 2 + i / 2 >= pairs) o.v[i] = c.v[i];
-          *reinterpret_cast<C*>(y + lo) = o;
+        for (int i = 0; i < EPC / 2; ++i) {
+          r[2 * i] = f[2 * i] * cs[i].x - f[2 * i + 1] * cs[i].y;
+          r[2 * i + 1] = f[2 * i] * cs[i].y + f[2 * i + 1] * cs[i].x;
         }
+        C o = pack<T, EPC>(r);
+        if (lo / 2 + EPC / 2 > pairs) {  // channels behind the pairs keep their bits
+#pragma unroll
+          for (int i = 0; i < EPC; ++i)
+            if (lo / 2 + i / 2 >= pairs) o.v[i] = c.v[i];
+        }
+        *reinterpret_cast<C*>(y) = o;
       }
     }
   }
@@ -156,12 +170,16 @@ cudaError_t launch_typed(const RotaryArgs& b, int sms, cudaStream_t s) {
   a.inverse = b.inverse;
   const int pairs = a.axes * a.nfreq;
   auto whole = [&](int64_t v) { return v % kWide == 0; };
-  const bool vec = ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out)) & 15u) == 0 &&
+  // Where one pair and head to a thread does not fill the machine, the angles
+  // (fp64, about 5 us for the eight of a 16-byte chunk) are what takes the time:
+  // one to a thread then.
+  const bool few = a.n * a.heads * a.dim <= static_cast<int64_t>(sms) * 1024;
+  const bool vec = !few && ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out)) & 15u) == 0 &&
                    whole(a.xs_row) && whole(a.xs_head) && whole(a.os_row) && whole(a.os_head) && whole(a.dim) &&
                    (!b.half || whole(pairs));
   const int elems = vec ? kWide : (b.half ? 1 : 2);
   const int64_t per_row = b.half ? pairs / elems + (a.dim - 2 * pairs + elems - 1) / elems : (a.dim + elems - 1) / elems;
-  // A run of heads as long as leaves half the machine's threads busy.
+  // A run of heads as long as leaves a thousand threads on each SM.
   const int64_t fill = static_cast<int64_t>(sms) * 1024;
   int64_t run = a.n * per_row * a.heads / fill;
   run = run < 1 ? 1 : (run > a.heads ? a.heads : run);

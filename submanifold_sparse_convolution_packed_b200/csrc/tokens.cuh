@@ -24,18 +24,86 @@ template <> __device__ __forceinline__ __half from_f<__half>(float x) { return _
 // EPC consecutive elements moved as one access: 16 bytes, or one element.
 template <typename T, int EPC> struct alignas(sizeof(T) * EPC) Chunk { T v[EPC]; };
 
+__device__ __forceinline__ float2 to_f2(__nv_bfloat16 a, __nv_bfloat16 b) {
+  return __bfloat1622float2(__halves2bfloat162(a, b));
+}
+__device__ __forceinline__ float2 to_f2(__half a, __half b) { return __half22float2(__halves2half2(a, b)); }
+
 template <typename T, int EPC>
 __device__ __forceinline__ void unpack(const Chunk<T, EPC>& c, float (&f)[EPC]) {
+  if constexpr (sizeof(T) == 2 && EPC % 2 == 0) {
 #pragma unroll
-  for (int i = 0; i < EPC; ++i) f[i] = to_f(c.v[i]);
+    for (int i = 0; i < EPC; i += 2) {
+      const float2 t = to_f2(c.v[i], c.v[i + 1]);
+      f[i] = t.x;
+      f[i + 1] = t.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPC; ++i) f[i] = to_f(c.v[i]);
+  }
+}
+
+__device__ __forceinline__ void from_f2(float a, float b, __nv_bfloat16* x) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  x[0] = h.x;
+  x[1] = h.y;
+}
+__device__ __forceinline__ void from_f2(float a, float b, __half* x) {
+  const __half2 h = __floats2half2_rn(a, b);
+  x[0] = h.x;
+  x[1] = h.y;
 }
 
 template <typename T, int EPC>
 __device__ __forceinline__ Chunk<T, EPC> pack(const float (&f)[EPC]) {
   Chunk<T, EPC> c;
+  if constexpr (sizeof(T) == 2 && EPC % 2 == 0) {
 #pragma unroll
-  for (int i = 0; i < EPC; ++i) c.v[i] = from_f<T>(f[i]);
+    for (int i = 0; i < EPC; i += 2) from_f2(f[i], f[i + 1], &c.v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPC; ++i) c.v[i] = from_f<T>(f[i]);
+  }
   return c;
+}
+
+// 2^x, within 2 ulp; results below the normal range are zero.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 // Sum over groups of W neighbouring lanes (W a power of two, at most 32).
