@@ -29,11 +29,14 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _device_of(first: torch.Tensor, *others: Optional[torch.Tensor]) -> torch.device:
-    for t in (first, *others):
-        if t is not None and (not t.is_cuda or t.device != first.device):
-            raise ValueError("all tensors must be on one CUDA device")
-    return first.device
+def _device_of(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
+    d = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != d:
+            d = -1
+    if d < 0:
+        raise ValueError("all tensors must be on one CUDA device")
+    return d
 
 
 def _act(act: Optional[str]) -> int:
@@ -68,31 +71,22 @@ def _strides(t: torch.Tensor):
 
 
 class _On:
-    """The device and stream a call runs on, as current ones: the stream then
-    owns the tensors made inside, as the caching allocator needs.  Nothing is
-    switched where nothing differs (a switch takes longer than a launch).
-    Entering gives the stream's handle."""
+    """Makes a device and a stream the current ones: the stream then owns the
+    tensors made inside, as the caching allocator needs.  Calls on the current
+    device and stream go without (a switch takes longer than a launch)."""
 
-    __slots__ = ("device", "stream", "inner")
+    def __init__(self, device: int, stream):
+        self.inner = [torch.cuda.device(device)]
+        if stream is not None:
+            self.inner.append(torch.cuda.stream(stream))
 
-    def __init__(self, device: torch.device, stream):
-        self.device, self.stream, self.inner = device, stream, None
-
-    def __enter__(self) -> int:
-        if self.device.index != _current_device():
-            self.inner = [torch.cuda.device(self.device)]
-            self.inner[0].__enter__()
-        if self.stream is None:
-            return _current_stream(self.device.index)
-        s = torch.cuda.stream(self.stream)
-        s.__enter__()
-        self.inner = (self.inner or []) + [s]
-        return self.stream.cuda_stream
+    def __enter__(self):
+        for c in self.inner:
+            c.__enter__()
 
     def __exit__(self, *error):
-        if self.inner:
-            for c in reversed(self.inner):
-                c.__exit__(*error)
+        for c in reversed(self.inner):
+            c.__exit__(*error)
 
 
 def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
@@ -116,12 +110,15 @@ def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Opti
         if out.data_ptr() == x.data_ptr() and not x.is_contiguous():
             raise ValueError("out may be x only if x is contiguous")
     dev = _device_of(x, gamma, beta, out, stats)
-    with _On(dev, stream) as on:
-        x = x.contiguous()
-        gamma, beta = (None if t is None else t.contiguous() for t in (gamma, beta))
-        out = _result(out, (n, c), x.dtype, dev, "out")
-        _check(lib().smc_layer_norm(_ptr(x), n, c, _ptr(gamma), _ptr(beta), float(eps), a, _ptr(out), _ptr(stats),
-                                    _DTYPES[x.dtype], on), "smc_layer_norm")
+    if stream is not None or dev != _current_device():
+        with _On(dev, stream):
+            return layer_norm(x, gamma, beta, eps, act, out, stats)
+    x = x.contiguous()
+    gamma, beta = gamma if gamma is None else gamma.contiguous(), beta if beta is None else beta.contiguous()
+    if out is None:
+        out = torch.empty_like(x)
+    _check(lib().smc_layer_norm(x.data_ptr(), n, c, _ptr(gamma), _ptr(beta), eps, a, out.data_ptr(), _ptr(stats),
+                                _DTYPES[x.dtype], _current_stream(dev)), "smc_layer_norm")
     return out
 
 
@@ -154,17 +151,20 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, 
         if t is not None:
             _result(t, (c,), x.dtype, x.device, what)
     dev = _device_of(x, dy, stats, gamma, beta, dx, dgamma, dbeta)
-    with _On(dev, stream) as on:
-        dy, x, stats = dy.contiguous(), x.contiguous(), stats.contiguous()
-        gamma, beta = (None if t is None else t.contiguous() for t in (gamma, beta))
-        dx = _result(dx, (n, c), x.dtype, dev, "dx")
-        if gamma is not None or dgamma is not None:
-            dgamma = _result(dgamma, (c,), x.dtype, dev, "dgamma")
-        if beta is not None or dbeta is not None:
-            dbeta = _result(dbeta, (c,), x.dtype, dev, "dbeta")
-        _check(lib().smc_layer_norm_backward(_ptr(dy), _ptr(x), n, c, _ptr(stats), _ptr(gamma), _ptr(beta), a,
-                                             _ptr(dx), _ptr(dgamma), _ptr(dbeta), _DTYPES[x.dtype], on),
-               "smc_layer_norm_backward")
+    if stream is not None or dev != _current_device():
+        with _On(dev, stream):
+            return layer_norm_backward(dy, x, stats, gamma, beta, act, dx, dgamma, dbeta)
+    dy, x, stats = dy.contiguous(), x.contiguous(), stats.contiguous()
+    gamma, beta = gamma if gamma is None else gamma.contiguous(), beta if beta is None else beta.contiguous()
+    if dx is None:
+        dx = torch.empty_like(x)
+    if dgamma is None and gamma is not None:
+        dgamma = torch.empty_like(gamma)
+    if dbeta is None and beta is not None:
+        dbeta = torch.empty_like(beta)
+    _check(lib().smc_layer_norm_backward(dy.data_ptr(), x.data_ptr(), n, c, stats.data_ptr(), _ptr(gamma), _ptr(beta),
+                                         a, dx.data_ptr(), _ptr(dgamma), _ptr(dbeta), _DTYPES[x.dtype],
+                                         _current_stream(dev)), "smc_layer_norm_backward")
     return dx, dgamma, dbeta
 
 
@@ -229,13 +229,19 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, layout
         if out.data_ptr() == x.data_ptr() and d > 1 and x.stride(-1) != 1:
             raise ValueError("out may be x only if x is dense along its last axis")
     dev = _device_of(x, positions, freqs, out)
-    with _On(dev, stream) as on:
-        x, freqs = _last_dense(x), freqs.contiguous()
-        out = _result(out, (n, h, d), x.dtype, dev, "out", dense=False)
-        _check(lib().smc_rotary(_ptr(x), _strides(x), n, h, d, _ptr(positions), _strides(positions), _ptr(freqs),
-                                freqs.shape[0], freqs.shape[1], ROTARY_LAYOUTS[layout], float(scale),
-                                1 if inverse else 0, _ptr(out), _strides(out), _DTYPES[x.dtype], on),
-               "smc_rotary")
+    if stream is not None or dev != _current_device():
+        with _On(dev, stream):
+            return rotary(x, positions, freqs, layout, scale, inverse, out)
+    x, freqs = _last_dense(x), freqs.contiguous()
+    out_stride = None  # dense
+    if out is None:
+        out = torch.empty((n, h, d), dtype=x.dtype, device=x.device)
+    else:
+        out_stride = _strides(out)
+    axes, f = freqs.shape
+    _check(lib().smc_rotary(x.data_ptr(), _strides(x), n, h, d, positions.data_ptr(), _strides(positions),
+                            freqs.data_ptr(), axes, f, ROTARY_LAYOUTS[layout], scale, 1 if inverse else 0,
+                            out.data_ptr(), out_stride, _DTYPES[x.dtype], _current_stream(dev)), "smc_rotary")
     return out
 
 
@@ -283,14 +289,18 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.
     if lse is not None:
         _result(lse, (n, h), torch.float32, q.device, "lse")
     dev = _device_of(q, k, v, offsets, k_offsets, out, lse)
-    with _On(dev, stream) as on:
-        q, k, v = _last_dense(q), _last_dense(k), _last_dense(v)
-        offsets, k_offsets = offsets.contiguous(), k_offsets.contiguous()
-        out = _result(out, (n, h, d), q.dtype, dev, "out")
-        _check(lib().smc_attention(_ptr(q), _strides(q), _ptr(k), _strides(k), _ptr(v), _strides(v), _ptr(offsets),
-                                   _ptr(k_offsets), offsets.shape[0] - 1, n, k.shape[0], h, k.shape[1], d, scale,
-                                   1 if causal else 0, _ptr(out), _ptr(lse), _DTYPES[q.dtype], on),
-               "smc_attention")
+    if stream is not None or dev != _current_device():
+        with _On(dev, stream):
+            return attention(q, k, v, offsets, k_offsets, scale, causal, out, lse)
+    q, k, v = _last_dense(q), _last_dense(k), _last_dense(v)
+    offsets, k_offsets = offsets.contiguous(), k_offsets.contiguous()
+    if out is None:
+        out = torch.empty((n, h, d), dtype=q.dtype, device=q.device)
+    m, hk, _ = k.shape
+    _check(lib().smc_attention(q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), v.data_ptr(), _strides(v),
+                               offsets.data_ptr(), k_offsets.data_ptr(), offsets.shape[0] - 1, n, m, h, hk, d, scale,
+                               1 if causal else 0, out.data_ptr(), _ptr(lse), _DTYPES[q.dtype], _current_stream(dev)),
+           "smc_attention")
     return out
 
 
@@ -315,15 +325,22 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
         if t is not None:
             _result(t, shape, q.dtype, q.device, what, dense=False)
     dev = _device_of(q, k, v, dout, out, lse, offsets, k_offsets, dq, dk, dv)
-    with _On(dev, stream) as on:
-        q, k, v, dout = _last_dense(q), _last_dense(k), _last_dense(v), _last_dense(dout)
-        out, lse = out.contiguous(), lse.contiguous()
-        offsets, k_offsets = offsets.contiguous(), k_offsets.contiguous()
-        dq, dk, dv = (_result(t, shape, q.dtype, dev, what, dense=False) for t, shape, what in shapes)
-        _check(lib().smc_attention_backward(_ptr(dout), _strides(dout), _ptr(q), _strides(q), _ptr(k), _strides(k),
-                                            _ptr(v), _strides(v), _ptr(out), _ptr(lse), _ptr(offsets),
-                                            _ptr(k_offsets), offsets.shape[0] - 1, n, m, h, hk, d, scale,
-                                            1 if causal else 0, _ptr(dq), _strides(dq), _ptr(dk), _strides(dk),
-                                            _ptr(dv), _strides(dv), _DTYPES[q.dtype], on),
-               "smc_attention_backward")
+    if stream is not None or dev != _current_device():
+        with _On(dev, stream):
+            return attention_backward(dout, q, k, v, out, lse, offsets, k_offsets, scale, causal, dq, dk, dv)
+    q, k, v, dout = _last_dense(q), _last_dense(k), _last_dense(v), _last_dense(dout)
+    out, lse = out.contiguous(), lse.contiguous()
+    offsets, k_offsets = offsets.contiguous(), k_offsets.contiguous()
+    if dq is None:
+        dq = torch.empty((n, h, d), dtype=q.dtype, device=q.device)
+    if dk is None:
+        dk = torch.empty((m, hk, d), dtype=q.dtype, device=q.device)
+    if dv is None:
+        dv = torch.empty((m, hk, d), dtype=q.dtype, device=q.device)
+    _check(lib().smc_attention_backward(dout.data_ptr(), _strides(dout), q.data_ptr(), _strides(q), k.data_ptr(),
+                                        _strides(k), v.data_ptr(), _strides(v), out.data_ptr(), lse.data_ptr(),
+                                        offsets.data_ptr(), k_offsets.data_ptr(), offsets.shape[0] - 1, n, m, h, hk,
+                                        d, scale, 1 if causal else 0, dq.data_ptr(), _strides(dq), dk.data_ptr(),
+                                        _strides(dk), dv.data_ptr(), _strides(dv), _DTYPES[q.dtype],
+                                        _current_stream(dev)), "smc_attention_backward")
     return dq, dk, dv

@@ -2,21 +2,24 @@
 //
 //   S = scale Q K^T,  P = exp2(S log2e - top),  O = sum P V / sum P
 //
-// One CTA holds two tiles of 128 packed rows (row = query * G + head of the
-// group, so the heads that share keys share the tile) of one key/value head
-// against a run of the item's keys, 128 at a time:
-//   warp 9     TMA: both Q tiles once, then K and V tiles into a ring;
-//   warp 8     tcgen05.mma: S = Q K^T (both from shared memory), then
-//              O += P V with P in TMEM and V read MN-major as it lies;
-//   warps 0-3, 4-7  the softmax of the first and second tile: one thread per
-//              row, 128 scores in registers, running maximum and sum in fp32,
-//              P rounded to the input type into the columns its scores came
-//              from.
+// One CTA holds kTiles (1 or 2) tiles of 128 packed rows (row = query * G +
+// head of the group, so the heads that share keys share the tile) of one
+// key/value head against a run of the item's keys, 128 at a time.  Its warps:
+//   softmax    four for each tile and, up to 64 channels, for each half of a
+//              step's columns: one thread per row, its scores in registers,
+//              running maximum and sum in fp32, P rounded to the input type
+//              into the TMEM columns its scores came from;
+//   MMA        S = Q K^T (both from shared memory), then O += P V with P in
+//              TMEM and V read MN-major as it lies;
+//   TMA        the Q tiles once, then K and V tiles into a ring.
 // While one tile's scores are exponentiated, the tensor cores work on the
-// other tile.  The accumulator is rescaled in TMEM only when a row's maximum
-// has grown by more than 2^8 (P stays below 256, far inside fp16's range);
-// the sums use the unrounded P.  Keys behind the item's end are masked, and V
-// rows there are zeroed in shared memory, since P = 0 does not undo a NaN.
+// other tile (or the other CTA of the SM: one-tile CTAs run two to an SM).
+// The two halves of a step keep maxima, sums and accumulators of their own
+// (TMEM has the room), so a row's two threads meet only at the end.
+// An accumulator is rescaled in TMEM only when a row's maximum has grown by
+// more than 2^8 (P stays below 256, far inside fp16's range); the sums use the
+// unrounded P.  Keys behind the item's end are masked, and V rows there are
+// zeroed in shared memory, since P = 0 does not undo a NaN.
 // With few queries over many keys the keys are split between CTAs; each writes
 // its unnormalised fp32 O, maximum and sum, and k_attn_join adds them up in
 // order.
@@ -30,12 +33,13 @@ namespace {
 
 using namespace attn;
 
-constexpr int kFwdThreads = 320;
+constexpr int kShortItem = 512;  // packed rows
 
 struct FwdParams {
   const int32_t *q_off, *k_off;
   int64_t n, m;
   int items, heads, kv_heads, dim, group, qpt;  // qpt: queries of a tile
+  int per_unit;                                  // queries of a CTA
   int chunk;                                     // keys of a split (0: no split)
   int slot_rows;                                 // rows of a split's partial results
   float c;                                       // scale * log2 e
@@ -47,20 +51,29 @@ struct FwdParams {
   uint64_t wait_ns;
 };
 
-template <int DP> struct FwdLayout {
+template <int DP, int kTiles> struct FwdLayout {
   static constexpr uint32_t kTileBytes = DP / 64 * kPanel;
-  static constexpr int kSlots = DP == 64 ? 8 : 4;
-  static constexpr uint32_t kQ = 0, kKv = 2 * kTileBytes, kBar = kKv + kSlots * kTileBytes;
-  // barriers: q, kv full[kSlots], kv empty[kSlots], s full[2], p ready[2], o done[2], tail
-  static constexpr uint32_t kMisc = kBar + 8 * (2 * kSlots + 8), kTotal = kMisc + 32 + 1024;
+  // one-tile CTAs leave room for a second one on the SM
+  static constexpr int kSlots = (DP == 64 ? 4 : 2) * kTiles;
+  static constexpr int kHalves = DP == 64 ? 2 : 1, kGroups = kTiles * kHalves;
+  static constexpr int kThreads = 128 * kGroups + 64;
+  static constexpr uint32_t kQ = 0, kKv = kTiles * kTileBytes, kBar = kKv + kSlots * kTileBytes;
+  // barriers: q, kv full[kSlots], kv empty[kSlots], s full[kTiles], p ready[kGroups], o done[kTiles], tail
+  static constexpr uint32_t kMisc = kBar + 8 * (2 * kSlots + 2 * kTiles + kGroups + 2);
+  static constexpr uint32_t kMl = (kMisc + 16 + 15) / 16 * 16;  // (maximum, sum) of each row and half
+  static constexpr uint32_t kTotal = kMl + kGroups * kRows * 8 + 1024;
+  // TMEM columns: S of the tiles, then O of the tiles' halves
+  static constexpr uint32_t kO = kTiles * kRows, kColumns = kTiles == 2 ? 512 : 256;
+  static_assert(kO + kGroups * DP <= kColumns, "accumulators fit");
 };
 
-template <typename T, int DP>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+template <typename T, int DP, int kTiles>
+__global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
     k_attn_fwd_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const FwdParams p) {
-  using L = FwdLayout<DP>;
-  constexpr int kSlots = L::kSlots, kPanels = DP / 64;
+  using L = FwdLayout<DP, kTiles>;
+  constexpr int kSlots = L::kSlots, kPanels = DP / 64, kHalves = L::kHalves, kCols = kRows / kHalves;
+  constexpr int kMmaWarp = 4 * L::kGroups, kTmaWarp = kMmaWarp + 1;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Unit s_unit;
@@ -68,30 +81,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   uint8_t* smem = smem_raw + (sbase - raw);
   volatile uint32_t* s_misc = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);  // [0] tmem
   const uint32_t bar_q = sbase + L::kBar, bar_full = bar_q + 8, bar_empty = bar_full + 8 * kSlots;
-  const uint32_t bar_s = bar_empty + 8 * kSlots, bar_p = bar_s + 16, bar_o = bar_p + 16;
-  const uint32_t bar_tail = bar_o + 16;
+  const uint32_t bar_s = bar_empty + 8 * kSlots, bar_p = bar_s + 8 * kTiles, bar_o = bar_p + 8 * L::kGroups;
+  const uint32_t bar_tail = bar_o + 8 * kTiles;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // causal: the tiles with the most keys come last in an item and start first
   const int64_t ux = p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-  find_unit<kFwdThreads>(p.q_off, p.k_off, p.items, p.n, p.m, 2 * p.qpt, p.chunk, false, ux, &s_unit, p.err);
+  find_unit<L::kThreads>(p.q_off, p.k_off, p.items, p.n, p.m, kTiles * p.qpt, p.chunk, false, ux, &s_unit, p.err);
   if (s_unit.item < 0) return;
   const Unit u = s_unit;
   const int hk = blockIdx.y;
-  const int32_t q0 = u.tile * 2 * p.qpt;
+  const int32_t q0 = u.tile * kTiles * p.qpt;
   const int32_t left = u.q.count - q0;
   const int32_t k_lo = u.split * p.chunk;
   const int32_t k_hi = u.splits > 1 && u.k.count - k_lo > p.chunk ? k_lo + p.chunk : u.k.count;
-  int queries[2], steps[2];
+  int queries[kTiles], steps[kTiles];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  for (int t = 0; t < kTiles; ++t) {
     const int32_t rest = left - t * p.qpt;
     queries[t] = rest < 0 ? 0 : (rest < p.qpt ? rest : p.qpt);
     const int32_t seen = queries[t] > 0 ? keys_seen(u, q0 + t * p.qpt + queries[t] - 1, p.causal) : 0;
     const int32_t hi = seen < k_hi ? seen : k_hi;
     steps[t] = hi > k_lo ? (hi - k_lo + kRows - 1) / kRows : 0;
   }
-  const int nsteps = steps[0] > steps[1] ? steps[0] : steps[1];
+  const int nsteps = kTiles == 2 && steps[kTiles - 1] > steps[0] ? steps[kTiles - 1] : steps[0];
 
   if (tid == 0) {
     prefetch_tmap(&qmap);
@@ -102,17 +115,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
     }
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < kTiles; ++t) {
       mbar_init(bar_s + 8 * t, 1);
-      mbar_init(bar_p + 8 * t, 4);
       mbar_init(bar_o + 8 * t, 1);
     }
+    for (int g = 0; g < L::kGroups; ++g) mbar_init(bar_p + 8 * g, 4);
     mbar_init(bar_tail, 1);
     fence_mbarrier_init();
     fence_proxy_async_smem();
   }
-  if (warp == 8) {
-    tmem_alloc(smem_u32(const_cast<uint32_t*>(&s_misc[0])), 512);
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(const_cast<uint32_t*>(&s_misc[0])), L::kColumns);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -120,12 +133,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_misc[0];
 
-  if (warp == 9) {
+  if (warp == kTmaWarp) {
     // ------------------------------------------------------------- TMA loads
     // 2 * nsteps tiles in the order they are used: K0 V0 K1 V1 ...
     if (nsteps > 0) {
       if (elect_one()) {
-        const int tiles = queries[1] > 0 ? 2 : 1;
+        const int tiles = kTiles == 2 && queries[kTiles - 1] > 0 ? 2 : 1;
         mbar_arrive_expect_tx(bar_q, static_cast<uint32_t>(tiles * kPanels * p.group * p.qpt) * 128u);
         for (int t = 0; t < tiles; ++t)
           for (int c = 0; c < kPanels; ++c)
@@ -162,7 +175,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------- MMA issue
     // The whole warp runs the loop; one elected lane issues each batch, with
     // the descriptors advanced by additions only (computing them anew made
@@ -192,27 +205,33 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     };
     bool ok = nsteps > 0 && wait(bar_q, 0) && wait(bar_full, 0);
     if (ok) {
-      if (steps[0] > 0) scores(0, kd);
-      if (steps[1] > 0) scores(1, kd);
+      for (int t = 0; t < kTiles; ++t)
+        if (steps[t] > 0) scores(t, kd);
       if (kSlots < 2 * nsteps) umma_commit_elect(bar_empty);
     }
     int sv = 1, sk = 2 % kSlots;  // slots of V of this step, of K of the next
-    uint32_t pv = 0, pk = 0;
+    uint32_t pv = 0, pk = kSlots == 2 ? 1 : 0;
     for (int j = 0; j < nsteps && ok; ++j) {
       bool next = false;  // K of the next step awaited
       ok = wait(bar_full + 8 * sv, pv);
       const uint64_t v0 = vd + sv * kTile, k0 = kd + sk * kTile;
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (j >= steps[t]) continue;
-        ok = wait(bar_p + 8 * t, j & 1);
-        if (!ok) break;
-        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kRows / 16; ++k)
-            umma_f16_ts(tmem + 2 * kRows + t * DP, tmem + t * kRows + k * 8, v0 + 128 * k, idesc_o, j > 0 || k > 0);
-          if (j + 1 == steps[t]) umma_commit(bar_o + 8 * t);
+      for (int t = 0; t < kTiles; ++t) {
+        if (j >= steps[t] || !ok) continue;
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+          const int g = t * kHalves + h;
+          ok = ok && wait(bar_p + 8 * g, j & 1);
+          if (ok && elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kCols / 16; ++k)
+              umma_f16_ts(tmem + L::kO + g * DP, tmem + t * kRows + h * kCols + k * 8, v0 + 128 * (h * kCols / 16 + k),
+                          idesc_o, j > 0 || k > 0);
+            if (h + 1 == kHalves && j + 1 == steps[t]) umma_commit(bar_o + 8 * t);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (!ok) continue;
         if (j + 1 < steps[t]) {
           ok = next || wait(bar_full + 8 * sk, pk);
           next = true;
@@ -234,118 +253,140 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
   } else {
     // --------------------------------------------------------------- softmax
-    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
+    const int g = warp >> 2, t = g / kHalves, h = g % kHalves, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + t * kRows, to = tmem + lanes + 2 * kRows + t * DP;
+    const uint32_t ts = tmem + lanes + t * kRows + h * kCols, to = tmem + lanes + L::kO + g * DP;
     const int32_t qi = r / p.group;  // query in the tile
     const bool row = qi < queries[t];
+    const bool used = __any_sync(0xffffffffu, row);  // a warp without rows only keeps step
     int32_t lim = row ? keys_seen(u, q0 + t * p.qpt + qi, p.causal) : 0;  // keys [0, lim) are seen
-    lim = lim < k_hi ? lim : k_hi;
+    lim = (lim < k_hi ? lim : k_hi) - k_lo - h * kCols;
     float top = -INFINITY, sum = 0.f;  // top: the rounded product with c the sums refer to
     bool ok = true;
     for (int j = 0; j < steps[t]; ++j) {
       ok = __all_sync(0xffffffffu, mbar_wait_short(bar_s + 8 * t, j & 1, p.err, p.wait_ns));
       if (!ok) break;
       tc_fence_after();
-      float x[kRows];
-      tmem_ld(ts, x);
-      const int32_t seen = lim - (k_lo + j * kRows);
-      if (__any_sync(0xffffffffu, seen < kRows)) {
+      if (used) {
+        float x[kCols];
+        tmem_ld(ts, x);
+        const int32_t seen = lim - j * kRows;
+        if (__any_sync(0xffffffffu, seen < kCols)) {
 #pragma unroll
-        for (int i = 0; i < kRows; ++i)
-          if (i >= seen) x[i] = -INFINITY;
-      }
-      float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
-#pragma unroll
-      for (int i = 4; i < kRows; i += 4) {
-        m0 = fmaxf(m0, x[i]);
-        m1 = fmaxf(m1, x[i + 1]);
-        m2 = fmaxf(m2, x[i + 2]);
-        m3 = fmaxf(m3, x[i + 3]);
-      }
-      const float m = __fmul_rn(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), p.c);
-      const bool grown = m > top + 8.f || (top == -INFINITY && m > -INFINITY);
-      if (__any_sync(0xffffffffu, grown)) {
-        const float keep = grown ? exp2_fast(top - m) : 1.f;
-        if (grown) {
-          sum *= keep;
-          top = m;
+          for (int i = 0; i < kCols; ++i)
+            if (i >= seen) x[i] = -INFINITY;
         }
-        if (j > 0) {  // this tile's products so far are complete: its scores came after them
-          for (int c0 = 0; c0 < DP; c0 += 32) {
-            float o[32];
-            uint32_t b[32];
-            tmem_ld(to + c0, o);
+        float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) b[i] = __float_as_uint(o[i] * keep);
-            tmem_st(to + c0, b);
+        for (int i = 4; i < kCols; i += 4) {
+          m0 = fmaxf(m0, x[i]);
+          m1 = fmaxf(m1, x[i + 1]);
+          m2 = fmaxf(m2, x[i + 2]);
+          m3 = fmaxf(m3, x[i + 3]);
+        }
+        const float m = __fmul_rn(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), p.c);
+        const bool grown = m > top + 8.f || (top == -INFINITY && m > -INFINITY);
+        if (__any_sync(0xffffffffu, grown)) {
+          const float keep = grown ? exp2_fast(top - m) : 1.f;
+          if (grown) {
+            sum *= keep;
+            top = m;
+          }
+          if (j > 0) {  // the products so far are complete: these scores came after them
+#pragma unroll 1
+            for (int c0 = 0; c0 < DP; c0 += 16) {
+              float o[16];
+              uint32_t b[16];
+              tmem_ld(to + c0, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) b[i] = __float_as_uint(o[i] * keep);
+              tmem_st(to + c0, b);
+            }
           }
         }
-      }
-      const float base = top == -INFINITY ? 0.f : top;
-      float2 sa = make_float2(0.f, 0.f), sb = sa;
-      const float2 c2 = make_float2(p.c, p.c), b2 = make_float2(-base, -base);
+        const float base = top == -INFINITY ? 0.f : top;
+        float2 sa = make_float2(0.f, 0.f), sb = sa;
+        const float2 c2 = make_float2(p.c, p.c), b2 = make_float2(-base, -base);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t w[32];
+        for (int q = 0; q < kCols / 64; ++q) {
+          uint32_t w[32];
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const int e = h * 64 + 2 * i;
-          const float2 y0 = fma2(make_float2(x[e], x[e + 1]), c2, b2), y1 = fma2(make_float2(x[e + 2], x[e + 3]), c2, b2);
-          const float2 e0 = make_float2(exp2_fast(y0.x), exp2_fast(y0.y)), e1 = make_float2(exp2_fast(y1.x), exp2_fast(y1.y));
-          sa = add2(sa, e0);
-          sb = add2(sb, e1);
-          w[i] = pack2<T>(e0.x, e0.y);
-          w[i + 1] = pack2<T>(e1.x, e1.y);
+          for (int i = 0; i < 32; i += 2) {
+            const int e = q * 64 + 2 * i;
+            const float2 y0 = fma2(make_float2(x[e], x[e + 1]), c2, b2), y1 = fma2(make_float2(x[e + 2], x[e + 3]), c2, b2);
+            const float2 e0 = make_float2(exp2_fast(y0.x), exp2_fast(y0.y)), e1 = make_float2(exp2_fast(y1.x), exp2_fast(y1.y));
+            sa = add2(sa, e0);
+            sb = add2(sb, e1);
+            w[i] = pack2<T>(e0.x, e0.y);
+            w[i + 1] = pack2<T>(e1.x, e1.y);
+          }
+          tmem_st(ts + q * 32, w);
         }
-        tmem_st(ts + h * 32, w);
+        sum += (sa.x + sa.y) + (sb.x + sb.y);
+        tmem_st_wait();
+        tc_fence_before();
       }
-      sum += (sa.x + sa.y) + (sb.x + sb.y);
-      tmem_st_wait();
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_p + 8 * t);
+      if (lane == 0) mbar_arrive(bar_p + 8 * g);
       __syncwarp();
     }
     // --------------------------------------------------------------- results
+    float2* s_ml = reinterpret_cast<float2*>(smem + L::kMl);
+    float weight = 1.f, weight2 = 0.f;  // of this half's accumulator, and the other's
+    if (kHalves == 2) {
+      s_ml[g * kRows + r] = make_float2(top, sum);
+      asm volatile("bar.sync %0, 256;" ::"r"(1 + t) : "memory");  // the tile's two groups
+      const float2 other = s_ml[(g ^ 1) * kRows + r];
+      const float m = fmaxf(top, other.x);
+      weight = top == -INFINITY ? 0.f : exp2_fast(top - m);
+      weight2 = other.x == -INFINITY ? 0.f : exp2_fast(other.x - m);
+      sum = sum * weight + other.y * weight2;
+      top = m;
+    }
     if (ok && steps[t] > 0) {
       ok = __all_sync(0xffffffffu, mbar_wait_short(bar_o + 8 * t, 0, p.err, p.wait_ns));
       tc_fence_after();
     }
-    if (ok) {
+    if (ok && used) {
       const int64_t at = static_cast<int64_t>(u.q.begin + q0 + t * p.qpt + qi) * p.heads + hk * p.group + r % p.group;
       const bool split = p.part_o != nullptr;
-      const int64_t slot =
-          (ux * p.kv_heads + hk) * p.slot_rows + t * p.qpt * p.group + r;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const int64_t slot = (ux * p.kv_heads + hk) * p.slot_rows + t * p.qpt * p.group + r;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum, f1 = split ? weight : weight * inv, f2 = split ? weight2 : weight2 * inv;
+      const uint32_t to2 = tmem + lanes + L::kO + (g ^ 1) * DP;
 #pragma unroll 1
-      for (int c0 = 0; c0 < DP; c0 += 32) {
+      for (int c0 = h * (DP / kHalves); c0 < (h + 1) * (DP / kHalves); c0 += 32) {
         if (c0 >= p.dim) break;
         float o[32];
         if (steps[t] > 0) {
           tmem_ld(to + c0, o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= f1;
+          if (kHalves == 2) {
+            float o2[32];
+            tmem_ld(to2 + c0, o2);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = fmaf(o2[i], f2, o[i]);
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
         }
-        if (!row) {
-          // nothing to store; the warp reads TMEM together
-        } else if (split) {
+        if (row && split) {
           float4* d = reinterpret_cast<float4*>(p.part_o + slot * p.dim + c0);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (c0 + 4 * i < p.dim) d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        } else {
+        } else if (row) {
           uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * p.dim + c0);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (c0 + 8 * i < p.dim)
-              d[i] = make_uint4(pack2<T>(o[8 * i] * inv, o[8 * i + 1] * inv), pack2<T>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                pack2<T>(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack2<T>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+              d[i] = make_uint4(pack2<T>(o[8 * i], o[8 * i + 1]), pack2<T>(o[8 * i + 2], o[8 * i + 3]),
+                                pack2<T>(o[8 * i + 4], o[8 * i + 5]), pack2<T>(o[8 * i + 6], o[8 * i + 7]));
         }
         __syncwarp();
       }
-      if (row) {
+      if (row && h == 0) {
         if (split) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(top, sum);
         else if (p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
       }
@@ -353,19 +394,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, L::kColumns);
 }
 
 // Joins the splits of one tile, in order: O = sum 2^(top_s - top) O_s / sum ...
 template <typename T>
 __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p) {
   __shared__ Unit s_unit;
-  find_unit<256>(p.q_off, p.k_off, p.items, p.n, p.m, 2 * p.qpt, p.chunk, false, blockIdx.x, &s_unit, p.err);
+  find_unit<256>(p.q_off, p.k_off, p.items, p.n, p.m, p.per_unit, p.chunk, false, blockIdx.x, &s_unit, p.err);
   const Unit u = s_unit;
   if (u.item < 0 || u.split != 0) return;
   const int hk = blockIdx.y, lane = threadIdx.x & 31;
-  const int32_t q0 = u.tile * 2 * p.qpt;
-  const int32_t queries = u.q.count - q0 < 2 * p.qpt ? u.q.count - q0 : 2 * p.qpt;
+  const int32_t q0 = u.tile * p.per_unit;
+  const int32_t queries = u.q.count - q0 < p.per_unit ? u.q.count - q0 : p.per_unit;
   for (int r = threadIdx.x >> 5; r < queries * p.group; r += 8) {
     const int64_t first = (static_cast<int64_t>(blockIdx.x) * p.kv_heads + hk) * p.slot_rows + r;
     const int64_t step = static_cast<int64_t>(p.kv_heads) * p.slot_rows;
@@ -394,20 +435,26 @@ __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p) {
   }
 }
 
-struct SplitPlan {
+struct FwdPlan {
+  int tiles;      // tiles of a CTA
   int64_t units;  // blocks along x
   int chunk, slot_rows;
 };
 
-// Splits the keys when the tiles alone leave more than half of the SMs idle:
-// into runs of about (keys x tiles) / (2 x SMs), at least 256 keys.
-SplitPlan split_plan(const AttnArgs& a, int sms) {
-  const int group = a.heads / a.kv_heads, per = 2 * (kRows / group);
-  const int64_t tiles = a.n / per + a.items;  // upper bound
-  SplitPlan s = {tiles, 0, 0};
-  if (2 * tiles * a.kv_heads > sms) return s;
+// One tile to a CTA where items are short on average: such a CTA's start and
+// end are most of its life, and two of them share an SM.  Keys are split when
+// the tiles alone leave half of the CTA slots idle: into runs of about
+// (keys x tiles) / slots, at least 256 keys.
+FwdPlan fwd_plan(const AttnArgs& a, int sms) {
+  const int group = a.heads / a.kv_heads, qpt = kRows / group;
+  FwdPlan s = {};
+  s.tiles = a.n <= a.items * static_cast<int64_t>(kShortItem / kRows * qpt) ? 1 : 2;
+  const int per = s.tiles * qpt;
+  const int64_t tiles = a.n / per + a.items, slots = static_cast<int64_t>(sms) * (3 - s.tiles);
+  s.units = tiles;
+  if (2 * tiles * a.kv_heads > slots) return s;
   const int64_t most = a.n / per + 1;  // tiles of one item, upper bound
-  int64_t chunk = a.m * most * a.kv_heads / (2 * sms);
+  int64_t chunk = a.m * most * a.kv_heads / slots;
   chunk = (chunk < 256 ? 256 : chunk + kRows - 1) / kRows * kRows;
   if (a.m <= chunk) return s;  // no item is longer than one run
   s.chunk = static_cast<int>(chunk);
@@ -417,18 +464,25 @@ SplitPlan split_plan(const AttnArgs& a, int sms) {
   return s;
 }
 
-template <typename T, int DP>
-cudaError_t launch_fwd(const AttnArgs& a, const FwdParams& p, const SplitPlan& s, const CUtensorMap& qm,
-                       const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
-  auto kern = k_attn_fwd_tc<T, DP>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(FwdLayout<DP>::kTotal));
+template <typename T, int DP, int kTiles>
+cudaError_t launch_tiles(const AttnArgs& a, const FwdParams& p, const FwdPlan& s, const CUtensorMap* maps,
+                         cudaStream_t st) {
+  using L = FwdLayout<DP, kTiles>;
+  auto kern = k_attn_fwd_tc<T, DP, kTiles>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L::kTotal));
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(s.units), a.kv_heads);
-  kern<<<grid, kFwdThreads, FwdLayout<DP>::kTotal, st>>>(qm, km, vm, p);
+  kern<<<grid, L::kThreads, L::kTotal, st>>>(maps[0], maps[1], maps[2], p);
   if (s.chunk) k_attn_join<T><<<grid, 256, 0, st>>>(p);
   count_launches(s.chunk ? 2 : 1);
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_fwd(const AttnArgs& a, const FwdParams& p, const FwdPlan& s, const CUtensorMap* maps,
+                       cudaStream_t st) {
+  if (a.dim <= 64) return s.tiles == 1 ? launch_tiles<T, 64, 1>(a, p, s, maps, st) : launch_tiles<T, 64, 2>(a, p, s, maps, st);
+  return s.tiles == 1 ? launch_tiles<T, 128, 1>(a, p, s, maps, st) : launch_tiles<T, 128, 2>(a, p, s, maps, st);
 }
 
 }  // namespace
@@ -439,17 +493,17 @@ bool attn_tc_supported(const AttnArgs& a) {
 }
 
 int64_t attn_tc_scratch(const AttnArgs& a, int sms) {
-  const SplitPlan s = split_plan(a, sms);
+  const FwdPlan s = fwd_plan(a, sms);
   return s.chunk ? s.units * a.kv_heads * s.slot_rows * (a.dim + 2) * static_cast<int64_t>(sizeof(float)) : 0;
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, void* scratch, int sms, cudaStream_t st) {
   const int group = a.heads / a.kv_heads, qpt = kRows / group;
-  const SplitPlan s = split_plan(a, sms);
-  CUtensorMap qm, km, vm;
-  if (!make_map(&qm, a.q, a.dtype, a.n, a.heads, a.dim, a.q_stride, group, qpt) ||
-      !make_map(&km, a.k, a.dtype, a.m, a.kv_heads, a.dim, a.k_stride, 1, kRows) ||
-      !make_map(&vm, a.v, a.dtype, a.m, a.kv_heads, a.dim, a.v_stride, 1, kRows))
+  const FwdPlan s = fwd_plan(a, sms);
+  CUtensorMap maps[3];
+  if (!make_map(&maps[0], a.q, a.dtype, a.n, a.heads, a.dim, a.q_stride, group, qpt) ||
+      !make_map(&maps[1], a.k, a.dtype, a.m, a.kv_heads, a.dim, a.k_stride, 1, kRows) ||
+      !make_map(&maps[2], a.v, a.dtype, a.m, a.kv_heads, a.dim, a.v_stride, 1, kRows))
     return cudaErrorInvalidValue;
   FwdParams p = {};
   p.q_off = a.q_off;
@@ -462,6 +516,7 @@ cudaError_t launch_attn_tc(const AttnArgs& a, void* scratch, int sms, cudaStream
   p.dim = a.dim;
   p.group = group;
   p.qpt = qpt;
+  p.per_unit = s.tiles * qpt;
   p.chunk = s.chunk;
   p.slot_rows = s.slot_rows;
   p.c = a.scale * kLog2e;
@@ -475,10 +530,7 @@ cudaError_t launch_attn_tc(const AttnArgs& a, void* scratch, int sms, cudaStream
   p.err = a.err;
   // never below 100 ms, so that no CTA leaves with its loads in flight
   p.wait_ns = scan_wait_limit_ns() > 100000000ull ? scan_wait_limit_ns() : 100000000ull;
-  if (a.dtype == kBF16)
-    return a.dim <= 64 ? launch_fwd<__nv_bfloat16, 64>(a, p, s, qm, km, vm, st)
-                       : launch_fwd<__nv_bfloat16, 128>(a, p, s, qm, km, vm, st);
-  return a.dim <= 64 ? launch_fwd<__half, 64>(a, p, s, qm, km, vm, st) : launch_fwd<__half, 128>(a, p, s, qm, km, vm, st);
+  return a.dtype == kBF16 ? launch_fwd<__nv_bfloat16>(a, p, s, maps, st) : launch_fwd<__half>(a, p, s, maps, st);
 }
 
 }  // namespace smc
