@@ -44,7 +44,7 @@ struct BwdParams {
   int qpt, qps;  // queries of a resident tile, of a step
   float scale;
   bool causal;
-  const float *lse, *delta;  // as k_attn_delta_tc leaves them: lse log2e (+inf for a row that saw no key), delta
+  const float *lse, *delta;  // as k_attn_delta_tc leaves them: -lse log2e (-inf for a row that saw no key), -delta
   const uint32_t* norms;  // fp16: bits of max |dO|^2, max |V|^2
   void *d1, *d2;          // dQ, -- or dK, dV
   int64_t s1[2], s2[2];
@@ -55,10 +55,14 @@ struct BwdParams {
 template <int DP> struct BwdLayout {
   static constexpr uint32_t kResident = DP / 64 * kPanel, kPass = DP / 64 * kStepPanel;
   static constexpr int kSlots = DP == 64 ? 6 : 4;
+  // TMEM: buffers of S and dP (64 columns each), then the accumulators
+  static constexpr int kBufs = DP == 64 ? 3 : 2;
+  static constexpr uint32_t kAcc = kBufs * 2 * kStep;
+  static_assert(kAcc + 2 * DP <= 512, "accumulators fit");
   static constexpr uint32_t kA = 0, kB = 2 * kResident, kRowVals = kB + kSlots * 2 * kPass;
   static constexpr uint32_t kBar = kRowVals + kSlots * 2 * kStep * 4;
-  // barriers: resident, full[kSlots], empty[kSlots], s[2], p[2], out, tail
-  static constexpr uint32_t kMisc = kBar + 8 * (2 * kSlots + 7), kTotal = kMisc + 32 + 1024;
+  // barriers: resident, full[kSlots], empty[kSlots], s[kBufs], p[kBufs], out, tail
+  static constexpr uint32_t kMisc = kBar + 8 * (2 * kSlots + 2 * kBufs + 3), kTotal = kMisc + 32 + 1024;
 };
 
 // The power of two that dS carries in fp16.
@@ -77,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap b1map, const __grid_constant__ CUtensorMap b2map,
                   const BwdParams p) {
   using L = BwdLayout<DP>;
-  constexpr int kSlots = L::kSlots, kPanels = DP / 64;
+  constexpr int kSlots = L::kSlots, kPanels = DP / 64, kBufs = L::kBufs;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr float kShift = kBf16 || kDQ ? 0.f : 14.f;  // P carries 2^kShift
   extern __shared__ uint8_t smem_raw[];
@@ -86,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + (sbase - raw);
   volatile uint32_t* s_misc = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);  // [0] tmem
   const uint32_t bar_a = sbase + L::kBar, bar_full = bar_a + 8, bar_empty = bar_full + 8 * kSlots;
-  const uint32_t bar_s = bar_empty + 8 * kSlots, bar_p = bar_s + 16, bar_o = bar_p + 16, bar_tail = bar_o + 8;
+  const uint32_t bar_s = bar_empty + 8 * kSlots, bar_p = bar_s + 8 * kBufs, bar_o = bar_p + 8 * kBufs, bar_tail = bar_o + 8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // causal: the tiles with the most work (the last queries, the first keys) start first
@@ -122,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_full + 8 * s, kDQ ? 1 : 33);
       mbar_init(bar_empty + 8 * s, 1);
     }
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < kBufs; ++t) {
       mbar_init(bar_s + 8 * t, 1);
       mbar_init(bar_p + 8 * t, 8);
     }
@@ -238,35 +242,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    bool ok = nsteps > 0 && wait(bar_a, 0) && wait(bar_full, 0);
-    if (ok) scores(tmem, b1, bar_s);
-    int slot = 0, nslot = 1;
-    uint32_t nparity = 0;
-    for (int j = 0; j < nsteps && ok; ++j) {
-      const uint32_t b = j & 1, d = tmem + b * 2 * kStep;
-      if (j + 1 < nsteps) {
-        if (!wait(bar_full + 8 * nslot, nparity)) break;
-        scores(tmem + (b ^ 1) * 2 * kStep, b1 + nslot * kSlot, bar_s + 8 * (b ^ 1));
+    bool ok = nsteps > 0 && wait(bar_a, 0);
+    // S and dP run kBufs - 1 steps ahead of the products: step j + kBufs - 1 goes
+    // into the buffer whose P and dS the products of step j - 1 have read.
+    int slot = 0, buf = 0, aslot = 0, abuf = 0;
+    uint32_t pparity = 0, aparity = 0;
+    auto ahead = [&]() {
+      if (!wait(bar_full + 8 * aslot, aparity)) return false;
+      scores(tmem + abuf * 2 * kStep, b1 + aslot * kSlot, bar_s + 8 * abuf);
+      if (++aslot == kSlots) {
+        aslot = 0;
+        aparity ^= 1;
       }
-      if (!wait(bar_p + 8 * b, (j >> 1) & 1)) break;
+      if (++abuf == kBufs) abuf = 0;
+      return true;
+    };
+    for (int j = 0; j < kBufs - 1 && j < nsteps && ok; ++j) ok = ahead();
+    for (int j = 0; j < nsteps && ok; ++j) {
+      if (j + kBufs - 1 < nsteps && !ahead()) break;
+      if (!wait(bar_p + 8 * buf, pparity)) break;
+      const uint32_t d = tmem + buf * 2 * kStep;
       const uint64_t at = n1 + slot * kSlot;
       if (elect_one()) {
         if (!kDQ) {
 #pragma unroll
           for (int k = 0; k < kStep / 16; ++k)
-            umma_f16_ts(tmem + 4 * kStep + DP, d + 8 * k + 16 * (k >> 1), at + kSecond + 128 * k, idesc_o, j > 0 || k > 0);
+            umma_f16_ts(tmem + L::kAcc + DP, d + 8 * k + 16 * (k >> 1), at + kSecond + 128 * k, idesc_o, j > 0 || k > 0);
         }
 #pragma unroll
         for (int k = 0; k < kStep / 16; ++k)
-          umma_f16_ts(tmem + 4 * kStep, d + kStep + 8 * k + 16 * (k >> 1), at + 128 * k, idesc_o, j > 0 || k > 0);
+          umma_f16_ts(tmem + L::kAcc, d + kStep + 8 * k + 16 * (k >> 1), at + 128 * k, idesc_o, j > 0 || k > 0);
         if (j + kSlots < nsteps) umma_commit(bar_empty + 8 * slot);
         if (j + 1 == nsteps) umma_commit(bar_o);
       }
       __syncwarp();
-      slot = nslot;
-      if (++nslot == kSlots) {
-        nslot = 0;
-        nparity ^= 1;
+      if (++slot == kSlots) slot = 0;
+      if (++buf == kBufs) {
+        buf = 0;
+        pparity ^= 1;
       }
     }
   } else {
@@ -274,36 +287,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     // w & 1: even or odd steps; w >> 1: columns 0-31 or 32-63 of them
     const int w = warp >> 2, r = (warp & 3) * 32 + lane, par = w & 1, half = w >> 1;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t buf = tmem + lanes + par * 2 * kStep;
     const float factor = ds_factor(p.norms);
     const float2 c2 = make_float2(p.scale * kLog2e, p.scale * kLog2e);
     const float2 f2 = make_float2(factor * exp2f(-kShift), factor * exp2f(-kShift));
     const int32_t qi = kDQ ? r / p.group : 0;
     const bool row = kDQ ? qi < count : r < count;
-    float l = -INFINITY, e = 0.f;  // dQ: minus those of this thread's query; exp2(s - inf) = 0
+    float l = -INFINITY, e = 0.f;  // dQ: of this thread's query; exp2(s - inf) = 0
     int32_t lim = 0;               // dQ: keys [0, lim) are seen; dK / dV: packed query rows [lim, ..) of the item see the key
     if (kDQ) {
       if (row) {
         const int64_t at = static_cast<int64_t>(u.q.begin + r0 + qi) * p.heads + hk * p.group + r % p.group;
-        l = -p.lse[at];
-        e = -p.delta[at];
+        l = p.lse[at];
+        e = p.delta[at];
         lim = keys_seen(u, r0 + qi, p.causal);
       }
     } else if (p.causal) {
       const int64_t first = static_cast<int64_t>(r0) + r + u.q.count - u.k.count;  // the first query that sees this key
       lim = first < 0 ? 0 : static_cast<int32_t>(first < u.q.count ? first : u.q.count) * p.group;
     }
-    int slot = par % kSlots;
+    int slot = par, b = par;
     uint32_t fparity = 0, sparity = 0;
     bool ok = true;
     for (int j = par; j < nsteps; j += 2) {
       if (!kDQ) ok = mbar_wait_short(bar_full + 8 * slot, fparity, p.err, p.wait_ns);  // the rows' values
-      ok = ok && mbar_wait_short(bar_s + 8 * par, sparity, p.err, p.wait_ns);
+      ok = ok && mbar_wait_short(bar_s + 8 * b, sparity, p.err, p.wait_ns);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
       tc_fence_after();
+      const uint32_t buf = tmem + lanes + b * 2 * kStep;
       float s[32], d[32];
       tmem_ld(buf + 32 * half, s);
       tmem_ld(buf + kStep + 32 * half, d);
@@ -317,9 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 32; i += 4) {
         float4 l4 = make_float4(l, l, l, l), e4 = make_float4(e, e, e, e);
         if (!kDQ) {
-          const float4 a = vl[i / 4], b = vl[kStep / 4 + i / 4];
-          l4 = make_float4(kShift - a.x, kShift - a.y, kShift - a.z, kShift - a.w);
-          e4 = make_float4(-b.x, -b.y, -b.z, -b.w);
+          l4 = vl[i / 4];
+          e4 = vl[kStep / 4 + i / 4];
+          if (kShift != 0.f) l4 = make_float4(l4.x + kShift, l4.y + kShift, l4.z + kShift, l4.w + kShift);
         }
         const float2 x0 = fma2(make_float2(s[i], s[i + 1]), c2, make_float2(l4.x, l4.y));
         const float2 x1 = fma2(make_float2(s[i + 2], s[i + 3]), c2, make_float2(l4.z, l4.w));
@@ -352,9 +365,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_p + 8 * par);
+      if (lane == 0) mbar_arrive(bar_p + 8 * b);
       __syncwarp();
-      sparity ^= 1;
+      if ((b += 2) >= kBufs) {
+        b -= kBufs;
+        sparity ^= 1;
+      }
       if ((slot += 2) >= kSlots) {
         slot -= kSlots;
         fparity ^= 1;
@@ -370,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // and 2, dV: 1 and 3, half of the columns each
       const int c_lo = kDQ ? 32 * w : half * (DP / 2), c_hi = kDQ ? (c_lo + 32 < DP ? c_lo + 32 : DP) : c_lo + DP / 2;
       const bool second = !kDQ && par == 1;
-      const uint32_t acc = tmem + lanes + 4 * kStep + (second ? DP : 0);
+      const uint32_t acc = tmem + lanes + L::kAcc + (second ? DP : 0);
       const float mul = second ? exp2f(-kShift) : p.scale / factor;
       const int64_t out_row = kDQ ? static_cast<int64_t>(u.q.begin) + r0 + qi : static_cast<int64_t>(u.k.begin) + r0 + r;
       const int head = kDQ ? hk * p.group + r % p.group : hk;
@@ -402,8 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
-// delta[row, head] = sum of dO * O, and lse2 = lse log2e, or +infinity for a
-// row that saw no key, whose P = exp2(S - lse2) is then 0; fp16: also the largest squared norms of
+// delta[row, head] = -sum of dO * O, and lse2 = -lse log2e, or -infinity for a
+// row that saw no key, whose P = exp2(S + lse2) is then 0; fp16: also the largest squared norms of
 // the rows of dO and of V that belong to items (as bits: they are not
 // negative).  LPR lanes hold a row of up to 8 LPR channels.
 template <typename T, int LPR>
@@ -439,8 +455,8 @@ __global__ void __launch_bounds__(256) k_attn_delta_tc(const AttnArgs a, float* 
     }
     s = group_sum<LPR>(s);
     if (there && l == 0) {
-      a.delta[i] = s;
-      lse2[i] = a.lse[i] == -INFINITY ? INFINITY : a.lse[i] * kLog2e;
+      a.delta[i] = -s;
+      lse2[i] = a.lse[i] == -INFINITY ? -INFINITY : a.lse[i] * -kLog2e;
     }
     if (norms) top = fmaxf(top, group_sum<LPR>(q));
   }

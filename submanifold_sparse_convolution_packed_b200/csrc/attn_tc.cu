@@ -9,13 +9,14 @@
 //              step's columns: one thread per row, its scores in registers,
 //              running maximum and sum in fp32, P rounded to the input type
 //              into the TMEM columns its scores came from;
-//   MMA        S = Q K^T (both from shared memory), then O += P V with P in
-//              TMEM and V read MN-major as it lies;
+//   MMA        one for each tile: S = Q K^T (both from shared memory), then
+//              O += P V with P in TMEM and V read MN-major as it lies;
 //   TMA        the Q tiles once, then K and V tiles into a ring.
-// While one tile's scores are exponentiated, the tensor cores work on the
-// other tile (or the other CTA of the SM: one-tile CTAs run two to an SM).
-// The two halves of a step keep maxima, sums and accumulators of their own
-// (TMEM has the room), so a row's two threads meet only at the end.
+// Each tile's half is a chain of its own, S -> softmax -> product -> next S,
+// with its own maxima, sums and accumulator (TMEM has the room), so a row's two
+// threads meet only at the end, and while one chain waits for the tensor cores
+// the others keep the special-function unit busy (an SM runs four chains: two
+// tiles, or two one-tile CTAs).
 // An accumulator is rescaled in TMEM only when a row's maximum has grown by
 // more than 2^8 (P stays below 256, far inside fp16's range); the sums use the
 // unrounded P.  Keys behind the item's end are masked, and V rows there are
@@ -56,10 +57,10 @@ template <int DP, int kTiles> struct FwdLayout {
   // one-tile CTAs leave room for a second one on the SM
   static constexpr int kSlots = (DP == 64 ? 4 : 2) * kTiles;
   static constexpr int kHalves = DP == 64 ? 2 : 1, kGroups = kTiles * kHalves;
-  static constexpr int kThreads = 128 * kGroups + 64;
+  static constexpr int kThreads = 128 * kGroups + 32 * (kTiles + 1);
   static constexpr uint32_t kQ = 0, kKv = kTiles * kTileBytes, kBar = kKv + kSlots * kTileBytes;
-  // barriers: q, kv full[kSlots], kv empty[kSlots], s full[kTiles], p ready[kGroups], o done[kTiles], tail
-  static constexpr uint32_t kMisc = kBar + 8 * (2 * kSlots + 2 * kTiles + kGroups + 2);
+  // barriers: q, kv full[kSlots], kv empty[kSlots], s full[kGroups], p ready[kGroups], o done[kTiles], tail
+  static constexpr uint32_t kMisc = kBar + 8 * (2 * kSlots + kTiles + 2 * kGroups + 2);
   static constexpr uint32_t kMl = (kMisc + 16 + 15) / 16 * 16;  // (maximum, sum) of each row and half
   static constexpr uint32_t kTotal = kMl + kGroups * kRows * 8 + 1024;
   // TMEM columns: S of the tiles, then O of the tiles' halves
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
                   const __grid_constant__ CUtensorMap vmap, const FwdParams p) {
   using L = FwdLayout<DP, kTiles>;
   constexpr int kSlots = L::kSlots, kPanels = DP / 64, kHalves = L::kHalves, kCols = kRows / kHalves;
-  constexpr int kMmaWarp = 4 * L::kGroups, kTmaWarp = kMmaWarp + 1;
+  constexpr int kMmaWarp = 4 * L::kGroups, kTmaWarp = kMmaWarp + kTiles;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Unit s_unit;
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
   uint8_t* smem = smem_raw + (sbase - raw);
   volatile uint32_t* s_misc = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);  // [0] tmem
   const uint32_t bar_q = sbase + L::kBar, bar_full = bar_q + 8, bar_empty = bar_full + 8 * kSlots;
-  const uint32_t bar_s = bar_empty + 8 * kSlots, bar_p = bar_s + 8 * kTiles, bar_o = bar_p + 8 * L::kGroups;
+  const uint32_t bar_s = bar_empty + 8 * kSlots, bar_p = bar_s + 8 * L::kGroups, bar_o = bar_p + 8 * L::kGroups;
   const uint32_t bar_tail = bar_o + 8 * kTiles;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -113,13 +114,13 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
     mbar_init(bar_q, 1);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar_full + 8 * s, 1);
-      mbar_init(bar_empty + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, kTiles);
     }
-    for (int t = 0; t < kTiles; ++t) {
-      mbar_init(bar_s + 8 * t, 1);
-      mbar_init(bar_o + 8 * t, 1);
+    for (int t = 0; t < kTiles; ++t) mbar_init(bar_o + 8 * t, 1);
+    for (int g = 0; g < L::kGroups; ++g) {
+      mbar_init(bar_s + 8 * g, 1);
+      mbar_init(bar_p + 8 * g, 4);
     }
-    for (int g = 0; g < L::kGroups; ++g) mbar_init(bar_p + 8 * g, 4);
     mbar_init(bar_tail, 1);
     fence_mbarrier_init();
     fence_proxy_async_smem();
@@ -175,73 +176,86 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
         }
       }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
     // ------------------------------------------------------------- MMA issue
-    // The whole warp runs the loop; one elected lane issues each batch, with
-    // the descriptors advanced by additions only (computing them anew made
-    // each MMA cost about 120 clocks of this warp's time).
+    // A warp for each tile; one elected lane issues each batch, with the
+    // descriptors advanced by additions only (computing them anew made each
+    // MMA cost about 120 clocks of the warp's time).
+    const int t = warp - kMmaWarp, mine = steps[t];
     const uint32_t ab = kBf16 ? 1u : 0u;
     const int ks = (p.dim + 15) / 16;
-    const uint32_t idesc_s = idesc_f16(ab, kRows), idesc_o = idesc_f16(ab, static_cast<uint32_t>(ks * 16)) | kIdescBMn;
-    const uint64_t q = kmajor_desc(sbase + L::kQ, 128), kd = kmajor_desc(sbase + L::kKv, 128);
-    const uint64_t vd = mnmajor_desc(sbase + L::kKv, kPanel);
+    const uint32_t idesc_s = idesc_f16(ab, kCols), idesc_o = idesc_f16(ab, static_cast<uint32_t>(ks * 16)) | kIdescBMn;
     constexpr uint64_t kTile = L::kTileBytes >> 4;
+    const uint64_t q = kmajor_desc(sbase + L::kQ, 128) + t * kTile, kd = kmajor_desc(sbase + L::kKv, 128);
+    const uint64_t vd = mnmajor_desc(sbase + L::kKv, kPanel);
     auto wait = [&](uint32_t bar, uint32_t parity) {
       const bool w = __all_sync(0xffffffffu, mbar_wait_short(bar, parity, p.err, p.wait_ns));
       tc_fence_after();
       return w;
     };
-    auto scores = [&](int t, uint64_t k0) {
-      if (elect_one()) {
-        const uint64_t a0 = q + t * kTile;
+    auto scores = [&](int h, uint64_t k0) {  // in the elected lane
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k)
-          if (k < ks)
-            umma_f16(tmem + t * kRows, a0 + (k >> 2) * (kPanel >> 4) + 2 * (k & 3),
-                     k0 + (k >> 2) * (kPanel >> 4) + 2 * (k & 3), idesc_s, k > 0);
-        umma_commit(bar_s + 8 * t);
+      for (int k = 0; k < DP / 16; ++k)
+        if (k < ks)
+          umma_f16(tmem + t * kRows + h * kCols, q + (k >> 2) * (kPanel >> 4) + 2 * (k & 3),
+                   k0 + h * (kCols * 8) + (k >> 2) * (kPanel >> 4) + 2 * (k & 3), idesc_s, k > 0);
+      umma_commit(bar_s + 8 * (t * kHalves + h));
+    };
+    // A slot is free once every tile's warp has let go of it: behind the products
+    // that read it, or at once where the tile has none.  Only slots that are
+    // loaded again: no arrival is left under way at the end.
+    auto release = [&](int slot, int index, bool read) {
+      if (index + kSlots < 2 * nsteps && elect_one()) {
+        if (read) umma_commit(bar_empty + 8 * slot);
+        else mbar_arrive(bar_empty + 8 * slot);
       }
       __syncwarp();
     };
     bool ok = nsteps > 0 && wait(bar_q, 0) && wait(bar_full, 0);
     if (ok) {
-      for (int t = 0; t < kTiles; ++t)
-        if (steps[t] > 0) scores(t, kd);
-      if (kSlots < 2 * nsteps) umma_commit_elect(bar_empty);
+      if (mine > 0 && elect_one()) {
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) scores(h, kd);
+      }
+      __syncwarp();
+      release(0, 0, mine > 0);
     }
     int sv = 1, sk = 2 % kSlots;  // slots of V of this step, of K of the next
     uint32_t pv = 0, pk = kSlots == 2 ? 1 : 0;
     for (int j = 0; j < nsteps && ok; ++j) {
-      bool next = false;  // K of the next step awaited
-      ok = wait(bar_full + 8 * sv, pv);
       const uint64_t v0 = vd + sv * kTile, k0 = kd + sk * kTile;
+      const bool last = j + 1 == mine, more = j + 1 < nsteps;
+      ok = wait(bar_full + 8 * sv, pv);
+      // with two slots, K of the next step may still be on its way when P is ready
+      constexpr bool kEarly = kSlots > 2;
+      if (kEarly && ok && more) ok = wait(bar_full + 8 * sk, pk);
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        if (j >= steps[t] || !ok) continue;
+      for (int h = 0; h < kHalves; ++h) {
+        if (j >= mine || !ok) continue;
+        const int g = t * kHalves + h;
+        ok = wait(bar_p + 8 * g, j & 1);
+        if (ok && elect_one()) {
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
-          const int g = t * kHalves + h;
-          ok = ok && wait(bar_p + 8 * g, j & 1);
-          if (ok && elect_one()) {
-#pragma unroll
-            for (int k = 0; k < kCols / 16; ++k)
-              umma_f16_ts(tmem + L::kO + g * DP, tmem + t * kRows + h * kCols + k * 8, v0 + 128 * (h * kCols / 16 + k),
-                          idesc_o, j > 0 || k > 0);
-            if (h + 1 == kHalves && j + 1 == steps[t]) umma_commit(bar_o + 8 * t);
-          }
-          __syncwarp();
+          for (int k = 0; k < kCols / 16; ++k)
+            umma_f16_ts(tmem + L::kO + g * DP, tmem + t * kRows + h * kCols + k * 8, v0 + 128 * (h * kCols / 16 + k),
+                        idesc_o, j > 0 || k > 0);
+          if (kEarly && !last) scores(h, k0);
+          if (last && h + 1 == kHalves) umma_commit(bar_o + 8 * t);
         }
-        if (!ok) continue;
-        if (j + 1 < steps[t]) {
-          ok = next || wait(bar_full + 8 * sk, pk);
-          next = true;
-          if (ok) scores(t, k0);
-        }
+        __syncwarp();
       }
       if (!ok) break;
-      // only for slots that are loaded again: no arrival is left under way at the end
-      if (2 * j + 1 + kSlots < 2 * nsteps) umma_commit_elect(bar_empty + 8 * sv);
-      if (next && 2 * j + 2 + kSlots < 2 * nsteps) umma_commit_elect(bar_empty + 8 * sk);
+      release(sv, 2 * j + 1, j < mine);
+      if (!kEarly && more) {
+        ok = wait(bar_full + 8 * sk, pk);
+        if (ok && j + 1 < mine && elect_one()) {
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) scores(h, k0);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (more) release(sk, 2 * j + 2, j + 1 < mine);
       if ((sv += 2) >= kSlots) {
         sv -= kSlots;
         pv ^= 1;
@@ -264,7 +278,7 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
     float top = -INFINITY, sum = 0.f;  // top: the rounded product with c the sums refer to
     bool ok = true;
     for (int j = 0; j < steps[t]; ++j) {
-      ok = __all_sync(0xffffffffu, mbar_wait_short(bar_s + 8 * t, j & 1, p.err, p.wait_ns));
+      ok = __all_sync(0xffffffffu, mbar_wait_short(bar_s + 8 * g, j & 1, p.err, p.wait_ns));
       if (!ok) break;
       tc_fence_after();
       if (used) {
@@ -278,13 +292,15 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
         }
         float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
 #pragma unroll
-        for (int i = 4; i < kCols; i += 4) {
-          m0 = fmaxf(m0, x[i]);
-          m1 = fmaxf(m1, x[i + 1]);
-          m2 = fmaxf(m2, x[i + 2]);
-          m3 = fmaxf(m3, x[i + 3]);
+        for (int i = 4; i + 8 <= kCols; i += 8) {
+          m0 = max3(m0, x[i], x[i + 1]);
+          m1 = max3(m1, x[i + 2], x[i + 3]);
+          m2 = max3(m2, x[i + 4], x[i + 5]);
+          m3 = max3(m3, x[i + 6], x[i + 7]);
         }
-        const float m = __fmul_rn(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), p.c);
+        m0 = max3(m0, x[kCols - 4], x[kCols - 3]);
+        m1 = max3(m1, x[kCols - 2], x[kCols - 1]);
+        const float m = __fmul_rn(fmaxf(max3(m0, m1, m2), m3), p.c);
         const bool grown = m > top + 8.f || (top == -INFINITY && m > -INFINITY);
         if (__any_sync(0xffffffffu, grown)) {
           const float keep = grown ? exp2_fast(top - m) : 1.f;
@@ -314,7 +330,8 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
           for (int i = 0; i < 32; i += 2) {
             const int e = q * 64 + 2 * i;
             const float2 y0 = fma2(make_float2(x[e], x[e + 1]), c2, b2), y1 = fma2(make_float2(x[e + 2], x[e + 3]), c2, b2);
-            const float2 e0 = make_float2(exp2_fast(y0.x), exp2_fast(y0.y)), e1 = make_float2(exp2_fast(y1.x), exp2_fast(y1.y));
+            const float2 e0 = make_float2(exp2_fast(y0.x), exp2_fast(y0.y));
+            const float2 e1 = make_float2(exp2_fast(y1.x), exp2_fast(y1.y));
             sa = add2(sa, e0);
             sb = add2(sb, e1);
             w[i] = pack2<T>(e0.x, e0.y);
