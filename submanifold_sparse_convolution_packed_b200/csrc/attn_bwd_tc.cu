@@ -38,9 +38,8 @@ constexpr int kStep = 64;                       // passing rows of a step
 constexpr uint32_t kStepPanel = kStep * 128;
 
 struct BwdParams {
-  const int32_t *q_off, *k_off;
-  int64_t n, m;
-  int items, heads, kv_heads, dim, group;
+  Cut cut;
+  int heads, kv_heads, dim, group;
   int qpt, qps;  // queries of a resident tile, of a step
   float scale;
   bool causal;
@@ -93,9 +92,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar_s = bar_empty + 8 * kSlots, bar_p = bar_s + 8 * kBufs, bar_o = bar_p + 8 * kBufs, bar_tail = bar_o + 8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  // causal: the tiles with the most work (the last queries, the first keys) start first
   const int64_t ux = kDQ && p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-  find_unit<kThreads>(p.q_off, p.k_off, p.items, p.n, p.m, kDQ ? p.qpt : kRows, 0, !kDQ, ux, &s_unit, p.err);
+  find_unit<kThreads>(p.cut, ux, &s_unit, p.err);
   if (s_unit.item < 0) return;
   const Unit u = s_unit;
   const int hk = blockIdx.y;
@@ -115,7 +113,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   const int nsteps = b_hi > b_lo ? (b_hi - b_lo + per_step - 1) / per_step : 0;
-
   if (tid == 0) {
     prefetch_tmap(&a1map);
     prefetch_tmap(&a2map);
@@ -390,8 +387,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float mul = second ? exp2f(-kShift) : p.scale / factor;
       const int64_t out_row = kDQ ? static_cast<int64_t>(u.q.begin) + r0 + qi : static_cast<int64_t>(u.k.begin) + r0 + r;
       const int head = kDQ ? hk * p.group + r % p.group : hk;
-      T* to = static_cast<T*>(second ? p.d2 : p.d1) + out_row * (second ? p.s2[0] : p.s1[0]) +
-              head * (second ? p.s2[1] : p.s1[1]);
+      T* to = static_cast<T*>(second ? p.d2 : p.d1);
+      const int64_t at = out_row * (second ? p.s2[0] : p.s1[0]) + head * (second ? p.s2[1] : p.s1[1]);
+      // the resident tiles are no longer needed: every product is done
+      uint8_t* stage = smem + L::kA + warp * 2048;
 #pragma unroll 1
       for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
         if (c0 >= p.dim) break;
@@ -402,14 +401,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
         }
-        uint4* d = reinterpret_cast<uint4*>(to + c0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (row && c0 + 8 * i < p.dim)
-            d[i] = make_uint4(pack2<T>(o[8 * i] * mul, o[8 * i + 1] * mul), pack2<T>(o[8 * i + 2] * mul, o[8 * i + 3] * mul),
-                              pack2<T>(o[8 * i + 4] * mul, o[8 * i + 5] * mul),
-                              pack2<T>(o[8 * i + 6] * mul, o[8 * i + 7] * mul));
-        __syncwarp();  // the warp reads TMEM together
+        for (int i = 0; i < 32; ++i) o[i] *= mul;
+        store_rows<T>(stage, o, to, row ? at : -1, c0, p.dim);
       }
     }
   }
@@ -504,6 +498,8 @@ cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const CUtensorMap* maps
   for (int i = 0; i < 2; ++i) p.s1[i] = a.dq_stride[i];
   kq<<<dim3(static_cast<unsigned>(a.n / p.qpt + a.items), a.kv_heads), kThreads, kSmem, st>>>(maps[0], maps[1], maps[2],
                                                                                              maps[3], p);
+  p.cut.per_tile = divisor(kRows);
+  p.cut.by_keys = true;
   p.d1 = a.dk;
   p.d2 = a.dv;
   for (int i = 0; i < 2; ++i) {
@@ -546,11 +542,7 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs& a, float* lse2, uint32_t* norms, 
       !keys(&maps[4], a.k, a.k_stride, kRows) || !keys(&maps[5], a.v, a.v_stride, kRows) ||
       !queries(&maps[6], a.q, a.q_stride, p.qps) || !queries(&maps[7], a.dout, a.dout_stride, p.qps))
     return cudaErrorInvalidValue;
-  p.q_off = a.q_off;
-  p.k_off = a.k_off;
-  p.n = a.n;
-  p.m = a.m;
-  p.items = a.items;
+  p.cut = {a.q_off, a.k_off, static_cast<int32_t>(a.n), static_cast<int32_t>(a.m), a.items, 0, divisor(p.qpt), false};
   p.heads = a.heads;
   p.kv_heads = a.kv_heads;
   p.dim = a.dim;

@@ -116,13 +116,13 @@ __device__ __forceinline__ int32_t keys_seen(const Unit& u, int32_t qi, bool cau
 }
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut cut) {
   extern __shared__ float sm[];
   __shared__ Unit unit;
   constexpr int LD = DP + 4, W = DP / 16;
   float *sq = sm, *sk = sq + kTile * LD, *sv = sk + kTile * LD, *sp = sv + kTile * LD;
   const int group = a.heads / a.kv_heads, per_tile = kTile / group;
-  find_unit<kThreads>(a.q_off, a.k_off, a.items, a.n, a.m, per_tile, 0, false, blockIdx.x, &unit, a.err);
+  find_unit<kThreads>(cut, blockIdx.x, &unit, a.err);
   if (unit.item < 0) return;
   const Unit u = unit;
   const int hk = blockIdx.y, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -206,14 +206,14 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a) {
 // kDQ: a tile of packed queries against all its keys -> dQ.  Otherwise a tile
 // of keys against all its packed queries -> dK, dV.  A1, A2 stay; B1, B2 pass.
 template <typename T, int DP, bool kDQ>
-__global__ void __launch_bounds__(kThreads) k_attn_bwd(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads) k_attn_bwd(const AttnArgs a, const Cut cut) {
   extern __shared__ float sm[];
   __shared__ Unit unit;
   __shared__ float s_lse[kTile], s_delta[kTile];
   constexpr int LD = DP + 4, W = DP / 16;
   float *a1 = sm, *a2 = a1 + kTile * LD, *b1 = a2 + kTile * LD, *b2 = b1 + kTile * LD, *sp = b2 + kTile * LD;
   const int group = a.heads / a.kv_heads, per_tile = kTile / group;
-  find_unit<kThreads>(a.q_off, a.k_off, a.items, a.n, a.m, kDQ ? per_tile : kTile, 0, !kDQ, blockIdx.x, &unit, a.err);
+  find_unit<kThreads>(cut, blockIdx.x, &unit, a.err);
   if (unit.item < 0) return;
   const Unit u = unit;
   const int hk = blockIdx.y, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -350,11 +350,12 @@ template <typename T, int DP>
 cudaError_t launch_dim(const AttnArgs& a, bool backward, cudaStream_t s) {
   const int per_tile = kTile / (a.heads / a.kv_heads);
   const dim3 qgrid(static_cast<unsigned>(a.n / per_tile + a.items), a.kv_heads);
+  Cut cut = {a.q_off, a.k_off, static_cast<int32_t>(a.n), static_cast<int32_t>(a.m), a.items, 0, divisor(per_tile), false};
   const size_t tile = kTile * (DP + 4) * sizeof(float), extra = kTile * (kTile + 4) * sizeof(float);
   cudaError_t e;
   if (!backward) {
     if ((e = allow_smem(k_attn<T, DP>, 3 * tile + extra)) != cudaSuccess) return e;
-    k_attn<T, DP><<<qgrid, kThreads, 3 * tile + extra, s>>>(a);
+    k_attn<T, DP><<<qgrid, kThreads, 3 * tile + extra, s>>>(a, cut);
     count_launches(1);
     return cudaGetLastError();
   }
@@ -363,12 +364,14 @@ cudaError_t launch_dim(const AttnArgs& a, bool backward, cudaStream_t s) {
   const int64_t warps = a.n * a.heads, want = (warps + 7) / 8;
   if (a.n > 0) {
     k_attn_delta<T><<<static_cast<unsigned>(want < 4096 ? want : 4096), kThreads, 0, s>>>(a);
-    k_attn_bwd<T, DP, true><<<qgrid, kThreads, 4 * tile + extra, s>>>(a);
+    k_attn_bwd<T, DP, true><<<qgrid, kThreads, 4 * tile + extra, s>>>(a, cut);
     count_launches(2);
   }
   if (a.m > 0) {
     const dim3 kgrid(static_cast<unsigned>(a.m / kTile + a.items), a.kv_heads);
-    k_attn_bwd<T, DP, false><<<kgrid, kThreads, 4 * tile + extra, s>>>(a);
+    cut.per_tile = divisor(kTile);
+    cut.by_keys = true;
+    k_attn_bwd<T, DP, false><<<kgrid, kThreads, 4 * tile + extra, s>>>(a, cut);
     count_launches(1);
   }
   return cudaGetLastError();

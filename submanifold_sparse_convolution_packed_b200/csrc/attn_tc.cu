@@ -4,9 +4,10 @@
 //
 // One CTA holds kTiles (1 or 2) tiles of 128 packed rows (row = query * G +
 // head of the group, so the heads that share keys share the tile) of one
-// key/value head against a run of the item's keys, 128 at a time.  Its warps:
-//   softmax    four for each tile and, up to 64 channels, for each half of a
-//              step's columns: one thread per row, its scores in registers,
+// key/value head against a run of the item's keys, 128 (or 64) at a time.  Its
+// warps:
+//   softmax    four for each tile and, with two tiles of up to 64 channels, for
+//              each half of a step's columns: one thread per row, its scores in registers,
 //              running maximum and sum in fp32, P rounded to the input type
 //              into the TMEM columns its scores came from;
 //   MMA        one for each tile: S = Q K^T (both from shared memory), then
@@ -15,8 +16,8 @@
 // Each tile's half is a chain of its own, S -> softmax -> product -> next S,
 // with its own maxima, sums and accumulator (TMEM has the room), so a row's two
 // threads meet only at the end, and while one chain waits for the tensor cores
-// the others keep the special-function unit busy (an SM runs four chains: two
-// tiles, or two one-tile CTAs).
+// the others keep the special-function unit busy (up to 64 channels an SM runs
+// four chains: two tiles with two halves, or four one-tile CTAs).
 // An accumulator is rescaled in TMEM only when a row's maximum has grown by
 // more than 2^8 (P stays below 256, far inside fp16's range); the sums use the
 // unrounded P.  Keys behind the item's end are masked, and V rows there are
@@ -37,12 +38,9 @@ using namespace attn;
 constexpr int kShortItem = 512;  // packed rows
 
 struct FwdParams {
-  const int32_t *q_off, *k_off;
-  int64_t n, m;
-  int items, heads, kv_heads, dim, group, qpt;  // qpt: queries of a tile
-  int per_unit;                                  // queries of a CTA
-  int chunk;                                     // keys of a split (0: no split)
-  int slot_rows;                                 // rows of a split's partial results
+  Cut cut;                                // per_tile: queries of a CTA; chunk: keys of a split
+  int heads, kv_heads, dim, group, qpt;   // qpt: queries of a tile
+  int slot_rows;                          // rows of a split's partial results
   float c;                                       // scale * log2 e
   bool causal;
   void* out;
@@ -52,28 +50,33 @@ struct FwdParams {
   uint64_t wait_ns;
 };
 
+// Two tiles: one CTA to an SM.  One tile: CTAs share an SM, two of up to 128
+// channels, or four of up to 64 with steps of 64 keys.
 template <int DP, int kTiles> struct FwdLayout {
-  static constexpr uint32_t kTileBytes = DP / 64 * kPanel;
-  // one-tile CTAs leave room for a second one on the SM
-  static constexpr int kSlots = (DP == 64 ? 4 : 2) * kTiles;
-  static constexpr int kHalves = DP == 64 ? 2 : 1, kGroups = kTiles * kHalves;
+  static constexpr bool kSmall = kTiles == 1 && DP == 64;
+  static constexpr int kKeys = kSmall ? 64 : 128;  // keys of a step
+  static constexpr int kBlocks = kTiles == 2 ? 1 : kSmall ? 4 : 2;
+  static constexpr uint32_t kQBytes = DP / 64 * kPanel;                                   // a tile of Q
+  static constexpr uint32_t kKvPanel = kKeys * 128, kKvBytes = DP / 64 * kKvPanel;        // a step of K or V
+  static constexpr int kSlots = kTiles == 2 ? (DP == 64 ? 8 : 4) : kSmall ? 4 : 2;
+  static constexpr int kHalves = kTiles == 2 && DP == 64 ? 2 : 1, kGroups = kTiles * kHalves;
   static constexpr int kThreads = 128 * kGroups + 32 * (kTiles + 1);
-  static constexpr uint32_t kQ = 0, kKv = kTiles * kTileBytes, kBar = kKv + kSlots * kTileBytes;
+  static constexpr uint32_t kQ = 0, kKv = kTiles * kQBytes, kBar = kKv + kSlots * kKvBytes;
   // barriers: q, kv full[kSlots], kv empty[kSlots], s full[kGroups], p ready[kGroups], o done[kTiles], tail
   static constexpr uint32_t kMisc = kBar + 8 * (2 * kSlots + kTiles + 2 * kGroups + 2);
   static constexpr uint32_t kMl = (kMisc + 16 + 15) / 16 * 16;  // (maximum, sum) of each row and half
-  static constexpr uint32_t kTotal = kMl + kGroups * kRows * 8 + 1024;
+  static constexpr uint32_t kTotal = kMl + (kHalves == 2 ? kGroups * kRows * 8 : 0) + 1024;
   // TMEM columns: S of the tiles, then O of the tiles' halves
-  static constexpr uint32_t kO = kTiles * kRows, kColumns = kTiles == 2 ? 512 : 256;
+  static constexpr uint32_t kO = kTiles * kKeys, kColumns = 512 / kBlocks;
   static_assert(kO + kGroups * DP <= kColumns, "accumulators fit");
 };
 
 template <typename T, int DP, int kTiles>
-__global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
+__global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP, kTiles>::kBlocks)
     k_attn_fwd_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const FwdParams p) {
   using L = FwdLayout<DP, kTiles>;
-  constexpr int kSlots = L::kSlots, kPanels = DP / 64, kHalves = L::kHalves, kCols = kRows / kHalves;
+  constexpr int kSlots = L::kSlots, kPanels = DP / 64, kHalves = L::kHalves, kKeys = L::kKeys, kCols = kKeys / kHalves;
   constexpr int kMmaWarp = 4 * L::kGroups, kTmaWarp = kMmaWarp + kTiles;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ uint8_t smem_raw[];
@@ -85,27 +88,6 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
   const uint32_t bar_s = bar_empty + 8 * kSlots, bar_p = bar_s + 8 * L::kGroups, bar_o = bar_p + 8 * L::kGroups;
   const uint32_t bar_tail = bar_o + 8 * kTiles;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-
-  // causal: the tiles with the most keys come last in an item and start first
-  const int64_t ux = p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-  find_unit<L::kThreads>(p.q_off, p.k_off, p.items, p.n, p.m, kTiles * p.qpt, p.chunk, false, ux, &s_unit, p.err);
-  if (s_unit.item < 0) return;
-  const Unit u = s_unit;
-  const int hk = blockIdx.y;
-  const int32_t q0 = u.tile * kTiles * p.qpt;
-  const int32_t left = u.q.count - q0;
-  const int32_t k_lo = u.split * p.chunk;
-  const int32_t k_hi = u.splits > 1 && u.k.count - k_lo > p.chunk ? k_lo + p.chunk : u.k.count;
-  int queries[kTiles], steps[kTiles];
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
-    const int32_t rest = left - t * p.qpt;
-    queries[t] = rest < 0 ? 0 : (rest < p.qpt ? rest : p.qpt);
-    const int32_t seen = queries[t] > 0 ? keys_seen(u, q0 + t * p.qpt + queries[t] - 1, p.causal) : 0;
-    const int32_t hi = seen < k_hi ? seen : k_hi;
-    steps[t] = hi > k_lo ? (hi - k_lo + kRows - 1) / kRows : 0;
-  }
-  const int nsteps = kTiles == 2 && steps[kTiles - 1] > steps[0] ? steps[kTiles - 1] : steps[0];
 
   if (tid == 0) {
     prefetch_tmap(&qmap);
@@ -130,9 +112,31 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  // causal: the tiles with the most keys come last in an item and start first
+  const int64_t ux = p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+  find_unit<L::kThreads>(p.cut, ux, &s_unit, p.err);
   tc_fence_after();
   const uint32_t tmem = s_misc[0];
+  if (s_unit.item < 0) {
+    if (warp == kMmaWarp) tmem_dealloc(tmem, L::kColumns);
+    return;
+  }
+  const Unit u = s_unit;
+  const int hk = blockIdx.y;
+  const int32_t q0 = u.tile * kTiles * p.qpt;
+  const int32_t left = u.q.count - q0;
+  const int32_t k_lo = u.split * p.cut.chunk;
+  const int32_t k_hi = u.splits > 1 && u.k.count - k_lo > p.cut.chunk ? k_lo + p.cut.chunk : u.k.count;
+  int queries[kTiles], steps[kTiles];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) {
+    const int32_t rest = left - t * p.qpt;
+    queries[t] = rest < 0 ? 0 : (rest < p.qpt ? rest : p.qpt);
+    const int32_t seen = queries[t] > 0 ? keys_seen(u, q0 + t * p.qpt + queries[t] - 1, p.causal) : 0;
+    const int32_t hi = seen < k_hi ? seen : k_hi;
+    steps[t] = hi > k_lo ? (hi - k_lo + kKeys - 1) / kKeys : 0;
+  }
+  const int nsteps = kTiles == 2 && steps[kTiles - 1] > steps[0] ? steps[kTiles - 1] : steps[0];
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------- TMA loads
@@ -143,7 +147,7 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
         mbar_arrive_expect_tx(bar_q, static_cast<uint32_t>(tiles * kPanels * p.group * p.qpt) * 128u);
         for (int t = 0; t < tiles; ++t)
           for (int c = 0; c < kPanels; ++c)
-            tma_load_3d(sbase + L::kQ + t * L::kTileBytes + c * kPanel, &qmap, bar_q, c * 64, hk * p.group,
+            tma_load_3d(sbase + L::kQ + t * L::kQBytes + c * kPanel, &qmap, bar_q, c * 64, hk * p.group,
                         u.q.begin + q0 + t * p.qpt);
       }
       __syncwarp();
@@ -151,21 +155,21 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
       uint32_t parity = 1;
       for (int i = 0; i < 2 * nsteps; ++i) {
         if (!__all_sync(0xffffffffu, mbar_wait_short(bar_empty + 8 * slot, parity, p.err, p.wait_ns))) break;
-        const int32_t key = k_lo + (i >> 1) * kRows;
+        const int32_t key = k_lo + (i >> 1) * kKeys;
         const int rows = u.k.count - key;  // V rows behind the item's end are zeroed below
-        const bool tail = (i & 1) && rows < kRows;
-        const uint32_t dst = sbase + L::kKv + slot * L::kTileBytes, bar = tail ? bar_tail : bar_full + 8 * slot;
+        const bool tail = (i & 1) && rows < kKeys;
+        const uint32_t dst = sbase + L::kKv + slot * L::kKvBytes, bar = tail ? bar_tail : bar_full + 8 * slot;
         if (elect_one()) {
-          mbar_arrive_expect_tx(bar, L::kTileBytes);
+          mbar_arrive_expect_tx(bar, L::kKvBytes);
           for (int c = 0; c < kPanels; ++c)
-            tma_load_3d(dst + c * kPanel, (i & 1) ? &vmap : &kmap, bar, c * 64, hk, u.k.begin + key);
+            tma_load_3d(dst + c * L::kKvPanel, (i & 1) ? &vmap : &kmap, bar, c * 64, hk, u.k.begin + key);
         }
         __syncwarp();
         if (tail) {  // once, at the last step
           if (!__all_sync(0xffffffffu, mbar_wait_short(bar_tail, 0, p.err, p.wait_ns))) break;
-          uint4* base = reinterpret_cast<uint4*>(smem + L::kKv + slot * L::kTileBytes);
+          uint4* base = reinterpret_cast<uint4*>(smem + L::kKv + slot * L::kKvBytes);
           for (int c = 0; c < kPanels; ++c)
-            for (int j = rows * 8 + lane; j < kRows * 8; j += 32) base[c * (kPanel / 16) + j] = make_uint4(0, 0, 0, 0);
+            for (int j = rows * 8 + lane; j < kKeys * 8; j += 32) base[c * (L::kKvPanel / 16) + j] = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_full + 8 * slot);
@@ -185,9 +189,9 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
     const uint32_t ab = kBf16 ? 1u : 0u;
     const int ks = (p.dim + 15) / 16;
     const uint32_t idesc_s = idesc_f16(ab, kCols), idesc_o = idesc_f16(ab, static_cast<uint32_t>(ks * 16)) | kIdescBMn;
-    constexpr uint64_t kTile = L::kTileBytes >> 4;
-    const uint64_t q = kmajor_desc(sbase + L::kQ, 128) + t * kTile, kd = kmajor_desc(sbase + L::kKv, 128);
-    const uint64_t vd = mnmajor_desc(sbase + L::kKv, kPanel);
+    constexpr uint64_t kTile = L::kKvBytes >> 4;
+    const uint64_t q = kmajor_desc(sbase + L::kQ, 128) + t * (L::kQBytes >> 4), kd = kmajor_desc(sbase + L::kKv, 128);
+    const uint64_t vd = mnmajor_desc(sbase + L::kKv, L::kKvPanel);
     auto wait = [&](uint32_t bar, uint32_t parity) {
       const bool w = __all_sync(0xffffffffu, mbar_wait_short(bar, parity, p.err, p.wait_ns));
       tc_fence_after();
@@ -197,28 +201,27 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
 #pragma unroll
       for (int k = 0; k < DP / 16; ++k)
         if (k < ks)
-          umma_f16(tmem + t * kRows + h * kCols, q + (k >> 2) * (kPanel >> 4) + 2 * (k & 3),
-                   k0 + h * (kCols * 8) + (k >> 2) * (kPanel >> 4) + 2 * (k & 3), idesc_s, k > 0);
+          umma_f16(tmem + t * kKeys + h * kCols, q + (k >> 2) * (kPanel >> 4) + 2 * (k & 3),
+                   k0 + h * (kCols * 8) + (k >> 2) * (L::kKvPanel >> 4) + 2 * (k & 3), idesc_s, k > 0);
       umma_commit(bar_s + 8 * (t * kHalves + h));
     };
     // A slot is free once every tile's warp has let go of it: behind the products
     // that read it, or at once where the tile has none.  Only slots that are
     // loaded again: no arrival is left under way at the end.
-    auto release = [&](int slot, int index, bool read) {
-      if (index + kSlots < 2 * nsteps && elect_one()) {
-        if (read) umma_commit(bar_empty + 8 * slot);
-        else mbar_arrive(bar_empty + 8 * slot);
-      }
-      __syncwarp();
+    auto release = [&](int slot, int index, bool read) {  // in the elected lane
+      if (index + kSlots >= 2 * nsteps) return;
+      if (read) umma_commit(bar_empty + 8 * slot);
+      else mbar_arrive(bar_empty + 8 * slot);
     };
     bool ok = nsteps > 0 && wait(bar_q, 0) && wait(bar_full, 0);
     if (ok) {
-      if (mine > 0 && elect_one()) {
+      if (elect_one()) {
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h) scores(h, kd);
+        for (int h = 0; h < kHalves; ++h)
+          if (mine > 0) scores(h, kd);
+        release(0, 0, mine > 0);
       }
       __syncwarp();
-      release(0, 0, mine > 0);
     }
     int sv = 1, sk = 2 % kSlots;  // slots of V of this step, of K of the next
     uint32_t pv = 0, pk = kSlots == 2 ? 1 : 0;
@@ -231,31 +234,34 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
       if (kEarly && ok && more) ok = wait(bar_full + 8 * sk, pk);
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
-        if (j >= mine || !ok) continue;
         const int g = t * kHalves + h;
-        ok = wait(bar_p + 8 * g, j & 1);
+        if (ok && j < mine) ok = wait(bar_p + 8 * g, j & 1);
+        if (ok && elect_one()) {
+          if (j < mine) {
+#pragma unroll
+            for (int k = 0; k < kCols / 16; ++k)
+              umma_f16_ts(tmem + L::kO + g * DP, tmem + t * kKeys + h * kCols + k * 8, v0 + 128 * (h * kCols / 16 + k),
+                          idesc_o, j > 0 || k > 0);
+          }
+          if (kEarly && j + 1 < mine) scores(h, k0);
+          if (h + 1 == kHalves) {
+            if (last) umma_commit(bar_o + 8 * t);
+            release(sv, 2 * j + 1, j < mine);
+            if (kEarly && more) release(sk, 2 * j + 2, j + 1 < mine);
+          }
+        }
+        __syncwarp();
+      }
+      if (!kEarly && ok && more) {
+        ok = wait(bar_full + 8 * sk, pk);
         if (ok && elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kCols / 16; ++k)
-            umma_f16_ts(tmem + L::kO + g * DP, tmem + t * kRows + h * kCols + k * 8, v0 + 128 * (h * kCols / 16 + k),
-                        idesc_o, j > 0 || k > 0);
-          if (kEarly && !last) scores(h, k0);
-          if (last && h + 1 == kHalves) umma_commit(bar_o + 8 * t);
+          for (int h = 0; h < kHalves; ++h)
+            if (j + 1 < mine) scores(h, k0);
+          release(sk, 2 * j + 2, j + 1 < mine);
         }
         __syncwarp();
       }
-      if (!ok) break;
-      release(sv, 2 * j + 1, j < mine);
-      if (!kEarly && more) {
-        ok = wait(bar_full + 8 * sk, pk);
-        if (ok && j + 1 < mine && elect_one()) {
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h) scores(h, k0);
-        }
-        __syncwarp();
-      }
-      if (!ok) break;
-      if (more) release(sk, 2 * j + 2, j + 1 < mine);
       if ((sv += 2) >= kSlots) {
         sv -= kSlots;
         pv ^= 1;
@@ -269,7 +275,7 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
     // --------------------------------------------------------------- softmax
     const int g = warp >> 2, t = g / kHalves, h = g % kHalves, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + t * kRows + h * kCols, to = tmem + lanes + L::kO + g * DP;
+    const uint32_t ts = tmem + lanes + t * kKeys + h * kCols, to = tmem + lanes + L::kO + g * DP;
     const int32_t qi = r / p.group;  // query in the tile
     const bool row = qi < queries[t];
     const bool used = __any_sync(0xffffffffu, row);  // a warp without rows only keeps step
@@ -282,24 +288,32 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
       if (!ok) break;
       tc_fence_after();
       if (used) {
-        float x[kCols];
-        tmem_ld(ts, x);
-        const int32_t seen = lim - j * kRows;
-        if (__any_sync(0xffffffffu, seen < kCols)) {
+        // The scores in registers: all of this thread's, or (four CTAs to an SM)
+        // 32 at a time, read from TMEM twice.
+        constexpr int kPart = L::kSmall ? 32 : kCols, kParts = kCols / kPart;
+        const int32_t seen = lim - j * kKeys;
+        const bool whole = __all_sync(0xffffffffu, seen >= kCols);
+        float x[kPart];
+        float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
+        auto load = [&](int q) {
+          tmem_ld(ts + q * kPart, x);
+          if (!whole) {
 #pragma unroll
-          for (int i = 0; i < kCols; ++i)
-            if (i >= seen) x[i] = -INFINITY;
-        }
-        float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
+            for (int i = 0; i < kPart; ++i)
+              if (q * kPart + i >= seen) x[i] = -INFINITY;
+          }
+        };
 #pragma unroll
-        for (int i = 4; i + 8 <= kCols; i += 8) {
-          m0 = max3(m0, x[i], x[i + 1]);
-          m1 = max3(m1, x[i + 2], x[i + 3]);
-          m2 = max3(m2, x[i + 4], x[i + 5]);
-          m3 = max3(m3, x[i + 6], x[i + 7]);
+        for (int q = 0; q < kParts; ++q) {
+          load(q);
+#pragma unroll
+          for (int i = 0; i < kPart; i += 8) {
+            m0 = max3(m0, x[i], x[i + 1]);
+            m1 = max3(m1, x[i + 2], x[i + 3]);
+            m2 = max3(m2, x[i + 4], x[i + 5]);
+            m3 = max3(m3, x[i + 6], x[i + 7]);
+          }
         }
-        m0 = max3(m0, x[kCols - 4], x[kCols - 3]);
-        m1 = max3(m1, x[kCols - 2], x[kCols - 1]);
         const float m = __fmul_rn(fmaxf(max3(m0, m1, m2), m3), p.c);
         const bool grown = m > top + 8.f || (top == -INFINITY && m > -INFINITY);
         if (__any_sync(0xffffffffu, grown)) {
@@ -324,20 +338,25 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
         float2 sa = make_float2(0.f, 0.f), sb = sa;
         const float2 c2 = make_float2(p.c, p.c), b2 = make_float2(-base, -base);
 #pragma unroll
-        for (int q = 0; q < kCols / 64; ++q) {
-          uint32_t w[32];
+        for (int q = 0; q < kParts; ++q) {
+          if (kParts > 1) load(q);
+          constexpr int kWords = kPart >= 64 ? 32 : 16;
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const int e = q * 64 + 2 * i;
-            const float2 y0 = fma2(make_float2(x[e], x[e + 1]), c2, b2), y1 = fma2(make_float2(x[e + 2], x[e + 3]), c2, b2);
-            const float2 e0 = make_float2(exp2_fast(y0.x), exp2_fast(y0.y));
-            const float2 e1 = make_float2(exp2_fast(y1.x), exp2_fast(y1.y));
-            sa = add2(sa, e0);
-            sb = add2(sb, e1);
-            w[i] = pack2<T>(e0.x, e0.y);
-            w[i + 1] = pack2<T>(e1.x, e1.y);
+          for (int z = 0; z < kPart / (2 * kWords); ++z) {
+            uint32_t w[kWords];
+#pragma unroll
+            for (int i = 0; i < kWords; i += 2) {
+              const int e = z * 2 * kWords + 2 * i;
+              const float2 y0 = fma2(make_float2(x[e], x[e + 1]), c2, b2), y1 = fma2(make_float2(x[e + 2], x[e + 3]), c2, b2);
+              const float2 e0 = make_float2(exp2_fast(y0.x), exp2_fast(y0.y)), e1 = make_float2(exp2_fast(y1.x), exp2_fast(y1.y));
+              sa = add2(sa, e0);
+              sb = add2(sb, e1);
+              w[i] = pack2<T>(e0.x, e0.y);
+              w[i + 1] = pack2<T>(e1.x, e1.y);
+            }
+            // over scores that are in registers, or used up
+            tmem_st(ts + (q * kPart / 2 + z * kWords), w);
           }
-          tmem_st(ts + q * 32, w);
         }
         sum += (sa.x + sa.y) + (sb.x + sb.y);
         tmem_st_wait();
@@ -418,12 +437,12 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, 3 - kTiles)
 template <typename T>
 __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p) {
   __shared__ Unit s_unit;
-  find_unit<256>(p.q_off, p.k_off, p.items, p.n, p.m, p.per_unit, p.chunk, false, blockIdx.x, &s_unit, p.err);
+  find_unit<256>(p.cut, blockIdx.x, &s_unit, p.err);
   const Unit u = s_unit;
   if (u.item < 0 || u.split != 0) return;
   const int hk = blockIdx.y, lane = threadIdx.x & 31;
-  const int32_t q0 = u.tile * p.per_unit;
-  const int32_t queries = u.q.count - q0 < p.per_unit ? u.q.count - q0 : p.per_unit;
+  const int32_t per = static_cast<int32_t>(p.cut.per_tile.d), q0 = u.tile * per;
+  const int32_t queries = u.q.count - q0 < per ? u.q.count - q0 : per;
   for (int r = threadIdx.x >> 5; r < queries * p.group; r += 8) {
     const int64_t first = (static_cast<int64_t>(blockIdx.x) * p.kv_heads + hk) * p.slot_rows + r;
     const int64_t step = static_cast<int64_t>(p.kv_heads) * p.slot_rows;
@@ -459,15 +478,16 @@ struct FwdPlan {
 };
 
 // One tile to a CTA where items are short on average: such a CTA's start and
-// end are most of its life, and two of them share an SM.  Keys are split when
-// the tiles alone leave half of the CTA slots idle: into runs of about
+// end are most of its life, and the others on its SM fill them.  Keys are split
+// when the tiles alone leave half of the CTA slots idle: into runs of about
 // (keys x tiles) / slots, at least 256 keys.
 FwdPlan fwd_plan(const AttnArgs& a, int sms) {
   const int group = a.heads / a.kv_heads, qpt = kRows / group;
   FwdPlan s = {};
   s.tiles = a.n <= a.items * static_cast<int64_t>(kShortItem / kRows * qpt) ? 1 : 2;
+  const int blocks = s.tiles == 2 ? 1 : a.dim <= 64 ? FwdLayout<64, 1>::kBlocks : FwdLayout<128, 1>::kBlocks;
   const int per = s.tiles * qpt;
-  const int64_t tiles = a.n / per + a.items, slots = static_cast<int64_t>(sms) * (3 - s.tiles);
+  const int64_t tiles = a.n / per + a.items, slots = static_cast<int64_t>(sms) * blocks;
   s.units = tiles;
   if (2 * tiles * a.kv_heads > slots) return s;
   const int64_t most = a.n / per + 1;  // tiles of one item, upper bound
@@ -517,24 +537,20 @@ int64_t attn_tc_scratch(const AttnArgs& a, int sms) {
 cudaError_t launch_attn_tc(const AttnArgs& a, void* scratch, int sms, cudaStream_t st) {
   const int group = a.heads / a.kv_heads, qpt = kRows / group;
   const FwdPlan s = fwd_plan(a, sms);
+  const int keys = s.tiles == 1 && a.dim <= 64 ? FwdLayout<64, 1>::kKeys : kRows;
   CUtensorMap maps[3];
   if (!make_map(&maps[0], a.q, a.dtype, a.n, a.heads, a.dim, a.q_stride, group, qpt) ||
-      !make_map(&maps[1], a.k, a.dtype, a.m, a.kv_heads, a.dim, a.k_stride, 1, kRows) ||
-      !make_map(&maps[2], a.v, a.dtype, a.m, a.kv_heads, a.dim, a.v_stride, 1, kRows))
+      !make_map(&maps[1], a.k, a.dtype, a.m, a.kv_heads, a.dim, a.k_stride, 1, keys) ||
+      !make_map(&maps[2], a.v, a.dtype, a.m, a.kv_heads, a.dim, a.v_stride, 1, keys))
     return cudaErrorInvalidValue;
   FwdParams p = {};
-  p.q_off = a.q_off;
-  p.k_off = a.k_off;
-  p.n = a.n;
-  p.m = a.m;
-  p.items = a.items;
+  p.cut = {a.q_off, a.k_off, static_cast<int32_t>(a.n), static_cast<int32_t>(a.m), a.items, s.chunk,
+           divisor(s.tiles * qpt), false};
   p.heads = a.heads;
   p.kv_heads = a.kv_heads;
   p.dim = a.dim;
   p.group = group;
   p.qpt = qpt;
-  p.per_unit = s.tiles * qpt;
-  p.chunk = s.chunk;
   p.slot_rows = s.slot_rows;
   p.c = a.scale * kLog2e;
   p.causal = a.causal;

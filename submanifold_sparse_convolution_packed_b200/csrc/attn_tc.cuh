@@ -34,6 +34,31 @@ __device__ __forceinline__ int32_t keys_seen(const Unit& u, int64_t qi, bool cau
   return s < 0 ? 0 : (s > u.k.count ? u.k.count : static_cast<int32_t>(s));
 }
 
+// Stores 32 columns of a warp's 32 rows, one row per lane in o, through 2 KB of
+// shared memory: a row's 64 bytes leave from four neighbouring lanes, where the
+// lanes' own rows would leave 16 bytes at a time.  `at`: the place of the
+// lane's row in `to` (elements), negative for none.  Warp-collective.
+template <typename T>
+__device__ __forceinline__ void store_rows(uint8_t* stage, const float (&o)[32], T* to, int64_t at, int c0, int dim) {
+  const int lane = threadIdx.x & 31;
+  uint4* s = reinterpret_cast<uint4*>(stage);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)  // pieces swizzled so that eight rows meet eight banks groups
+    s[lane * 4 + (i ^ ((lane >> 1) & 3))] =
+        make_uint4(pack2<T>(o[8 * i], o[8 * i + 1]), pack2<T>(o[8 * i + 2], o[8 * i + 3]),
+                   pack2<T>(o[8 * i + 4], o[8 * i + 5]), pack2<T>(o[8 * i + 6], o[8 * i + 7]));
+  __syncwarp();
+  const int piece = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = i * 8 + (lane >> 2);
+    const int64_t there = __shfl_sync(0xffffffffu, at, row);
+    if (there >= 0 && c0 + 8 * piece < dim)
+      *reinterpret_cast<uint4*>(to + there + c0 + 8 * piece) = s[row * 4 + (piece ^ ((row >> 1) & 3))];
+  }
+  __syncwarp();
+}
+
 // A [rows, heads, dim] tensor as boxes of 64 channels x `bh` heads x `br` rows.
 inline bool make_map(CUtensorMap* map, const void* p, int dtype, int64_t rows, int heads, int dim, const int64_t st[2], int bh,
               int br) {

@@ -126,12 +126,26 @@ struct Span {
   int32_t begin, count;
 };
 
-__device__ __forceinline__ Span item_span(const int32_t* offsets, int item, int64_t n, bool* bad) {
-  const int64_t a = __ldg(offsets + item), b = __ldg(offsets + item + 1);
-  const int64_t lo = a < 0 ? 0 : (a > n ? n : a);
-  const int64_t hi = b < lo ? lo : (b > n ? n : b);
-  if (a < 0 || b < a || b > n) *bad = true;
-  return {static_cast<int32_t>(lo), static_cast<int32_t>(hi - lo)};
+__device__ __forceinline__ Span span_of(int32_t a, int32_t b, int32_t n, bool* bad) {
+  const int32_t lo = min(max(a, 0), n), hi = min(max(b, lo), n);
+  *bad = *bad || a != lo || b != hi;
+  return {lo, hi - lo};
+}
+
+// Division of a count below 2^31 by d, prepared on the host: x / d =
+// x * ceil(2^(31 + s) / d) >> (31 + s) with 2^s >= d.
+struct Divisor {
+  uint32_t d, mul, shift;
+};
+
+inline Divisor divisor(uint32_t d) {
+  uint32_t s = 0;
+  while ((1ull << s) < d) ++s;
+  return {d, static_cast<uint32_t>(((1ull << (31 + s)) + d - 1) / d), 31 + s};
+}
+
+__device__ __forceinline__ uint32_t over(uint32_t x, Divisor d) {
+  return d.d == 1 ? x : static_cast<uint32_t>((static_cast<uint64_t>(x) * d.mul) >> d.shift);
 }
 
 // A block's share: tile `tile` of item `item`'s rows, over the keys of its
@@ -141,59 +155,99 @@ struct Unit {
   Span q, k;
 };
 
-// Units of an item: (tiles of `per_tile` rows) x (splits of `chunk` keys,
-// chunk 0: one split).  tile_k: the tiles cut the keys instead of the queries.
-__device__ __forceinline__ int32_t units_of(Span q, Span k, int per_tile, int chunk, bool tile_k, int32_t* splits) {
-  const int32_t rows = tile_k ? k.count : q.count;
-  const int32_t sp = chunk > 0 && k.count > chunk ? (k.count + chunk - 1) / chunk : 1;
+// How the items' rows are cut into units: tiles of per_tile.d rows (queries, or
+// keys with by_keys) x splits of `chunk` keys (0: one split).
+struct Cut {
+  const int32_t *q_off, *k_off;
+  int32_t n, m;
+  int items, chunk;
+  Divisor per_tile;
+  bool by_keys;
+};
+
+__device__ __forceinline__ int32_t units_of(const Cut& c, Span q, Span k, int32_t* splits) {
+  const uint32_t rows = static_cast<uint32_t>(c.by_keys ? k.count : q.count);
+  int32_t sp = 1;
+  if (c.chunk > 0 && k.count > c.chunk) sp = (k.count + c.chunk - 1) / c.chunk;
   *splits = sp;
-  return (rows / per_tile + (rows % per_tile ? 1 : 0)) * sp;
+  return static_cast<int32_t>(over(rows + c.per_tile.d - 1, c.per_tile)) * sp;
 }
 
 // Finds unit `u` (every thread of the block calls this; the answer is in
-// shared memory).  Each thread adds up the units of a run of items, a block
-// scan numbers the runs, and the thread whose run holds u walks it: one pass
-// over the offsets, about a microsecond for up to a few thousand items, so the
-// host needs no lengths and no table is built.
+// shared memory, after a barrier).  Each thread adds up the units of a run of
+// up to kRun items, whose offsets it loads together; a block scan numbers the
+// runs, and the thread whose run holds u names it: one latency for up to
+// kRun * kThreads items (more take further rounds), so the host needs no
+// lengths and no table is built.  It stands at the start of every block, so
+// its instructions count where items are short.
 template <int kThreads>
-__device__ __forceinline__ void find_unit(const int32_t* q_off, const int32_t* k_off, int items, int64_t n, int64_t m,
-                                          int per_tile, int chunk, bool tile_k, int64_t u, Unit* out, uint32_t* err) {
+__device__ __forceinline__ void find_unit(const Cut& c, int64_t u, Unit* out, uint32_t* err) {
   static_assert(kThreads % 32 == 0, "whole warps");
-  __shared__ int64_t s_warp[kThreads / 32];
+  constexpr int kRun = 4, kWarps = kThreads / 32;
+  __shared__ int64_t s_warp[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int run = (items + kThreads - 1) / kThreads;
-  const int i0 = tid * run < items ? tid * run : items, i1 = i0 + run < items ? i0 + run : items;
   if (tid == 0) out->item = -1;
-  int64_t mine = 0;
-  int32_t sp;
-  bool bad = false;
-  for (int i = i0; i < i1; ++i)
-    mine += units_of(item_span(q_off, i, n, &bad), item_span(k_off, i, m, &bad), per_tile, chunk, tile_k, &sp);
-  int64_t incl = mine;
+  int64_t done = 0;  // units of the rounds before this one
+  for (int first = 0; first < c.items; first += kRun * kThreads) {
+    const int left = c.items - first;
+    const int run = left >= kRun * kThreads ? kRun : (left + kThreads - 1) / kThreads;
+    const int i0 = first + tid * run;
+    int32_t q[kRun + 1], k[kRun + 1], cnt[kRun];
+    int64_t mine = 0;
+    bool bad = false;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) s_warp[warp] = incl;
-  __syncthreads();
-  int64_t before = incl - mine;
-  for (int w = 0; w < warp; ++w) before += s_warp[w];
-  if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(err, kErrRange);
-  if (u >= before && u < before + mine) {
-    int64_t at = before;
-    for (int i = i0; i < i1; ++i) {
-      const Span q = item_span(q_off, i, n, &bad), k = item_span(k_off, i, m, &bad);
-      const int32_t cnt = units_of(q, k, per_tile, chunk, tile_k, &sp);
-      if (u < at + cnt) {
-        const int32_t r = static_cast<int32_t>(u - at);
-        *out = {i, r / sp, r % sp, sp, q, k};
-        break;
+    for (int x = 0; x <= kRun; ++x)
+      if (x <= run && i0 + x <= c.items) {
+        q[x] = __ldg(c.q_off + i0 + x);
+        k[x] = c.q_off == c.k_off ? q[x] : __ldg(c.k_off + i0 + x);
       }
-      at += cnt;
+#pragma unroll
+    for (int x = 0; x < kRun; ++x) {
+      cnt[x] = 0;
+      if (x < run && i0 + x < c.items) {
+        int32_t sp;
+        cnt[x] = units_of(c, span_of(q[x], q[x + 1], c.n, &bad), span_of(k[x], k[x + 1], c.m, &bad), &sp);
+      }
+      if (x < run) mine += cnt[x];
     }
+    int64_t incl = mine;
+    if (first + warp * 32 * run < c.items) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(err, kErrRange);
+    __syncthreads();
+    // the sums of the warps before this one, and of all
+    int64_t before = 0, all = 0;
+    const int busy = (left + 32 * run - 1) / (32 * run) < kWarps ? (left + 32 * run - 1) / (32 * run) : kWarps;
+    for (int w = 0; w < busy; ++w) {
+      const int64_t v = s_warp[w];
+      all += v;
+      if (w < warp) before += v;
+    }
+    int64_t at = done + before + incl - mine;
+    if (u >= at && u < at + mine) {
+#pragma unroll
+      for (int x = 0; x < kRun; ++x) {
+        if (x < run && u >= at && u < at + cnt[x]) {
+          const Span sq = span_of(q[x], q[x + 1], c.n, &bad), sk = span_of(k[x], k[x + 1], c.m, &bad);
+          int32_t sp;
+          units_of(c, sq, sk, &sp);
+          const int32_t r = static_cast<int32_t>(u - at);
+          *out = {i0 + x, r / sp, r % sp, sp, sq, sk};
+        }
+        at += cnt[x];
+      }
+    }
+    done += all;
+    __syncthreads();
+    // block 0 looks at every item, for the error word
+    if (u < done && (blockIdx.x != 0 || blockIdx.y != 0)) break;
   }
-  __syncthreads();
 }
 
 }  // namespace smc
