@@ -4,9 +4,9 @@
 //   P = exp2(S log2e - lse log2e),  dS = P * (dP - delta),  dP = dO V^T
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO
 //
-// Two launches of one kernel.  A CTA keeps 128 rows of two operands in shared
-// memory (queries: Q and dO, for dQ; keys: K and V, for dK and dV) and passes
-// 64 rows of the other two through a ring, so every sum over the passing rows
+// Two launches of one kernel.  A CTA keeps 128 rows of two operands in TMEM (or
+// shared memory; queries: Q and dO, for dQ; keys: K and V, for dK and dV) and
+// passes 64 rows of the other two through a ring in shared memory, so every sum over the passing rows
 // stays in one TMEM accumulator: no atomics, no fp32 copy of dQ in memory, and
 // the same bits every time, at the price of computing S and dP twice (7
 // products instead of 5).  The scores of the dK / dV launch are computed
@@ -45,20 +45,26 @@ struct BwdParams {
   bool causal;
   const float *lse, *delta;  // as k_attn_delta_tc leaves them: -lse log2e (-inf for a row that saw no key), -delta
   const uint32_t* norms;  // fp16: bits of max |dO|^2, max |V|^2
+  const void *a1, *a2;    // the resident operands: Q, dO or K, V
+  int64_t a1s[2], a2s[2];
   void *d1, *d2;          // dQ, -- or dK, dV
   int64_t s1[2], s2[2];
   uint32_t* err;
   uint64_t wait_ns;
 };
 
-template <int DP> struct BwdLayout {
+template <int DP, bool kDQ> struct BwdLayout {
   static constexpr uint32_t kResident = DP / 64 * kPanel, kPass = DP / 64 * kStepPanel;
   static constexpr int kSlots = DP == 64 ? 6 : 4;
-  // TMEM: buffers of S and dP (64 columns each), then the accumulators
-  static constexpr int kBufs = DP == 64 ? 3 : 2;
-  static constexpr uint32_t kAcc = kBufs * 2 * kStep;
-  static_assert(kAcc + 2 * DP <= 512, "accumulators fit");
-  static constexpr uint32_t kA = 0, kB = 2 * kResident, kRowVals = kB + kSlots * 2 * kPass;
+  // TMEM: buffers of S and dP (64 columns each), the accumulators and, where
+  // there is room, the resident operands as 16-bit pairs.  From TMEM they cost
+  // no shared-memory reads: with 64-column products those reads alone took 48
+  // clocks an MMA where the MMA takes 32, and more beside the other traffic.
+  static constexpr bool kTmemA = kDQ || DP == 64;
+  static constexpr int kBufs = kDQ && DP == 64 ? 3 : 2;
+  static constexpr uint32_t kAcc = kBufs * 2 * kStep, kAt = kAcc + (kDQ ? 1 : 2) * DP;
+  static_assert(kAt + (kTmemA ? DP : 0) <= 512, "TMEM columns");
+  static constexpr uint32_t kA = 0, kB = kTmemA ? 0 : 2 * kResident, kRowVals = kB + kSlots * 2 * kPass;
   static constexpr uint32_t kBar = kRowVals + kSlots * 2 * kStep * 4;
   // barriers: resident, full[kSlots], empty[kSlots], s[kBufs], p[kBufs], out, tail
   static constexpr uint32_t kMisc = kBar + 8 * (2 * kSlots + 2 * kBufs + 3), kTotal = kMisc + 32 + 1024;
@@ -79,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_attn_bwd_tc(const __grid_constant__ CUtensorMap a1map, const __grid_constant__ CUtensorMap a2map,
                   const __grid_constant__ CUtensorMap b1map, const __grid_constant__ CUtensorMap b2map,
                   const BwdParams p) {
-  using L = BwdLayout<DP>;
+  using L = BwdLayout<DP, kDQ>;
   constexpr int kSlots = L::kSlots, kPanels = DP / 64, kBufs = L::kBufs;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr float kShift = kBf16 || kDQ ? 0.f : 14.f;  // P carries 2^kShift
@@ -118,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&a2map);
     prefetch_tmap(&b1map);
     prefetch_tmap(&b2map);
-    mbar_init(bar_a, 1);
+    mbar_init(bar_a, L::kTmemA ? 16 : 1);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar_full + 8 * s, kDQ ? 1 : 33);
       mbar_init(bar_empty + 8 * s, 1);
@@ -153,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 17) {
     // ------------------------------------------------------------- TMA loads
     if (nsteps > 0) {
-      if (lane == 0) {
+      if (!L::kTmemA && lane == 0) {
         const uint32_t rows = kDQ ? p.group * p.qpt : kRows;
         mbar_arrive_expect_tx(bar_a, 2 * kPanels * rows * 128u);
         const int head = kDQ ? hk * p.group : hk, row = (kDQ ? u.q.begin : u.k.begin) + r0;
@@ -232,9 +238,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int k = 0; k < DP / 16; ++k)
-            if (k < ks)
-              umma_f16(d + x * kStep, a1 + x * kSecondA + (k >> 2) * (kPanel >> 4) + 2 * (k & 3),
-                       b + x * kSecond + (k >> 2) * (kStepPanel >> 4) + 2 * (k & 3), idesc_s, k > 0);
+            if (k < ks) {
+              const uint64_t bk = b + x * kSecond + (k >> 2) * (kStepPanel >> 4) + 2 * (k & 3);
+              if (L::kTmemA)
+                umma_f16_ts(d + x * kStep, tmem + L::kAt + x * (DP / 2) + 8 * k, bk, idesc_s, k > 0);
+              else
+                umma_f16(d + x * kStep, a1 + x * kSecondA + (k >> 2) * (kPanel >> 4) + 2 * (k & 3), bk, idesc_s, k > 0);
+            }
         umma_commit(bar);
       }
       __syncwarp();
@@ -302,7 +312,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t first = static_cast<int64_t>(r0) + r + u.q.count - u.k.count;  // the first query that sees this key
       lim = first < 0 ? 0 : static_cast<int32_t>(first < u.q.count ? first : u.q.count) * p.group;
     }
-    int slot = par, b = par;
+    if (L::kTmemA) {  // this thread's row of the resident operands: 32 words for each of the DP / 32 groups
+      if (w < DP / 32) {
+        constexpr int kPer = DP / 64;  // groups to an operand
+        const bool second = w / kPer == 1;
+        const int c0 = (w % kPer) * 64;
+        const int64_t* st = second ? p.a2s : p.a1s;
+        const int64_t at = kDQ ? (static_cast<int64_t>(u.q.begin) + r0 + qi) * st[0] + (hk * p.group + r % p.group) * st[1]
+                               : (static_cast<int64_t>(u.k.begin) + r0 + r) * st[0] + hk * st[1];
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(second ? p.a2 : p.a1) + (row ? at + c0 : 0));
+        uint32_t v[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 x = row && c0 + 8 * i < p.dim ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+          v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+        }
+        __syncwarp();
+        tmem_st(tmem + lanes + L::kAt + (second ? DP / 2 : 0) + c0 / 2, v);
+        tmem_st_wait();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_a);
+      __syncwarp();
+    }
+    int slot = par, b = par % kBufs;
     uint32_t fparity = 0, sparity = 0;
     bool ok = true;
     for (int j = par; j < nsteps; j += 2) {
@@ -314,51 +348,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const uint32_t buf = tmem + lanes + b * 2 * kStep;
-      float s[32], d[32];
-      tmem_ld(buf + 32 * half, s);
-      tmem_ld(buf + kStep + 32 * half, d);
-      uint32_t wp[16], ws[16];
       const int32_t b0 = b_lo + j * per_step;
       // columns [from, to) of this thread's 32 count
       const int from = kDQ ? 0 : lim - b0 * p.group - 32 * half, to = kDQ ? lim - b0 - 32 * half : 32;
       const bool whole = __all_sync(0xffffffffu, from <= 0 && to >= 32);
       const float4* vl = reinterpret_cast<const float4*>(smem + L::kRowVals + slot * 8 * kStep) + 8 * half;
+      // 16 columns at a time: with all 32 in registers there were none left to
+      // work on more than one group of four at once
 #pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        float4 l4 = make_float4(l, l, l, l), e4 = make_float4(e, e, e, e);
-        if (!kDQ) {
-          l4 = vl[i / 4];
-          e4 = vl[kStep / 4 + i / 4];
-          if (kShift != 0.f) l4 = make_float4(l4.x + kShift, l4.y + kShift, l4.z + kShift, l4.w + kShift);
+      for (int part = 0; part < 2; ++part) {
+        float s[16], d[16];
+        tmem_ld2(buf + 32 * half + 16 * part, s, buf + kStep + 32 * half + 16 * part, d);
+        uint32_t wp[8], ws[8];
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          float4 l4 = make_float4(l, l, l, l), e4 = make_float4(e, e, e, e);
+          if (!kDQ) {
+            l4 = vl[4 * part + i / 4];
+            e4 = vl[kStep / 4 + 4 * part + i / 4];
+            if (kShift != 0.f) l4 = make_float4(l4.x + kShift, l4.y + kShift, l4.z + kShift, l4.w + kShift);
+          }
+          const float2 x0 = fma2(make_float2(s[i], s[i + 1]), c2, make_float2(l4.x, l4.y));
+          const float2 x1 = fma2(make_float2(s[i + 2], s[i + 3]), c2, make_float2(l4.z, l4.w));
+          float2 p0 = make_float2(exp2_fast(x0.x), exp2_fast(x0.y)), p1 = make_float2(exp2_fast(x1.x), exp2_fast(x1.y));
+          float2 d0 = add2(make_float2(d[i], d[i + 1]), make_float2(e4.x, e4.y));
+          float2 d1 = add2(make_float2(d[i + 2], d[i + 3]), make_float2(e4.z, e4.w));
+          if (!kBf16) {  // exact: a power of two
+            d0 = mul2(d0, f2);
+            d1 = mul2(d1, f2);
+          }
+          d0 = mul2(p0, d0);
+          d1 = mul2(p1, d1);
+          if (!whole) {
+            auto keep = [&](int x, float v) { return 16 * part + i + x >= from && 16 * part + i + x < to ? v : 0.f; };
+            p0 = make_float2(keep(0, p0.x), keep(1, p0.y));
+            p1 = make_float2(keep(2, p1.x), keep(3, p1.y));
+            d0 = make_float2(keep(0, d0.x), keep(1, d0.y));
+            d1 = make_float2(keep(2, d1.x), keep(3, d1.y));
+          }
+          if (!kDQ) {
+            wp[i / 2] = pack2<T>(p0.x, p0.y);
+            wp[i / 2 + 1] = pack2<T>(p1.x, p1.y);
+          }
+          ws[i / 2] = pack2<T>(d0.x, d0.y);
+          ws[i / 2 + 1] = pack2<T>(d1.x, d1.y);
         }
-        const float2 x0 = fma2(make_float2(s[i], s[i + 1]), c2, make_float2(l4.x, l4.y));
-        const float2 x1 = fma2(make_float2(s[i + 2], s[i + 3]), c2, make_float2(l4.z, l4.w));
-        float2 p0 = make_float2(exp2_fast(x0.x), exp2_fast(x0.y)), p1 = make_float2(exp2_fast(x1.x), exp2_fast(x1.y));
-        float2 d0 = add2(make_float2(d[i], d[i + 1]), make_float2(e4.x, e4.y));
-        float2 d1 = add2(make_float2(d[i + 2], d[i + 3]), make_float2(e4.z, e4.w));
-        if (!kBf16) {  // exact: a power of two
-          d0 = mul2(d0, f2);
-          d1 = mul2(d1, f2);
-        }
-        d0 = mul2(p0, d0);
-        d1 = mul2(p1, d1);
-        if (!whole) {
-          auto keep = [&](int x, float v) { return i + x >= from && i + x < to ? v : 0.f; };
-          p0 = make_float2(keep(0, p0.x), keep(1, p0.y));
-          p1 = make_float2(keep(2, p1.x), keep(3, p1.y));
-          d0 = make_float2(keep(0, d0.x), keep(1, d0.y));
-          d1 = make_float2(keep(2, d1.x), keep(3, d1.y));
-        }
-        if (!kDQ) {
-          wp[i / 2] = pack2<T>(p0.x, p0.y);
-          wp[i / 2 + 1] = pack2<T>(p1.x, p1.y);
-        }
-        ws[i / 2] = pack2<T>(d0.x, d0.y);
-        ws[i / 2 + 1] = pack2<T>(d1.x, d1.y);
+        // over this thread's own scores, already read: the other half's may not be
+        if (!kDQ) tmem_st(buf + 32 * half + 8 * part, wp);
+        tmem_st(buf + kStep + 32 * half + 8 * part, ws);
       }
-      // over this thread's own scores: the other half's may not be read yet
-      if (!kDQ) tmem_st(buf + 32 * half, wp);
-      tmem_st(buf + kStep + 32 * half, ws);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -488,16 +526,26 @@ cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const CUtensorMap* maps
     if (e != cudaSuccess) return e;
   }
   k_attn_delta_tc<T, DP / 8><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, lse2, norms);
-  constexpr int kSmem = static_cast<int>(BwdLayout<DP>::kTotal);
+  constexpr int kSmemQ = static_cast<int>(BwdLayout<DP, true>::kTotal), kSmemK = static_cast<int>(BwdLayout<DP, false>::kTotal);
   auto kq = k_attn_bwd_tc<T, DP, true>;
   auto kk = k_attn_bwd_tc<T, DP, false>;
-  cudaError_t e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemQ);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemK);
   if (e != cudaSuccess) return e;
+  auto resident = [&](const void* x, const int64_t xs[2], const void* y, const int64_t ys[2]) {
+    p.a1 = x;
+    p.a2 = y;
+    for (int i = 0; i < 2; ++i) {
+      p.a1s[i] = xs[i];
+      p.a2s[i] = ys[i];
+    }
+  };
+  resident(a.q, a.q_stride, a.dout, a.dout_stride);
   p.d1 = a.dq;
   for (int i = 0; i < 2; ++i) p.s1[i] = a.dq_stride[i];
-  kq<<<dim3(static_cast<unsigned>(a.n / p.qpt + a.items), a.kv_heads), kThreads, kSmem, st>>>(maps[0], maps[1], maps[2],
-                                                                                             maps[3], p);
+  kq<<<dim3(static_cast<unsigned>(a.n / p.qpt + a.items), a.kv_heads), kThreads, kSmemQ, st>>>(maps[0], maps[1], maps[2],
+                                                                                              maps[3], p);
+  resident(a.k, a.k_stride, a.v, a.v_stride);
   p.cut.per_tile = divisor(kRows);
   p.cut.by_keys = true;
   p.d1 = a.dk;
@@ -506,8 +554,8 @@ cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const CUtensorMap* maps
     p.s1[i] = a.dk_stride[i];
     p.s2[i] = a.dv_stride[i];
   }
-  kk<<<dim3(static_cast<unsigned>(a.m / kRows + a.items), a.kv_heads), kThreads, kSmem, st>>>(maps[4], maps[5], maps[6],
-                                                                                              maps[7], p);
+  kk<<<dim3(static_cast<unsigned>(a.m / kRows + a.items), a.kv_heads), kThreads, kSmemK, st>>>(maps[4], maps[5], maps[6],
+                                                                                               maps[7], p);
   count_launches(3);
   return cudaGetLastError();
 }

@@ -19,6 +19,22 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[16]) {
       : "memory");
 }
 
+// The same from two places, with one wait.
+__device__ __forceinline__ void tmem_ld2(uint32_t a0, float (&v)[16], uint32_t a1, float (&u)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&f"(v[0]), "=&f"(v[1]), "=&f"(v[2]), "=&f"(v[3]), "=&f"(v[4]), "=&f"(v[5]), "=&f"(v[6]), "=&f"(v[7]),
+        "=&f"(v[8]), "=&f"(v[9]), "=&f"(v[10]), "=&f"(v[11]), "=&f"(v[12]), "=&f"(v[13]), "=&f"(v[14]), "=&f"(v[15]),
+        "=&f"(u[0]), "=&f"(u[1]), "=&f"(u[2]), "=&f"(u[3]), "=&f"(u[4]), "=&f"(u[5]), "=&f"(u[6]), "=&f"(u[7]),
+        "=&f"(u[8]), "=&f"(u[9]), "=&f"(u[10]), "=&f"(u[11]), "=&f"(u[12]), "=&f"(u[13]), "=&f"(u[14]), "=&f"(u[15])
+      : "r"(a0), "r"(a1)
+      : "memory");
+}
+
 // 32 consecutive fp32 columns of this warp's 32 TMEM lanes, one lane per thread.
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[32]) {
   asm volatile(
@@ -85,6 +101,15 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[128]) {
         "=f"(v[112]), "=f"(v[113]), "=f"(v[114]), "=f"(v[115]), "=f"(v[116]), "=f"(v[117]), "=f"(v[118]), "=f"(v[119]),
         "=f"(v[120]), "=f"(v[121]), "=f"(v[122]), "=f"(v[123]), "=f"(v[124]), "=f"(v[125]), "=f"(v[126]), "=f"(v[127])
       : "r"(taddr)
+      : "memory");
+}
+
+// 8 consecutive 32-bit columns of this warp's lanes written; wait with tmem_st_wait.
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+      ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
       : "memory");
 }
 
