@@ -15,10 +15,10 @@
 // lie; Q, dO, K are read a second time from the same shared memory, MN-major.
 //   warp 17    TMA: the resident tiles once, then the passing ones, with the
 //              lse and delta of their rows (dK / dV, cp.async);
-//   warp 16    tcgen05.mma: S and dP of step j + 1 are issued before
-//              the products of step j, into the other of two TMEM buffers;
-//   warps 0-15 P and dS, one thread per row and half of the step's columns:
-//              eight warps each for even and odd steps.
+//   warp 16    tcgen05.mma: behind the products of step j, S and dP of the step
+//              that takes over its TMEM buffer (two or three steps ahead), as
+//              one batch: this warp's waits are what there is to save;
+//   warps 0-15 P and dS, one thread per row and 16 of the step's 64 columns.
 // fp16: P carries a factor 2^14 and dS a power of two taken from the largest
 // norms of dO and V rows (|dP|, |delta| <= |dO| |V|), undone on the fp32
 // accumulators, so that the P of a long context do not fall below fp16's
@@ -64,6 +64,7 @@ template <int DP, bool kDQ> struct BwdLayout {
   static constexpr int kBufs = kDQ && DP == 64 ? 3 : 2;
   static constexpr uint32_t kAcc = kBufs * 2 * kStep, kAt = kAcc + (kDQ ? 1 : 2) * DP;
   static_assert(kAt + (kTmemA ? DP : 0) <= 512, "TMEM columns");
+  static_assert(kBufs < kSlots, "the first steps' loads need no waiting for slots");
   static constexpr uint32_t kA = 0, kB = kTmemA ? 0 : 2 * kResident, kRowVals = kB + kSlots * 2 * kPass;
   static constexpr uint32_t kBar = kRowVals + kSlots * 2 * kStep * 4;
   // barriers: resident, full[kSlots], empty[kSlots], s[kBufs], p[kBufs], out, tail
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < kBufs; ++t) {
       mbar_init(bar_s + 8 * t, 1);
-      mbar_init(bar_p + 8 * t, 8);
+      mbar_init(bar_p + 8 * t, 16);
     }
     mbar_init(bar_o, 1);
     mbar_init(bar_tail, 1);
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t parity = 1;
       const int head = kDQ ? hk : hk * p.group, base_row = kDQ ? u.k.begin : u.q.begin;
       for (int j = 0; j < nsteps; ++j) {
-        if (!__all_sync(0xffffffffu, mbar_wait_short(bar_empty + 8 * slot, parity, p.err, p.wait_ns))) break;
+        if (!mbar_wait_warp(bar_empty + 8 * slot, parity, p.err, p.wait_ns)) break;
         const int32_t b0 = b_lo + j * per_step;
         const int rows = (b_hi - b0 < per_step ? b_hi - b0 : per_step) * (kDQ ? 1 : p.group);
         // in the dQ launch b_hi may be the causal limit: rows behind it are the item's own, but not seen
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           cp_async_arrive(bar_full + 8 * slot);
         }
         if (tail) {  // once, at the last step: rows that are not the item's may hold NaN
-          if (!__all_sync(0xffffffffu, mbar_wait_short(bar_tail, 0, p.err, p.wait_ns))) break;
+          if (!mbar_wait_warp(bar_tail, 0, p.err, p.wait_ns)) break;
           for (int c = 0; c < 2 * kPanels; ++c) {
             uint4* base = reinterpret_cast<uint4*>(smem + L::kB + slot * 2 * L::kPass + c * kStepPanel);
             for (int i = rows * 8 + lane; i < rows_step * 8; i += 32) base[i] = make_uint4(0, 0, 0, 0);
@@ -227,63 +228,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t a1 = kmajor_desc(sbase + L::kA, 128);
     const uint64_t b1 = kmajor_desc(sbase + L::kB, 128), n1 = mnmajor_desc(sbase + L::kB, kStepPanel);
     constexpr uint64_t kSecondA = L::kResident >> 4, kSecond = L::kPass >> 4, kSlot = 2 * kSecond;
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-      const bool w = __all_sync(0xffffffffu, mbar_wait_short(bar, parity, p.err, p.wait_ns));
+    auto wait2 = [&](uint32_t bar, uint32_t parity, uint32_t bar2, uint32_t parity2) {
+      const bool w = mbar_wait_warp(bar, parity, p.err, p.wait_ns) && mbar_wait_warp(bar2, parity2, p.err, p.wait_ns);
       tc_fence_after();
       return w;
     };
-    auto scores = [&](uint32_t d, uint64_t b, uint32_t bar) {  // S and dP of a step
-      if (elect_one()) {
+    auto scores = [&](uint32_t d, uint64_t b, uint32_t bar) {  // S and dP of a step, in the elected lane
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int k = 0; k < DP / 16; ++k)
-            if (k < ks) {
-              const uint64_t bk = b + x * kSecond + (k >> 2) * (kStepPanel >> 4) + 2 * (k & 3);
-              if (L::kTmemA)
-                umma_f16_ts(d + x * kStep, tmem + L::kAt + x * (DP / 2) + 8 * k, bk, idesc_s, k > 0);
-              else
-                umma_f16(d + x * kStep, a1 + x * kSecondA + (k >> 2) * (kPanel >> 4) + 2 * (k & 3), bk, idesc_s, k > 0);
-            }
-        umma_commit(bar);
-      }
-      __syncwarp();
+        for (int k = 0; k < DP / 16; ++k)
+          if (k < ks) {
+            const uint64_t bk = b + x * kSecond + (k >> 2) * (kStepPanel >> 4) + 2 * (k & 3);
+            if (L::kTmemA)
+              umma_f16_ts(d + x * kStep, tmem + L::kAt + x * (DP / 2) + 8 * k, bk, idesc_s, k > 0);
+            else
+              umma_f16(d + x * kStep, a1 + x * kSecondA + (k >> 2) * (kPanel >> 4) + 2 * (k & 3), bk, idesc_s, k > 0);
+          }
+      umma_commit(bar);
     };
-    bool ok = nsteps > 0 && wait(bar_a, 0);
-    // S and dP run kBufs - 1 steps ahead of the products: step j + kBufs - 1 goes
-    // into the buffer whose P and dS the products of step j - 1 have read.
-    int slot = 0, buf = 0, aslot = 0, abuf = 0;
+    bool ok = nsteps > 0;
+    // step j + kBufs (aslot) takes over the buffer of step j (slot, buf)
+    int slot = 0, buf = 0, aslot = 0;
     uint32_t pparity = 0, aparity = 0;
-    auto ahead = [&]() {
-      if (!wait(bar_full + 8 * aslot, aparity)) return false;
-      scores(tmem + abuf * 2 * kStep, b1 + aslot * kSlot, bar_s + 8 * abuf);
-      if (++aslot == kSlots) {
-        aslot = 0;
-        aparity ^= 1;
-      }
-      if (++abuf == kBufs) abuf = 0;
-      return true;
-    };
-    for (int j = 0; j < kBufs - 1 && j < nsteps && ok; ++j) ok = ahead();
+    for (int j = 0; j < kBufs && j < nsteps && ok; ++j) {
+      ok = wait2(bar_full + 8 * aslot, 0, bar_a, 0);
+      if (ok && elect_one()) scores(tmem + j * 2 * kStep, b1 + aslot * kSlot, bar_s + 8 * j);
+      __syncwarp();
+      ++aslot;
+    }
     for (int j = 0; j < nsteps && ok; ++j) {
-      if (j + kBufs - 1 < nsteps && !ahead()) break;
-      if (!wait(bar_p + 8 * buf, pparity)) break;
+      const bool more = j + kBufs < nsteps;
+      ok = wait2(bar_p + 8 * buf, pparity, more ? bar_full + 8 * aslot : bar_a, more ? aparity : 0);
       const uint32_t d = tmem + buf * 2 * kStep;
       const uint64_t at = n1 + slot * kSlot;
-      if (elect_one()) {
+      if (ok && elect_one()) {
         if (!kDQ) {
 #pragma unroll
           for (int k = 0; k < kStep / 16; ++k)
-            umma_f16_ts(tmem + L::kAcc + DP, d + 8 * k + 16 * (k >> 1), at + kSecond + 128 * k, idesc_o, j > 0 || k > 0);
+            umma_f16_ts(tmem + L::kAcc + DP, d + 16 * k, at + kSecond + 128 * k, idesc_o, j > 0 || k > 0);
         }
 #pragma unroll
         for (int k = 0; k < kStep / 16; ++k)
-          umma_f16_ts(tmem + L::kAcc, d + kStep + 8 * k + 16 * (k >> 1), at + 128 * k, idesc_o, j > 0 || k > 0);
+          umma_f16_ts(tmem + L::kAcc, d + kStep + 16 * k, at + 128 * k, idesc_o, j > 0 || k > 0);
         if (j + kSlots < nsteps) umma_commit(bar_empty + 8 * slot);
+        if (more) scores(d, b1 + aslot * kSlot, bar_s + 8 * buf);
         if (j + 1 == nsteps) umma_commit(bar_o);
       }
       __syncwarp();
       if (++slot == kSlots) slot = 0;
+      if (++aslot == kSlots) {
+        aslot = 0;
+        aparity ^= 1;
+      }
       if (++buf == kBufs) {
         buf = 0;
         pparity ^= 1;
@@ -291,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------------------------------------------------------- P, dS
-    // w & 1: even or odd steps; w >> 1: columns 0-31 or 32-63 of them
+    // columns 16 w .. 16 w + 15 of every step; par, half: of the results
     const int w = warp >> 2, r = (warp & 3) * 32 + lane, par = w & 1, half = w >> 1;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float factor = ds_factor(p.norms);
@@ -336,84 +333,82 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar_a);
       __syncwarp();
     }
-    int slot = par, b = par % kBufs;
+    int slot = 0, b = 0;
     uint32_t fparity = 0, sparity = 0;
-    bool ok = true;
-    for (int j = par; j < nsteps; j += 2) {
-      if (!kDQ) ok = mbar_wait_short(bar_full + 8 * slot, fparity, p.err, p.wait_ns);  // the rows' values
-      ok = ok && mbar_wait_short(bar_s + 8 * b, sparity, p.err, p.wait_ns);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
+    bool ok = true, ready = false;  // ready: this step's scores were there before the last step's were worked on
+    for (int j = 0; j < nsteps; ++j) {
+      if (!__all_sync(0xffffffffu, ready)) {
+        if (!kDQ) ok = mbar_wait_warp(bar_full + 8 * slot, fparity, p.err, p.wait_ns);  // the rows' values
+        ok = ok && mbar_wait_warp(bar_s + 8 * b, sparity, p.err, p.wait_ns);
+        if (!ok) break;
       }
       tc_fence_after();
-      const uint32_t buf = tmem + lanes + b * 2 * kStep;
+      const uint32_t buf = tmem + lanes + b * 2 * kStep, bar = bar_p + 8 * b;
+      const float4* vl = reinterpret_cast<const float4*>(smem + L::kRowVals + slot * 8 * kStep) + 4 * w;
       const int32_t b0 = b_lo + j * per_step;
-      // columns [from, to) of this thread's 32 count
-      const int from = kDQ ? 0 : lim - b0 * p.group - 32 * half, to = kDQ ? lim - b0 - 32 * half : 32;
-      const bool whole = __all_sync(0xffffffffu, from <= 0 && to >= 32);
-      const float4* vl = reinterpret_cast<const float4*>(smem + L::kRowVals + slot * 8 * kStep) + 8 * half;
-      // 16 columns at a time: with all 32 in registers there were none left to
-      // work on more than one group of four at once
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        float s[16], d[16];
-        tmem_ld2(buf + 32 * half + 16 * part, s, buf + kStep + 32 * half + 16 * part, d);
-        uint32_t wp[8], ws[8];
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          float4 l4 = make_float4(l, l, l, l), e4 = make_float4(e, e, e, e);
-          if (!kDQ) {
-            l4 = vl[4 * part + i / 4];
-            e4 = vl[kStep / 4 + 4 * part + i / 4];
-            if (kShift != 0.f) l4 = make_float4(l4.x + kShift, l4.y + kShift, l4.z + kShift, l4.w + kShift);
-          }
-          const float2 x0 = fma2(make_float2(s[i], s[i + 1]), c2, make_float2(l4.x, l4.y));
-          const float2 x1 = fma2(make_float2(s[i + 2], s[i + 3]), c2, make_float2(l4.z, l4.w));
-          float2 p0 = make_float2(exp2_fast(x0.x), exp2_fast(x0.y)), p1 = make_float2(exp2_fast(x1.x), exp2_fast(x1.y));
-          float2 d0 = add2(make_float2(d[i], d[i + 1]), make_float2(e4.x, e4.y));
-          float2 d1 = add2(make_float2(d[i + 2], d[i + 3]), make_float2(e4.z, e4.w));
-          if (!kBf16) {  // exact: a power of two
-            d0 = mul2(d0, f2);
-            d1 = mul2(d1, f2);
-          }
-          d0 = mul2(p0, d0);
-          d1 = mul2(p1, d1);
-          if (!whole) {
-            auto keep = [&](int x, float v) { return 16 * part + i + x >= from && 16 * part + i + x < to ? v : 0.f; };
-            p0 = make_float2(keep(0, p0.x), keep(1, p0.y));
-            p1 = make_float2(keep(2, p1.x), keep(3, p1.y));
-            d0 = make_float2(keep(0, d0.x), keep(1, d0.y));
-            d1 = make_float2(keep(2, d1.x), keep(3, d1.y));
-          }
-          if (!kDQ) {
-            wp[i / 2] = pack2<T>(p0.x, p0.y);
-            wp[i / 2 + 1] = pack2<T>(p1.x, p1.y);
-          }
-          ws[i / 2] = pack2<T>(d0.x, d0.y);
-          ws[i / 2 + 1] = pack2<T>(d1.x, d1.y);
-        }
-        // over this thread's own scores, already read: the other half's may not be
-        if (!kDQ) tmem_st(buf + 32 * half + 8 * part, wp);
-        tmem_st(buf + kStep + 32 * half + 8 * part, ws);
+      // columns [from, to) of this thread's 16 count
+      const int from = kDQ ? 0 : lim - b0 * p.group - 16 * w, to = kDQ ? lim - b0 - 16 * w : 16;
+      const bool whole = __all_sync(0xffffffffu, from <= 0 && to >= 16);
+      float s[16], d[16];
+      tmem_ld2(buf + 16 * w, s, buf + kStep + 16 * w, d);
+      // Look for the next step's now: the answer arrives while these are worked on
+      // (a wait costs this loop about 200 clocks even on a complete barrier).
+      if (++b == kBufs) {
+        b = 0;
+        sparity ^= 1;
       }
+      if (++slot == kSlots) {
+        slot = 0;
+        fparity ^= 1;
+      }
+      ready = mbar_test(bar_s + 8 * b, sparity);
+      if (!kDQ) ready = ready && mbar_test(bar_full + 8 * slot, fparity);
+      uint32_t wp[8], ws[8];
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        float4 l4 = make_float4(l, l, l, l), e4 = make_float4(e, e, e, e);
+        if (!kDQ) {
+          l4 = vl[i / 4];
+          e4 = vl[kStep / 4 + i / 4];
+          if (kShift != 0.f) l4 = make_float4(l4.x + kShift, l4.y + kShift, l4.z + kShift, l4.w + kShift);
+        }
+        const float2 x0 = fma2(make_float2(s[i], s[i + 1]), c2, make_float2(l4.x, l4.y));
+        const float2 x1 = fma2(make_float2(s[i + 2], s[i + 3]), c2, make_float2(l4.z, l4.w));
+        float2 p0 = make_float2(exp2_fast(x0.x), exp2_fast(x0.y)), p1 = make_float2(exp2_fast(x1.x), exp2_fast(x1.y));
+        float2 d0 = add2(make_float2(d[i], d[i + 1]), make_float2(e4.x, e4.y));
+        float2 d1 = add2(make_float2(d[i + 2], d[i + 3]), make_float2(e4.z, e4.w));
+        if (!kBf16) {  // exact: a power of two
+          d0 = mul2(d0, f2);
+          d1 = mul2(d1, f2);
+        }
+        d0 = mul2(p0, d0);
+        d1 = mul2(p1, d1);
+        if (!whole) {
+          auto keep = [&](int x, float v) { return i + x >= from && i + x < to ? v : 0.f; };
+          p0 = make_float2(keep(0, p0.x), keep(1, p0.y));
+          p1 = make_float2(keep(2, p1.x), keep(3, p1.y));
+          d0 = make_float2(keep(0, d0.x), keep(1, d0.y));
+          d1 = make_float2(keep(2, d1.x), keep(3, d1.y));
+        }
+        if (!kDQ) {
+          wp[i / 2] = pack2<T>(p0.x, p0.y);
+          wp[i / 2 + 1] = pack2<T>(p1.x, p1.y);
+        }
+        ws[i / 2] = pack2<T>(d0.x, d0.y);
+        ws[i / 2 + 1] = pack2<T>(d1.x, d1.y);
+      }
+      // over this thread's own scores: the others' may not be read yet
+      if (!kDQ) tmem_st(buf + 16 * w, wp);
+      tmem_st(buf + kStep + 16 * w, ws);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_p + 8 * b);
+      if (lane == 0) mbar_arrive(bar);
       __syncwarp();
-      if ((b += 2) >= kBufs) {
-        b -= kBufs;
-        sparity ^= 1;
-      }
-      if ((slot += 2) >= kSlots) {
-        slot -= kSlots;
-        fparity ^= 1;
-      }
     }
     // --------------------------------------------------------------- results
     if (ok && nsteps > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait_short(bar_o, 0, p.err, p.wait_ns));
+      ok = mbar_wait_warp(bar_o, 0, p.err, p.wait_ns);
       tc_fence_after();
     }
     if (ok) {

@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
       int slot = 0;
       uint32_t parity = 1;
       for (int i = 0; i < 2 * nsteps; ++i) {
-        if (!__all_sync(0xffffffffu, mbar_wait_short(bar_empty + 8 * slot, parity, p.err, p.wait_ns))) break;
+        if (!mbar_wait_warp(bar_empty + 8 * slot, parity, p.err, p.wait_ns)) break;
         const int32_t key = k_lo + (i >> 1) * kKeys;
         const int rows = u.k.count - key;  // V rows behind the item's end are zeroed below
         const bool tail = (i & 1) && rows < kKeys;
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
         }
         __syncwarp();
         if (tail) {  // once, at the last step
-          if (!__all_sync(0xffffffffu, mbar_wait_short(bar_tail, 0, p.err, p.wait_ns))) break;
+          if (!mbar_wait_warp(bar_tail, 0, p.err, p.wait_ns)) break;
           uint4* base = reinterpret_cast<uint4*>(smem + L::kKv + slot * L::kKvBytes);
           for (int c = 0; c < kPanels; ++c)
             for (int j = rows * 8 + lane; j < kKeys * 8; j += 32) base[c * (L::kKvPanel / 16) + j] = make_uint4(0, 0, 0, 0);
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
     const uint64_t q = kmajor_desc(sbase + L::kQ, 128) + t * (L::kQBytes >> 4), kd = kmajor_desc(sbase + L::kKv, 128);
     const uint64_t vd = mnmajor_desc(sbase + L::kKv, L::kKvPanel);
     auto wait = [&](uint32_t bar, uint32_t parity) {
-      const bool w = __all_sync(0xffffffffu, mbar_wait_short(bar, parity, p.err, p.wait_ns));
+      const bool w = mbar_wait_warp(bar, parity, p.err, p.wait_ns);
       tc_fence_after();
       return w;
     };
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
     float top = -INFINITY, sum = 0.f;  // top: the rounded product with c the sums refer to
     bool ok = true;
     for (int j = 0; j < steps[t]; ++j) {
-      ok = __all_sync(0xffffffffu, mbar_wait_short(bar_s + 8 * g, j & 1, p.err, p.wait_ns));
+      ok = mbar_wait_warp(bar_s + 8 * g, j & 1, p.err, p.wait_ns);
       if (!ok) break;
       tc_fence_after();
       if (used) {
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
       top = m;
     }
     if (ok && steps[t] > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait_short(bar_o + 8 * t, 0, p.err, p.wait_ns));
+      ok = mbar_wait_warp(bar_o + 8 * t, 0, p.err, p.wait_ns);
       tc_fence_after();
     }
     if (ok && used) {

@@ -184,6 +184,24 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, u
   return true;
 }
 
+// The same for a whole converged warp.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint32_t* err, uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, mbar_wait_short(bar, parity, err, limit_ns));
+}
+
+// Whether the phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Four bytes from global to shared memory, asynchronously; zero when !there.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
