@@ -330,18 +330,18 @@ int smc_attention_backward(const void* dout, const int64_t dout_stride[2], const
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  // scratch: delta and the scaled lse, [n, heads] each, and two words
+  // scratch: delta and the scaled lse, [n, heads] each, two words, partial sums
+  const bool tc = smc::attn_bwd_tc_supported(a);
+  const int64_t count = n * heads, part = (2 * count + 2 + 63) / 64 * 64;
+  const int64_t floats = tc ? part + smc::attn_bwd_tc_scratch(a, dev.sms) : count;
   void* scratch = nullptr;
-  const size_t count = static_cast<size_t>(n) * heads;
-  if (n > 0 && smc::scratch_alloc(&scratch, (2 * count + 2) * sizeof(float), dev.id, s) != cudaSuccess) {
+  if (n > 0 && smc::scratch_alloc(&scratch, static_cast<size_t>(floats) * sizeof(float), dev.id, s) != cudaSuccess) {
     cudaGetLastError();
     return SMC_E_OOM;
   }
   a.delta = static_cast<float*>(scratch);
-  const cudaError_t e = smc::attn_bwd_tc_supported(a)
-                            ? smc::launch_attn_bwd_tc(a, a.delta + count, reinterpret_cast<uint32_t*>(a.delta + 2 * count),
-                                                      dev.sms, s)
-                            : smc::launch_attn_simt(a, true, s);
+  const smc::BwdScratch x = {a.delta + count, reinterpret_cast<uint32_t*>(a.delta + 2 * count), a.delta + part};
+  const cudaError_t e = tc ? smc::launch_attn_bwd_tc(a, x, dev.sms, s) : smc::launch_attn_simt(a, true, s);
   if (scratch) cudaFreeAsync(scratch, s);
   return outcome(e);
 }

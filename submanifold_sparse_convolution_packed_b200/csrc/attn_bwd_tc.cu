@@ -49,6 +49,7 @@ struct BwdParams {
   int64_t a1s[2], a2s[2];
   void *d1, *d2;          // dQ, -- or dK, dV
   int64_t s1[2], s2[2];
+  float* part;  // dK / dV of splits: [splits, m, kv_heads, 2, dim], or null
   uint32_t* err;
   uint64_t wait_ns;
 };
@@ -114,9 +115,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     b_hi = keys_seen(u, r0 + count - 1, p.causal);
   } else {
     b_hi = u.q.count;
+    if (u.splits > 1) {
+      b_lo = u.split * p.cut.chunk;
+      if (b_hi - b_lo > p.cut.chunk) b_hi = b_lo + p.cut.chunk;
+    }
     if (p.causal) {  // the first query that sees key r0
       const int64_t f = static_cast<int64_t>(r0) + u.q.count - u.k.count;
-      b_lo = f < 0 ? 0 : (f < b_hi ? static_cast<int32_t>(f) : b_hi);
+      if (f > b_lo) b_lo = f < b_hi ? static_cast<int32_t>(f) : b_hi;
     }
   }
   const int nsteps = b_hi > b_lo ? (b_hi - b_lo + per_step - 1) / per_step : 0;
@@ -411,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = mbar_wait_warp(bar_o, 0, p.err, p.wait_ns);
       tc_fence_after();
     }
-    if (ok) {
+    if (ok && (kDQ || !p.part || nsteps > 0)) {  // (k_attn_bwd_join leaves out the splits without a step)
       // dQ: 32 columns each (64 channels: the first two groups); dK: groups 0
       // and 2, dV: 1 and 3, half of the columns each
       const int c_lo = kDQ ? 32 * w : half * (DP / 2), c_hi = kDQ ? (c_lo + 32 < DP ? c_lo + 32 : DP) : c_lo + DP / 2;
@@ -436,6 +441,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] *= mul;
+        if (!kDQ && p.part) {  // a split: k_attn_bwd_join adds them up
+          if (row) {
+            float4* d = reinterpret_cast<float4*>(
+                p.part + (((static_cast<int64_t>(u.split) * p.cut.m + out_row) * p.kv_heads + hk) * 2 + (second ? 1 : 0)) * p.dim + c0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (c0 + 4 * i < p.dim) d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+          __syncwarp();
+          continue;
+        }
         store_rows<T>(stage, o, to, row ? at : -1, c0, p.dim);
       }
     }
@@ -443,6 +459,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 16) tmem_dealloc(tmem, 512);
+}
+
+// Adds up the splits of a tile's dK and dV, in order; kJoinParts blocks to a tile.
+constexpr int kJoinParts = 8;
+
+template <typename T>
+__global__ void __launch_bounds__(256) k_attn_bwd_join(const BwdParams p, const Cut tiles) {
+  __shared__ Unit s_unit;
+  find_unit<256>(tiles, blockIdx.x, &s_unit, p.err);
+  const Unit u = s_unit;
+  if (u.item < 0) return;
+  const int hk = blockIdx.y, r0 = u.tile * kRows, quads = p.dim / 4;
+  const int rows = u.k.count - r0 < kRows ? u.k.count - r0 : kRows;
+  const int splits = u.q.count > 0 ? (u.q.count - 1) / p.cut.chunk + 1 : 0;
+  // splits without a step have written nothing: those before the first query
+  // that sees a key of the tile
+  int s0 = 0;
+  if (p.causal) {
+    const int64_t f = static_cast<int64_t>(r0) + u.q.count - u.k.count;
+    if (f > 0) s0 = f >= u.q.count ? splits : static_cast<int>(f / p.cut.chunk);
+  }
+  const int64_t step = static_cast<int64_t>(p.cut.m) * p.kv_heads * 2 * p.dim;
+  constexpr int kPer = kRows / kJoinParts;  // rows of this block
+  const int i0 = blockIdx.z * kPer * 2 * quads, i1 = i0 + kPer * 2 * quads;
+  for (int i = i0 + threadIdx.x; i < i1 && i < rows * 2 * quads; i += 256) {
+    const int r = i / (2 * quads), rest = i - r * 2 * quads, second = rest / quads, c = (rest - second * quads) * 4;
+    const int64_t row = static_cast<int64_t>(u.k.begin) + r0 + r;
+    const float* from = p.part + ((row * p.kv_heads + hk) * 2 + second) * p.dim + c;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = s0; s < splits; ++s) {
+      const float4 v = *reinterpret_cast<const float4*>(from + s * step);
+      t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+    }
+    T* to = static_cast<T*>(second ? p.d2 : p.d1) + row * (second ? p.s2[0] : p.s1[0]) + hk * (second ? p.s2[1] : p.s1[1]) + c;
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack2<T>(t.x, t.y), pack2<T>(t.z, t.w));
+  }
 }
 
 // delta[row, head] = -sum of dO * O, and lse2 = -lse log2e, or -infinity for a
@@ -510,9 +563,34 @@ __global__ void __launch_bounds__(256) k_attn_delta_tc(const AttnArgs a, float* 
   if (threadIdx.x < 2) atomicMax(norms + threadIdx.x, s_top[threadIdx.x]);
 }
 
+// Where the tiles of keys do not fill the machine (shared heads: the heads of
+// a group are rows of one tile; causal: the first keys have all the work), the
+// queries in runs, for about two and a half CTAs to an SM, each of at least
+// 512 packed rows.
+struct BwdPlan {
+  int64_t units;
+  int chunk;  // queries of a run, 0: all
+};
+
+BwdPlan bwd_plan(const AttnArgs& a, int sms) {
+  const int group = a.heads / a.kv_heads;
+  const int64_t tiles = a.m / kRows + a.items;
+  BwdPlan b = {tiles, 0};
+  if (2 * tiles * a.kv_heads > 3ll * sms || a.items == 0) return b;
+  const int64_t runs = (5ll * sms / 2 + tiles * a.kv_heads - 1) / (tiles * a.kv_heads) * (a.items < 2 ? 1 : 2);
+  int64_t chunk = a.n / runs;
+  if (chunk < 512 / group) chunk = 512 / group;
+  if (a.n <= chunk) return b;
+  b.chunk = static_cast<int>(chunk);
+  b.units = tiles + (a.m / kRows + 1) * (a.n / chunk);
+  return b;
+}
+
 template <typename T, int DP>
-cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const CUtensorMap* maps, int sms, float* lse2,
-                         uint32_t* norms, cudaStream_t st) {
+cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const CUtensorMap* maps, int sms, const BwdScratch& x, cudaStream_t st) {
+  float* lse2 = x.lse2;
+  uint32_t* norms = a.dtype == kF16 ? x.norms : nullptr;
+  const BwdPlan plan = bwd_plan(a, sms);
   const int64_t rows = a.n * a.heads, per = DP == 64 ? 32 : 16;
   int64_t blocks = (rows + per - 1) / per;
   blocks = blocks < 8ll * sms ? (blocks < 1 ? 1 : blocks) : 8ll * sms;
@@ -543,15 +621,22 @@ cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const CUtensorMap* maps
   resident(a.k, a.k_stride, a.v, a.v_stride);
   p.cut.per_tile = divisor(kRows);
   p.cut.by_keys = true;
+  p.cut.chunk = plan.chunk;
+  p.part = plan.chunk ? x.part : nullptr;
   p.d1 = a.dk;
   p.d2 = a.dv;
   for (int i = 0; i < 2; ++i) {
     p.s1[i] = a.dk_stride[i];
     p.s2[i] = a.dv_stride[i];
   }
-  kk<<<dim3(static_cast<unsigned>(a.m / kRows + a.items), a.kv_heads), kThreads, kSmemK, st>>>(maps[4], maps[5], maps[6],
-                                                                                               maps[7], p);
-  count_launches(3);
+  const dim3 kgrid(static_cast<unsigned>(plan.units), a.kv_heads);
+  kk<<<kgrid, kThreads, kSmemK, st>>>(maps[4], maps[5], maps[6], maps[7], p);
+  if (plan.chunk) {
+    Cut tiles = p.cut;
+    tiles.chunk = 0;
+    k_attn_bwd_join<T><<<dim3(static_cast<unsigned>(a.m / kRows + a.items), a.kv_heads, kJoinParts), 256, 0, st>>>(p, tiles);
+  }
+  count_launches(plan.chunk ? 4 : 3);
   return cudaGetLastError();
 }
 
@@ -568,7 +653,12 @@ bool attn_bwd_tc_supported(const AttnArgs& a) {
          (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && encode_fn() != nullptr;
 }
 
-cudaError_t launch_attn_bwd_tc(const AttnArgs& a, float* lse2, uint32_t* norms, int sms, cudaStream_t st) {
+int64_t attn_bwd_tc_scratch(const AttnArgs& a, int sms) {
+  const BwdPlan b = bwd_plan(a, sms);
+  return b.chunk ? ((a.n - 1) / b.chunk + 1) * a.m * a.kv_heads * 2 * a.dim : 0;
+}
+
+cudaError_t launch_attn_bwd_tc(const AttnArgs& a, const BwdScratch& x, int sms, cudaStream_t st) {
   const int group = a.heads / a.kv_heads;
   BwdParams p = {};
   p.qpt = kRows / group;
@@ -592,18 +682,17 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs& a, float* lse2, uint32_t* norms, 
   p.group = group;
   p.scale = a.scale;
   p.causal = a.causal;
-  p.lse = lse2;
+  p.lse = x.lse2;
   p.delta = a.delta;
-  if (a.dtype != kF16) norms = nullptr;
-  p.norms = norms;
+  p.norms = a.dtype == kF16 ? x.norms : nullptr;
   p.err = a.err;
   // never below 100 ms, so that no CTA leaves with its loads in flight
   p.wait_ns = scan_wait_limit_ns() > 100000000ull ? scan_wait_limit_ns() : 100000000ull;
   if (a.dtype == kBF16)
-    return a.dim <= 64 ? launch_typed<__nv_bfloat16, 64>(a, p, maps, sms, lse2, norms, st)
-                       : launch_typed<__nv_bfloat16, 128>(a, p, maps, sms, lse2, norms, st);
-  return a.dim <= 64 ? launch_typed<__half, 64>(a, p, maps, sms, lse2, norms, st)
-                     : launch_typed<__half, 128>(a, p, maps, sms, lse2, norms, st);
+    return a.dim <= 64 ? launch_typed<__nv_bfloat16, 64>(a, p, maps, sms, x, st)
+                       : launch_typed<__nv_bfloat16, 128>(a, p, maps, sms, x, st);
+  return a.dim <= 64 ? launch_typed<__half, 64>(a, p, maps, sms, x, st)
+                     : launch_typed<__half, 128>(a, p, maps, sms, x, st);
 }
 
 }  // namespace smc

@@ -40,12 +40,11 @@ constexpr int kShortItem = 512;  // packed rows
 struct FwdParams {
   Cut cut;                                // per_tile: queries of a CTA; chunk: keys of a split
   int heads, kv_heads, dim, group, qpt;   // qpt: queries of a tile
-  int slot_rows;                          // rows of a split's partial results
   float c;                                       // scale * log2 e
   bool causal;
   void* out;
   float* lse;
-  float *part_o, *part_ml;  // [units, kv_heads, slot_rows, dim] and [.., 2]
+  float *part_o, *part_ml;  // of splits: [splits, n, heads, dim] and [.., 2], or null
   uint32_t* err;
   uint64_t wait_ns;
 };
@@ -386,7 +385,7 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
     if (ok && used) {
       const int64_t at = static_cast<int64_t>(u.q.begin + q0 + t * p.qpt + qi) * p.heads + hk * p.group + r % p.group;
       const bool split = p.part_o != nullptr;
-      const int64_t slot = (ux * p.kv_heads + hk) * p.slot_rows + t * p.qpt * p.group + r;
+      const int64_t slot = static_cast<int64_t>(u.split) * p.cut.n * p.heads + at;
       const float inv = sum == 0.f ? 0.f : 1.f / sum, f1 = split ? weight : weight * inv, f2 = split ? weight2 : weight2 * inv;
       const uint32_t to2 = tmem + lanes + L::kO + (g ^ 1) * DP;
 #pragma unroll 1
@@ -433,36 +432,47 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
   if (warp == kMmaWarp) tmem_dealloc(tmem, L::kColumns);
 }
 
-// Joins the splits of one tile, in order: O = sum 2^(top_s - top) O_s / sum ...
+// Joins the splits of a tile's rows, in order: O = sum 2^(top_s - top) O_s / sum ...
+// One warp to a row; lane s holds the weight of split s (32 at a time), so that
+// the loads of the splits' rows depend on nothing.
 template <typename T>
-__global__ void __launch_bounds__(256) k_attn_join(const FwdParams p) {
+__global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const Cut tiles) {
   __shared__ Unit s_unit;
-  find_unit<256>(p.cut, blockIdx.x, &s_unit, p.err);
+  find_unit<256>(tiles, blockIdx.x, &s_unit, p.err);
   const Unit u = s_unit;
-  if (u.item < 0 || u.split != 0) return;
+  if (u.item < 0) return;
   const int hk = blockIdx.y, lane = threadIdx.x & 31;
-  const int32_t per = static_cast<int32_t>(p.cut.per_tile.d), q0 = u.tile * per;
+  const int32_t per = static_cast<int32_t>(tiles.per_tile.d), q0 = u.tile * per;
   const int32_t queries = u.q.count - q0 < per ? u.q.count - q0 : per;
+  const int splits = u.k.count > p.cut.chunk ? (u.k.count - 1) / p.cut.chunk + 1 : 1;
+  const int64_t step = static_cast<int64_t>(p.cut.n) * p.heads;
   for (int r = threadIdx.x >> 5; r < queries * p.group; r += 8) {
-    const int64_t first = (static_cast<int64_t>(blockIdx.x) * p.kv_heads + hk) * p.slot_rows + r;
-    const int64_t step = static_cast<int64_t>(p.kv_heads) * p.slot_rows;
+    const int64_t at = static_cast<int64_t>(u.q.begin + q0 + r / p.group) * p.heads + hk * p.group + r % p.group;
     float top = -INFINITY;
-    for (int s = lane; s < u.splits; s += 32) top = fmaxf(top, p.part_ml[2 * (first + s * step)]);
+    for (int s = lane; s < splits; s += 32) top = fmaxf(top, p.part_ml[2 * (at + s * step)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
     const bool mine = 4 * lane < p.dim;
-    for (int s = 0; s < u.splits; ++s) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (first + s * step));
-      if (ml.x == -INFINITY) continue;  // this split's keys are hidden from the row
-      const float w = exp2f(ml.x - top);
-      sum += w * ml.y;
-      if (mine) {
-        const float4 v = *reinterpret_cast<const float4*>(p.part_o + (first + s * step) * p.dim + 4 * lane);
-        o[0] += w * v.x, o[1] += w * v.y, o[2] += w * v.z, o[3] += w * v.w;
+    for (int s0 = 0; s0 < splits; s0 += 32) {
+      const int many = splits - s0 < 32 ? splits - s0 : 32;
+      float w = 0.f, l = 0.f;
+      if (lane < many) {
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (at + (s0 + lane) * step));
+        w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);  // -inf: the split's keys are hidden from the row
+        l = w * ml.y;
+      }
+      sum += group_sum<32>(l);
+      const float* from = p.part_o + (at + s0 * step) * p.dim + 4 * lane;
+#pragma unroll 8
+      for (int s = 0; s < many; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, w, s);
+        if (mine) {
+          const float4 v = *reinterpret_cast<const float4*>(from + s * step * p.dim);
+          o[0] += ws * v.x, o[1] += ws * v.y, o[2] += ws * v.z, o[3] += ws * v.w;
+        }
       }
     }
-    const int64_t at = static_cast<int64_t>(u.q.begin + q0 + r / p.group) * p.heads + hk * p.group + r % p.group;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     if (mine)
       *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at * p.dim + 4 * lane) =
@@ -474,7 +484,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p) {
 struct FwdPlan {
   int tiles;      // tiles of a CTA
   int64_t units;  // blocks along x
-  int chunk, slot_rows;
+  int chunk;      // keys of a split, 0: all
 };
 
 // One tile to a CTA where items are short on average: such a CTA's start and
@@ -496,8 +506,6 @@ FwdPlan fwd_plan(const AttnArgs& a, int sms) {
   if (a.m <= chunk) return s;  // no item is longer than one run
   s.chunk = static_cast<int>(chunk);
   s.units = tiles + most * (a.m / chunk);
-  const int64_t rows = a.n * group;
-  s.slot_rows = static_cast<int>(rows < per * group ? rows : per * group);
   return s;
 }
 
@@ -510,7 +518,11 @@ cudaError_t launch_tiles(const AttnArgs& a, const FwdParams& p, const FwdPlan& s
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(s.units), a.kv_heads);
   kern<<<grid, L::kThreads, L::kTotal, st>>>(maps[0], maps[1], maps[2], p);
-  if (s.chunk) k_attn_join<T><<<grid, 256, 0, st>>>(p);
+  if (s.chunk) {
+    Cut tiles = p.cut;
+    tiles.chunk = 0;
+    k_attn_join<T><<<dim3(static_cast<unsigned>(a.n / tiles.per_tile.d + a.items), a.kv_heads), 256, 0, st>>>(p, tiles);
+  }
   count_launches(s.chunk ? 2 : 1);
   return cudaGetLastError();
 }
@@ -531,7 +543,7 @@ bool attn_tc_supported(const AttnArgs& a) {
 
 int64_t attn_tc_scratch(const AttnArgs& a, int sms) {
   const FwdPlan s = fwd_plan(a, sms);
-  return s.chunk ? s.units * a.kv_heads * s.slot_rows * (a.dim + 2) * static_cast<int64_t>(sizeof(float)) : 0;
+  return s.chunk ? ((a.m - 1) / s.chunk + 1) * a.n * a.heads * (a.dim + 2) * static_cast<int64_t>(sizeof(float)) : 0;
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, void* scratch, int sms, cudaStream_t st) {
@@ -551,14 +563,13 @@ cudaError_t launch_attn_tc(const AttnArgs& a, void* scratch, int sms, cudaStream
   p.dim = a.dim;
   p.group = group;
   p.qpt = qpt;
-  p.slot_rows = s.slot_rows;
   p.c = a.scale * kLog2e;
   p.causal = a.causal;
   p.out = a.out_w;
   p.lse = a.lse_w;
   if (s.chunk) {
     p.part_o = static_cast<float*>(scratch);
-    p.part_ml = p.part_o + s.units * a.kv_heads * s.slot_rows * a.dim;
+    p.part_ml = p.part_o + ((a.m - 1) / s.chunk + 1) * a.n * a.heads * a.dim;
   }
   p.err = a.err;
   // never below 100 ms, so that no CTA leaves with its loads in flight

@@ -225,9 +225,15 @@ bool attn_tc_supported(const AttnArgs& a);
 int64_t attn_tc_scratch(const AttnArgs& a, int sms);
 cudaError_t launch_attn_tc(const AttnArgs& a, void* scratch, int sms, cudaStream_t s);
 // Backward pass (attn_bwd_tc.cu): the same shapes, gradients and dout aligned
-// too; scratch: lse2 [n, heads], norms two words.
+// too.
+struct BwdScratch {
+  float* lse2;      // [n, heads]
+  uint32_t* norms;  // two words
+  float* part;      // attn_bwd_tc_scratch floats, 16-byte aligned
+};
 bool attn_bwd_tc_supported(const AttnArgs& a);
-cudaError_t launch_attn_bwd_tc(const AttnArgs& a, float* lse2, uint32_t* norms, int sms, cudaStream_t s);
+int64_t attn_bwd_tc_scratch(const AttnArgs& a, int sms);
+cudaError_t launch_attn_bwd_tc(const AttnArgs& a, const BwdScratch& x, int sms, cudaStream_t s);
 
 // dtype codes as in smc.h
 enum DType : int { kF32 = 0, kBF16 = 1, kF16 = 2 };

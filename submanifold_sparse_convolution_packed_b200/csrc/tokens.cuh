@@ -148,15 +148,15 @@ __device__ __forceinline__ uint32_t over(uint32_t x, Divisor d) {
   return d.d == 1 ? x : static_cast<uint32_t>((static_cast<uint64_t>(x) * d.mul) >> d.shift);
 }
 
-// A block's share: tile `tile` of item `item`'s rows, over the keys of its
-// split (split 0 of 1: all of them).  item < 0: nothing to do.
+// A block's share: tile `tile` of item `item`'s rows, over the other side's rows
+// of its split (split 0 of 1: all of them).  item < 0: nothing to do.
 struct Unit {
   int32_t item, tile, split, splits;
   Span q, k;
 };
 
 // How the items' rows are cut into units: tiles of per_tile.d rows (queries, or
-// keys with by_keys) x splits of `chunk` keys (0: one split).
+// keys with by_keys) x splits of `chunk` rows of the other side (0: one split).
 struct Cut {
   const int32_t *q_off, *k_off;
   int32_t n, m;
@@ -167,8 +167,9 @@ struct Cut {
 
 __device__ __forceinline__ int32_t units_of(const Cut& c, Span q, Span k, int32_t* splits) {
   const uint32_t rows = static_cast<uint32_t>(c.by_keys ? k.count : q.count);
+  const int32_t other = c.by_keys ? q.count : k.count;
   int32_t sp = 1;
-  if (c.chunk > 0 && k.count > c.chunk) sp = (k.count + c.chunk - 1) / c.chunk;
+  if (c.chunk > 0 && other > c.chunk) sp = (other - 1) / c.chunk + 1;
   *splits = sp;
   return static_cast<int32_t>(over(rows + c.per_tile.d - 1, c.per_tile)) * sp;
 }
