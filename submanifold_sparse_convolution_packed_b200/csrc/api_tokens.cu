@@ -270,14 +270,15 @@ int smc_attention(const void* q, const int64_t q_stride[2], const void* k, const
   a.out_w = out;
   a.lse_w = lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (!smc::attn_tc_supported(a)) return outcome(smc::launch_attn_simt(a, false, s));
+  const bool tc = smc::attn_tc_supported(a);
   void* scratch = nullptr;
-  const int64_t bytes = smc::attn_tc_scratch(a, dev.sms);
+  const int64_t bytes = tc ? smc::attn_tc_scratch(a, dev.sms) : smc::attn_simt_scratch(a, dev.sms);
   if (bytes > 0 && smc::scratch_alloc(&scratch, static_cast<size_t>(bytes), dev.id, s) != cudaSuccess) {
     cudaGetLastError();
     return SMC_E_OOM;
   }
-  const cudaError_t e = smc::launch_attn_tc(a, scratch, dev.sms, s);
+  const cudaError_t e =
+      tc ? smc::launch_attn_tc(a, scratch, dev.sms, s) : smc::launch_attn_simt(a, false, scratch, dev.sms, s);
   if (scratch) cudaFreeAsync(scratch, s);
   return outcome(e);
 }
@@ -341,7 +342,7 @@ int smc_attention_backward(const void* dout, const int64_t dout_stride[2], const
   }
   a.delta = static_cast<float*>(scratch);
   const smc::BwdScratch x = {a.delta + count, reinterpret_cast<uint32_t*>(a.delta + 2 * count), a.delta + part};
-  const cudaError_t e = tc ? smc::launch_attn_bwd_tc(a, x, dev.sms, s) : smc::launch_attn_simt(a, true, s);
+  const cudaError_t e = tc ? smc::launch_attn_bwd_tc(a, x, dev.sms, s) : smc::launch_attn_simt(a, true, nullptr, dev.sms, s);
   if (scratch) cudaFreeAsync(scratch, s);
   return outcome(e);
 }

@@ -18,6 +18,7 @@
 // 64 x 64 tiles, 256 threads, each with 4 x 4 scores and 4 rows of the
 // accumulator; operands are fp32 in shared memory, rows padded by 16 bytes so
 // that the float4 reads along a row meet no bank twice.
+#include "attn_join.cuh"
 #include "kernels.h"
 #include "tokens.cuh"
 
@@ -29,18 +30,36 @@ constexpr int kThreads = 256;
 constexpr int kTile = 64;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+__device__ __forceinline__ void cp_async16(float* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // kTile rows of one operand into shared memory as fp32, zero behind `rows` and
 // behind `dim`.  Row r is packed row first + r: source row (first + r) / group
-// of the item, head `head` + (first + r) % group.
+// of the item, head `head` + (first + r) % group.  fp32 rows of whole 16-byte
+// pieces (vec) arrive asynchronously, in the caller's group.
 template <typename T, int DP>
 __device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t row_stride, int64_t head_stride, int head,
-                                          int group, int32_t first, int rows, int dim) {
+                                          int group, int32_t first, int rows, int dim, bool vec) {
+  if (sizeof(T) == 4 && vec) {
+    for (int i = threadIdx.x; i < kTile * (DP / 4); i += kThreads) {
+      const int r = i / (DP / 4), c = i % (DP / 4) * 4;
+      const bool there = r < rows && c < dim;
+      const int pr = first + r, row = group == 1 ? pr : pr / group;
+      const T* at = there ? src + static_cast<int64_t>(row) * row_stride + (head + pr - row * group) * head_stride + c : src;
+      cp_async16(dst + r * (DP + 4) + c, at, there);
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < kTile * DP; i += kThreads) {
     const int r = i / DP, c = i % DP;
     float v = 0.f;
     if (r < rows && c < dim) {
-      const int pr = first + r;
-      v = to_f(src[static_cast<int64_t>(pr / group) * row_stride + (head + pr % group) * head_stride + c]);
+      const int pr = first + r, row = group == 1 ? pr : pr / group;
+      v = to_f(src[static_cast<int64_t>(row) * row_stride + (head + pr - row * group) * head_stride + c]);
     }
     dst[r * (DP + 4) + c] = v;
   }
@@ -116,7 +135,8 @@ __device__ __forceinline__ int32_t keys_seen(const Unit& u, int32_t qi, bool cau
 }
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut cut) {
+__global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut cut, bool vec, float* part_o,
+                                                   float* part_ml) {
   extern __shared__ float sm[];
   __shared__ Unit unit;
   constexpr int LD = DP + 4, W = DP / 16;
@@ -131,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
   const T* q = static_cast<const T*>(a.q) + u.q.begin * a.q_stride[0];
   const T* k = static_cast<const T*>(a.k) + u.k.begin * a.k_stride[0] + hk * a.k_stride[1];
   const T* v = static_cast<const T*>(a.v) + u.k.begin * a.v_stride[0] + hk * a.v_stride[1];
-  load_tile<T, DP>(sq, q, a.q_stride[0], a.q_stride[1], hk * group, group, q0 * group, rows, a.dim);
+  load_tile<T, DP>(sq, q, a.q_stride[0], a.q_stride[1], hk * group, group, q0 * group, rows, a.dim, vec);
   const float c = a.scale * kLog2e;
   int32_t seen[4];
   float top[4], sum[4], o[4][W];
@@ -144,15 +164,32 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
 #pragma unroll
     for (int j = 0; j < W; ++j) o[i][j] = 0.f;
   }
-  const int32_t last = keys_seen(u, q0 + queries - 1, a.causal);
-  for (int32_t k0 = 0; k0 < last; k0 += kTile) {
-    const int kr = u.k.count - k0 < kTile ? u.k.count - k0 : kTile;
-    __syncthreads();
-    load_tile<T, DP>(sk, k, a.k_stride[0], 0, 0, 1, k0, kr, a.dim);
-    load_tile<T, DP>(sv, v, a.v_stride[0], 0, 0, 1, k0, kr, a.dim);
+  // the keys of this block: of its split, up to the last that a query sees
+  const int32_t k_lo = u.split * cut.chunk;
+  int32_t last = keys_seen(u, q0 + queries - 1, a.causal);
+  if (u.splits > 1 && last - k_lo > cut.chunk) last = k_lo + cut.chunk;
+  auto load_k = [&](int32_t k0) {
+    if (k0 < last)
+      load_tile<T, DP>(sk, k, a.k_stride[0], 0, 0, 1, k0, u.k.count - k0 < kTile ? u.k.count - k0 : kTile, a.dim, vec);
+    cp_commit();
+  };
+  auto load_v = [&](int32_t k0) {
+    if (k0 < last)
+      load_tile<T, DP>(sv, v, a.v_stride[0], 0, 0, 1, k0, u.k.count - k0 < kTile ? u.k.count - k0 : kTile, a.dim, vec);
+    cp_commit();
+  };
+  // V of a step arrives during its scores, K of the next during its product.
+  load_k(k_lo);
+  load_v(k_lo);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) seen[i] = seen[i] < last ? seen[i] : last;
+  for (int32_t k0 = k_lo; k0 < last; k0 += kTile) {
+    cp_wait<1>();
     __syncthreads();
     float s[4][4];
     mm_nt<DP>(sq, sk, ty, tx, s);
+    __syncthreads();
+    load_k(k0 + kTile);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float m = -INFINITY;
@@ -184,8 +221,11 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
 #pragma unroll
       for (int j = 0; j < 4; ++j) sp[(4 * ty + i) * (kTile + 4) + tx + 16 * j] = s[i][j];
     }
-    __syncwarp();  // a warp reads back its own rows of P only
+    cp_wait<1>();
+    __syncthreads();
     mm_nn<DP>(sp, sv, ty, tx, o);
+    __syncthreads();
+    load_v(k0 + kTile);
   }
   T* out = static_cast<T*>(a.out_w);
 #pragma unroll
@@ -194,6 +234,16 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
     if (r >= rows) continue;
     const int64_t at = static_cast<int64_t>(u.q.begin + q0 + r / group) * a.heads + hk * group + r % group;
     const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];
+    if (part_o) {  // a split: unnormalised
+      const int64_t slot = static_cast<int64_t>(u.split) * a.n * a.heads + at;
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const int cc = col_of<DP>(tx, j);
+        if (cc < a.dim) part_o[slot * a.dim + cc] = o[i][j];
+      }
+      if (tx == 0) *reinterpret_cast<float2*>(part_ml + 2 * slot) = make_float2(top[i], sum[i]);
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < W; ++j) {
       const int cc = col_of<DP>(tx, j);
@@ -206,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
 // kDQ: a tile of packed queries against all its keys -> dQ.  Otherwise a tile
 // of keys against all its packed queries -> dK, dV.  A1, A2 stay; B1, B2 pass.
 template <typename T, int DP, bool kDQ>
-__global__ void __launch_bounds__(kThreads) k_attn_bwd(const AttnArgs a, const Cut cut) {
+__global__ void __launch_bounds__(kThreads) k_attn_bwd(const AttnArgs a, const Cut cut, bool vec) {
   extern __shared__ float sm[];
   __shared__ Unit unit;
   __shared__ float s_lse[kTile], s_delta[kTile];
@@ -223,8 +273,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_bwd(const AttnArgs a, const C
   const T* v = static_cast<const T*>(a.v) + u.k.begin * a.v_stride[0] + hk * a.v_stride[1];
   const float c = a.scale * kLog2e;
   auto load_q = [&](float* d1, float* d2, int32_t first, int rows) {
-    load_tile<T, DP>(d1, q, a.q_stride[0], a.q_stride[1], hk * group, group, first, rows, a.dim);
-    load_tile<T, DP>(d2, dout, a.dout_stride[0], a.dout_stride[1], hk * group, group, first, rows, a.dim);
+    load_tile<T, DP>(d1, q, a.q_stride[0], a.q_stride[1], hk * group, group, first, rows, a.dim, vec);
+    load_tile<T, DP>(d2, dout, a.dout_stride[0], a.dout_stride[1], hk * group, group, first, rows, a.dim, vec);
     if (threadIdx.x < kTile) {
       const int r = threadIdx.x;
       float l = INFINITY, e = 0.f;  // exp2(s - inf) = 0: rows that are not there, or saw no key
@@ -239,8 +289,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_bwd(const AttnArgs a, const C
   };
   auto load_k = [&](float* d1, float* d2, int32_t first) {
     const int rows = u.k.count - first < kTile ? u.k.count - first : kTile;
-    load_tile<T, DP>(d1, k, a.k_stride[0], 0, 0, 1, first, rows, a.dim);
-    load_tile<T, DP>(d2, v, a.v_stride[0], 0, 0, 1, first, rows, a.dim);
+    load_tile<T, DP>(d1, k, a.k_stride[0], 0, 0, 1, first, rows, a.dim, vec);
+    load_tile<T, DP>(d2, v, a.v_stride[0], 0, 0, 1, first, rows, a.dim, vec);
   };
   float acc1[4][W], acc2[4][W];
 #pragma unroll
@@ -269,6 +319,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_bwd(const AttnArgs a, const C
     __syncthreads();
     if constexpr (kDQ) load_k(b1, b2, b0);
     else load_q(b1, b2, b0, all - b0 < kTile ? all - b0 : kTile);
+    cp_commit();
+    cp_wait<0>();
     __syncthreads();
     float s[4][4], dp[4][4];
     mm_nt<DP>(a1, b1, ty, tx, s);
@@ -346,17 +398,38 @@ cudaError_t allow_smem(K kern, size_t bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
 }
 
+// fp32 operands whose rows are whole 16-byte pieces at 16-byte places.
+bool whole_pieces(const AttnArgs& a, bool backward) {
+  auto ok = [&](const void* p, const int64_t st[2]) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && st[0] % 4 == 0 && st[1] % 4 == 0;
+  };
+  return a.dtype == kF32 && a.dim % 4 == 0 && ok(a.q, a.q_stride) && ok(a.k, a.k_stride) && ok(a.v, a.v_stride) &&
+         (!backward || ok(a.dout, a.dout_stride));
+}
+
+// Runs of keys (attn_join.cuh), for three blocks to each of an SM's two places; the
+// join moves four channels at a time.
+int split_of(const AttnArgs& a, int sms) {
+  const bool fits = a.dim % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out_w) & 15u) == 0;
+  return fits ? attn::split_keys(a, kTile / (a.heads / a.kv_heads), 6ll * sms) : 0;
+}
+
 template <typename T, int DP>
-cudaError_t launch_dim(const AttnArgs& a, bool backward, cudaStream_t s) {
+cudaError_t launch_dim(const AttnArgs& a, bool backward, float* scratch, int chunk, cudaStream_t s) {
   const int per_tile = kTile / (a.heads / a.kv_heads);
-  const dim3 qgrid(static_cast<unsigned>(a.n / per_tile + a.items), a.kv_heads);
-  Cut cut = {a.q_off, a.k_off, static_cast<int32_t>(a.n), static_cast<int32_t>(a.m), a.items, 0, divisor(per_tile), false};
+  int64_t units = a.n / per_tile + a.items;
+  if (chunk) units += (a.n / per_tile + 1) * (a.m / chunk);
+  const dim3 qgrid(static_cast<unsigned>(units), a.kv_heads);
+  Cut cut = {a.q_off, a.k_off, static_cast<int32_t>(a.n), static_cast<int32_t>(a.m), a.items, chunk, divisor(per_tile), false};
+  const bool vec = whole_pieces(a, backward);
   const size_t tile = kTile * (DP + 4) * sizeof(float), extra = kTile * (kTile + 4) * sizeof(float);
   cudaError_t e;
   if (!backward) {
     if ((e = allow_smem(k_attn<T, DP>, 3 * tile + extra)) != cudaSuccess) return e;
-    k_attn<T, DP><<<qgrid, kThreads, 3 * tile + extra, s>>>(a, cut);
-    count_launches(1);
+    float* part_ml = chunk ? scratch + ((a.m - 1) / chunk + 1) * a.n * a.heads * a.dim : nullptr;
+    k_attn<T, DP><<<qgrid, kThreads, 3 * tile + extra, s>>>(a, cut, vec, chunk ? scratch : nullptr, part_ml);
+    if (chunk) attn::launch_join<T>(a, cut, scratch, part_ml, s);
+    count_launches(chunk ? 2 : 1);
     return cudaGetLastError();
   }
   if ((e = allow_smem(k_attn_bwd<T, DP, true>, 4 * tile + extra)) != cudaSuccess) return e;
@@ -364,32 +437,38 @@ cudaError_t launch_dim(const AttnArgs& a, bool backward, cudaStream_t s) {
   const int64_t warps = a.n * a.heads, want = (warps + 7) / 8;
   if (a.n > 0) {
     k_attn_delta<T><<<static_cast<unsigned>(want < 4096 ? want : 4096), kThreads, 0, s>>>(a);
-    k_attn_bwd<T, DP, true><<<qgrid, kThreads, 4 * tile + extra, s>>>(a, cut);
+    k_attn_bwd<T, DP, true><<<qgrid, kThreads, 4 * tile + extra, s>>>(a, cut, vec);
     count_launches(2);
   }
   if (a.m > 0) {
     const dim3 kgrid(static_cast<unsigned>(a.m / kTile + a.items), a.kv_heads);
     cut.per_tile = divisor(kTile);
     cut.by_keys = true;
-    k_attn_bwd<T, DP, false><<<kgrid, kThreads, 4 * tile + extra, s>>>(a, cut);
+    k_attn_bwd<T, DP, false><<<kgrid, kThreads, 4 * tile + extra, s>>>(a, cut, vec);
     count_launches(1);
   }
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_typed(const AttnArgs& a, bool backward, cudaStream_t s) {
-  if (a.dim <= 32) return launch_dim<T, 32>(a, backward, s);
-  if (a.dim <= 64) return launch_dim<T, 64>(a, backward, s);
-  return launch_dim<T, 128>(a, backward, s);
+cudaError_t launch_typed(const AttnArgs& a, bool backward, float* scratch, int chunk, cudaStream_t s) {
+  if (a.dim <= 32) return launch_dim<T, 32>(a, backward, scratch, chunk, s);
+  if (a.dim <= 64) return launch_dim<T, 64>(a, backward, scratch, chunk, s);
+  return launch_dim<T, 128>(a, backward, scratch, chunk, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_simt(const AttnArgs& a, bool backward, cudaStream_t s) {
-  if (a.dtype == kF32) return launch_typed<float>(a, backward, s);
-  if (a.dtype == kBF16) return launch_typed<__nv_bfloat16>(a, backward, s);
-  return launch_typed<__half>(a, backward, s);
+int64_t attn_simt_scratch(const AttnArgs& a, int sms) {
+  return attn::split_words(a, split_of(a, sms)) * static_cast<int64_t>(sizeof(float));
+}
+
+cudaError_t launch_attn_simt(const AttnArgs& a, bool backward, void* scratch, int sms, cudaStream_t s) {
+  const int chunk = backward ? 0 : split_of(a, sms);
+  float* x = static_cast<float*>(scratch);
+  if (a.dtype == kF32) return launch_typed<float>(a, backward, x, chunk, s);
+  if (a.dtype == kBF16) return launch_typed<__nv_bfloat16>(a, backward, x, chunk, s);
+  return launch_typed<__half>(a, backward, x, chunk, s);
 }
 
 }  // namespace smc

@@ -27,6 +27,7 @@
 // order.
 #include <type_traits>
 
+#include "attn_join.cuh"
 #include "attn_tc.cuh"
 
 namespace smc {
@@ -432,55 +433,6 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
   if (warp == kMmaWarp) tmem_dealloc(tmem, L::kColumns);
 }
 
-// Joins the splits of a tile's rows, in order: O = sum 2^(top_s - top) O_s / sum ...
-// One warp to a row; lane s holds the weight of split s (32 at a time), so that
-// the loads of the splits' rows depend on nothing.
-template <typename T>
-__global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const Cut tiles) {
-  __shared__ Unit s_unit;
-  find_unit<256>(tiles, blockIdx.x, &s_unit, p.err);
-  const Unit u = s_unit;
-  if (u.item < 0) return;
-  const int hk = blockIdx.y, lane = threadIdx.x & 31;
-  const int32_t per = static_cast<int32_t>(tiles.per_tile.d), q0 = u.tile * per;
-  const int32_t queries = u.q.count - q0 < per ? u.q.count - q0 : per;
-  const int splits = u.k.count > p.cut.chunk ? (u.k.count - 1) / p.cut.chunk + 1 : 1;
-  const int64_t step = static_cast<int64_t>(p.cut.n) * p.heads;
-  for (int r = threadIdx.x >> 5; r < queries * p.group; r += 8) {
-    const int64_t at = static_cast<int64_t>(u.q.begin + q0 + r / p.group) * p.heads + hk * p.group + r % p.group;
-    float top = -INFINITY;
-    for (int s = lane; s < splits; s += 32) top = fmaxf(top, p.part_ml[2 * (at + s * step)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    const bool mine = 4 * lane < p.dim;
-    for (int s0 = 0; s0 < splits; s0 += 32) {
-      const int many = splits - s0 < 32 ? splits - s0 : 32;
-      float w = 0.f, l = 0.f;
-      if (lane < many) {
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (at + (s0 + lane) * step));
-        w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);  // -inf: the split's keys are hidden from the row
-        l = w * ml.y;
-      }
-      sum += group_sum<32>(l);
-      const float* from = p.part_o + (at + s0 * step) * p.dim + 4 * lane;
-#pragma unroll 8
-      for (int s = 0; s < many; ++s) {
-        const float ws = __shfl_sync(0xffffffffu, w, s);
-        if (mine) {
-          const float4 v = *reinterpret_cast<const float4*>(from + s * step * p.dim);
-          o[0] += ws * v.x, o[1] += ws * v.y, o[2] += ws * v.z, o[3] += ws * v.w;
-        }
-      }
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    if (mine)
-      *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at * p.dim + 4 * lane) =
-          make_uint2(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv));
-    if (lane == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-  }
-}
-
 struct FwdPlan {
   int tiles;      // tiles of a CTA
   int64_t units;  // blocks along x
@@ -488,9 +440,7 @@ struct FwdPlan {
 };
 
 // One tile to a CTA where items are short on average: such a CTA's start and
-// end are most of its life, and the others on its SM fill them.  Keys are split
-// when the tiles alone leave half of the CTA slots idle: into runs of about
-// (keys x tiles) / slots, at least 256 keys.
+// end are most of its life, and the others on its SM fill them.
 FwdPlan fwd_plan(const AttnArgs& a, int sms) {
   const int group = a.heads / a.kv_heads, qpt = kRows / group;
   FwdPlan s = {};
@@ -499,13 +449,8 @@ FwdPlan fwd_plan(const AttnArgs& a, int sms) {
   const int per = s.tiles * qpt;
   const int64_t tiles = a.n / per + a.items, slots = static_cast<int64_t>(sms) * blocks;
   s.units = tiles;
-  if (2 * tiles * a.kv_heads > slots) return s;
-  const int64_t most = a.n / per + 1;  // tiles of one item, upper bound
-  int64_t chunk = a.m * most * a.kv_heads / slots;
-  chunk = (chunk < 256 ? 256 : chunk + kRows - 1) / kRows * kRows;
-  if (a.m <= chunk) return s;  // no item is longer than one run
-  s.chunk = static_cast<int>(chunk);
-  s.units = tiles + most * (a.m / chunk);
+  s.chunk = split_keys(a, per, slots);
+  if (s.chunk) s.units += (a.n / per + 1) * (a.m / s.chunk);
   return s;
 }
 
@@ -519,9 +464,7 @@ cudaError_t launch_tiles(const AttnArgs& a, const FwdParams& p, const FwdPlan& s
   const dim3 grid(static_cast<unsigned>(s.units), a.kv_heads);
   kern<<<grid, L::kThreads, L::kTotal, st>>>(maps[0], maps[1], maps[2], p);
   if (s.chunk) {
-    Cut tiles = p.cut;
-    tiles.chunk = 0;
-    k_attn_join<T><<<dim3(static_cast<unsigned>(a.n / tiles.per_tile.d + a.items), a.kv_heads), 256, 0, st>>>(p, tiles);
+    launch_join<T>(a, p.cut, p.part_o, p.part_ml, st);
   }
   count_launches(s.chunk ? 2 : 1);
   return cudaGetLastError();
@@ -543,7 +486,7 @@ bool attn_tc_supported(const AttnArgs& a) {
 
 int64_t attn_tc_scratch(const AttnArgs& a, int sms) {
   const FwdPlan s = fwd_plan(a, sms);
-  return s.chunk ? ((a.m - 1) / s.chunk + 1) * a.n * a.heads * (a.dim + 2) * static_cast<int64_t>(sizeof(float)) : 0;
+  return split_words(a, s.chunk) * static_cast<int64_t>(sizeof(float));
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, void* scratch, int sms, cudaStream_t st) {

@@ -216,8 +216,10 @@ struct AttnArgs {
   void *dq, *dk, *dv;
   int64_t dq_stride[2], dk_stride[2], dv_stride[2];
 };
-// FMA kernels: every dtype, dim <= 128, heads / kv_heads <= 64.
-cudaError_t launch_attn_simt(const AttnArgs& a, bool backward, cudaStream_t s);
+// FMA kernels: every dtype, dim <= 128, heads / kv_heads <= 64; scratch of
+// attn_simt_scratch bytes (forward).
+int64_t attn_simt_scratch(const AttnArgs& a, int sms);
+cudaError_t launch_attn_simt(const AttnArgs& a, bool backward, void* scratch, int sms, cudaStream_t s);
 
 // tcgen05 kernels (attn_tc.cu): bf16 / fp16, dim a multiple of 8, 16-byte
 // aligned tensors and strides; scratch of attn_tc_scratch bytes.
