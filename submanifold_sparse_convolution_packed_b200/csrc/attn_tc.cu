@@ -62,8 +62,8 @@ template <int DP, int kTiles> struct FwdLayout {
   static constexpr int kHalves = kTiles == 2 && DP == 64 ? 2 : 1, kGroups = kTiles * kHalves;
   static constexpr int kThreads = 128 * kGroups + 32 * (kTiles + 1);
   static constexpr uint32_t kQ = 0, kKv = kTiles * kQBytes, kBar = kKv + kSlots * kKvBytes;
-  // barriers: q, kv full[kSlots], kv empty[kSlots], s full[kGroups], p ready[kGroups], o done[kTiles], tail
-  static constexpr uint32_t kMisc = kBar + 8 * (2 * kSlots + kTiles + 2 * kGroups + 2);
+  // barriers: q, kv full[kSlots], kv empty[kSlots], s full[kGroups], p ready[kGroups], o done[kTiles], tail, q free
+  static constexpr uint32_t kMisc = kBar + 8 * (2 * kSlots + kTiles + 2 * kGroups + 3);
   static constexpr uint32_t kMl = (kMisc + 16 + 15) / 16 * 16;  // (maximum, sum) of each row and half
   static constexpr uint32_t kTotal = kMl + (kHalves == 2 ? kGroups * kRows * 8 : 0) + 1024;
   // TMEM columns: S of the tiles, then O of the tiles' halves
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
   volatile uint32_t* s_misc = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);  // [0] tmem
   const uint32_t bar_q = sbase + L::kBar, bar_full = bar_q + 8, bar_empty = bar_full + 8 * kSlots;
   const uint32_t bar_s = bar_empty + 8 * kSlots, bar_p = bar_s + 8 * L::kGroups, bar_o = bar_p + 8 * L::kGroups;
-  const uint32_t bar_tail = bar_o + 8 * kTiles;
+  const uint32_t bar_tail = bar_o + 8 * kTiles, bar_qfree = bar_tail + 8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
       mbar_init(bar_p + 8 * g, 4);
     }
     mbar_init(bar_tail, 1);
+    mbar_init(bar_qfree, kTiles);
     fence_mbarrier_init();
     fence_proxy_async_smem();
   }
@@ -122,7 +123,8 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
     return;
   }
   const Unit u = s_unit;
-  const int hk = blockIdx.y;
+  // this block's key/value heads: blockIdx.y, + gridDim.y, ...
+  const int nheads = (p.kv_heads - 1 - static_cast<int>(blockIdx.y)) / static_cast<int>(gridDim.y) + 1;
   const int32_t q0 = u.tile * kTiles * p.qpt;
   const int32_t left = u.q.count - q0;
   const int32_t k_lo = u.split * p.cut.chunk;
@@ -141,8 +143,13 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------- TMA loads
     // 2 * nsteps tiles in the order they are used: K0 V0 K1 V1 ...
-    if (nsteps > 0) {
-      if (elect_one()) {
+    int slot = 0;
+    uint32_t parity = 1;
+    bool ok = nsteps > 0;
+    for (int i = 0; i < nheads && ok; ++i) {
+      const int hk = blockIdx.y + i * gridDim.y;
+      ok = mbar_wait_warp(bar_qfree, (i & 1) ^ 1, p.err, p.wait_ns);  // the head before has no scores left to do
+      if (ok && elect_one()) {
         const int tiles = kTiles == 2 && queries[kTiles - 1] > 0 ? 2 : 1;
         mbar_arrive_expect_tx(bar_q, static_cast<uint32_t>(tiles * kPanels * p.group * p.qpt) * 128u);
         for (int t = 0; t < tiles; ++t)
@@ -151,28 +158,29 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
                         u.q.begin + q0 + t * p.qpt);
       }
       __syncwarp();
-      int slot = 0;
-      uint32_t parity = 1;
-      for (int i = 0; i < 2 * nsteps; ++i) {
-        if (!mbar_wait_warp(bar_empty + 8 * slot, parity, p.err, p.wait_ns)) break;
-        const int32_t key = k_lo + (i >> 1) * kKeys;
+      for (int j = 0; j < 2 * nsteps && ok; ++j) {
+        ok = mbar_wait_warp(bar_empty + 8 * slot, parity, p.err, p.wait_ns);
+        if (!ok) break;
+        const int32_t key = k_lo + (j >> 1) * kKeys;
         const int rows = u.k.count - key;  // V rows behind the item's end are zeroed below
-        const bool tail = (i & 1) && rows < kKeys;
+        const bool tail = (j & 1) && rows < kKeys;
         const uint32_t dst = sbase + L::kKv + slot * L::kKvBytes, bar = tail ? bar_tail : bar_full + 8 * slot;
         if (elect_one()) {
           mbar_arrive_expect_tx(bar, L::kKvBytes);
           for (int c = 0; c < kPanels; ++c)
-            tma_load_3d(dst + c * L::kKvPanel, (i & 1) ? &vmap : &kmap, bar, c * 64, hk, u.k.begin + key);
+            tma_load_3d(dst + c * L::kKvPanel, (j & 1) ? &vmap : &kmap, bar, c * 64, hk, u.k.begin + key);
         }
         __syncwarp();
-        if (tail) {  // once, at the last step
-          if (!mbar_wait_warp(bar_tail, 0, p.err, p.wait_ns)) break;
+        if (tail) {  // once for each head, at the last step
+          ok = mbar_wait_warp(bar_tail, i & 1, p.err, p.wait_ns);
+          if (!ok) break;
           uint4* base = reinterpret_cast<uint4*>(smem + L::kKv + slot * L::kKvBytes);
           for (int c = 0; c < kPanels; ++c)
-            for (int j = rows * 8 + lane; j < kKeys * 8; j += 32) base[c * (L::kKvPanel / 16) + j] = make_uint4(0, 0, 0, 0);
+            for (int z = rows * 8 + lane; z < kKeys * 8; z += 32) base[c * (L::kKvPanel / 16) + z] = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_full + 8 * slot);
+          __syncwarp();
         }
         if (++slot == kSlots) {
           slot = 0;
@@ -208,67 +216,79 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
     // A slot is free once every tile's warp has let go of it: behind the products
     // that read it, or at once where the tile has none.  Only slots that are
     // loaded again: no arrival is left under way at the end.
-    auto release = [&](int slot, int index, bool read) {  // in the elected lane
-      if (index + kSlots >= 2 * nsteps) return;
+    auto release = [&](int slot, int index, bool read) {  // in the elected lane; index: of all this block's loads
+      if (index + kSlots >= 2 * nsteps * nheads) return;
       if (read) umma_commit(bar_empty + 8 * slot);
       else mbar_arrive(bar_empty + 8 * slot);
     };
-    bool ok = nsteps > 0 && wait(bar_q, 0) && wait(bar_full, 0);
-    if (ok) {
-      if (elect_one()) {
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h)
-          if (mine > 0) scores(h, kd);
-        release(0, 0, mine > 0);
-      }
-      __syncwarp();
-    }
-    int sv = 1, sk = 2 % kSlots;  // slots of V of this step, of K of the next
-    uint32_t pv = 0, pk = kSlots == 2 ? 1 : 0;
-    for (int j = 0; j < nsteps && ok; ++j) {
-      const uint64_t v0 = vd + sv * kTile, k0 = kd + sk * kTile;
-      const bool last = j + 1 == mine, more = j + 1 < nsteps;
-      ok = wait(bar_full + 8 * sv, pv);
-      // with two slots, K of the next step may still be on its way when P is ready
-      constexpr bool kEarly = kSlots > 2;
-      if (kEarly && ok && more) ok = wait(bar_full + 8 * sk, pk);
-#pragma unroll
-      for (int h = 0; h < kHalves; ++h) {
-        const int g = t * kHalves + h;
-        if (ok && j < mine) ok = wait(bar_p + 8 * g, j & 1);
-        if (ok && elect_one()) {
-          if (j < mine) {
-#pragma unroll
-            for (int k = 0; k < kCols / 16; ++k)
-              umma_f16_ts(tmem + L::kO + g * DP, tmem + t * kKeys + h * kCols + k * 8, v0 + 128 * (h * kCols / 16 + k),
-                          idesc_o, j > 0 || k > 0);
-          }
-          if (kEarly && j + 1 < mine) scores(h, k0);
-          if (h + 1 == kHalves) {
-            if (last) umma_commit(bar_o + 8 * t);
-            release(sv, 2 * j + 1, j < mine);
-            if (kEarly && more) release(sk, 2 * j + 2, j + 1 < mine);
-          }
-        }
-        __syncwarp();
-      }
-      if (!kEarly && ok && more) {
-        ok = wait(bar_full + 8 * sk, pk);
-        if (ok && elect_one()) {
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h)
-            if (j + 1 < mine) scores(h, k0);
-          release(sk, 2 * j + 2, j + 1 < mine);
-        }
-        __syncwarp();
-      }
-      if ((sv += 2) >= kSlots) {
-        sv -= kSlots;
-        pv ^= 1;
-      }
+    // Slots and phases run on over the heads: the loads are one sequence K V K V.
+    int sk = 0, sv = 1;
+    uint32_t pk = 0, pv = 0, pp = 0;
+    bool ok = nsteps > 0;
+    auto next_k = [&]() {
       if ((sk += 2) >= kSlots) {
         sk -= kSlots;
         pk ^= 1;
+      }
+    };
+    for (int i = 0; i < nheads && ok; ++i) {
+      const int load0 = 2 * nsteps * i;
+      // the first scores; with one step they are the last that read this Q
+      ok = wait(bar_q, i & 1) && wait(bar_full + 8 * sk, pk);
+      if (ok && elect_one()) {
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+          if (mine > 0) scores(h, kd + sk * kTile);
+        release(sk, load0, mine > 0);
+        if (nsteps == 1 && i + 1 < nheads) umma_commit(bar_qfree);
+      }
+      __syncwarp();
+      next_k();
+      for (int j = 0; j < nsteps && ok; ++j) {
+        const uint64_t v0 = vd + sv * kTile, k0 = kd + sk * kTile;
+        const bool last = j + 1 == mine, more = j + 1 < nsteps, qdone = j + 2 == nsteps && i + 1 < nheads;
+        ok = wait(bar_full + 8 * sv, pv);
+        // with two slots, K of the next step may still be on its way when P is ready
+        constexpr bool kEarly = kSlots > 2;
+        if (kEarly && ok && more) ok = wait(bar_full + 8 * sk, pk);
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+          const int g = t * kHalves + h;
+          if (ok && j < mine) ok = wait(bar_p + 8 * g, pp);
+          if (ok && elect_one()) {
+            if (j < mine) {
+#pragma unroll
+              for (int k = 0; k < kCols / 16; ++k)
+                umma_f16_ts(tmem + L::kO + g * DP, tmem + t * kKeys + h * kCols + k * 8, v0 + 128 * (h * kCols / 16 + k),
+                            idesc_o, j > 0 || k > 0);
+            }
+            if (kEarly && j + 1 < mine) scores(h, k0);
+            if (h + 1 == kHalves) {
+              if (last) umma_commit(bar_o + 8 * t);
+              release(sv, load0 + 2 * j + 1, j < mine);
+              if (kEarly && more) release(sk, load0 + 2 * j + 2, j + 1 < mine);
+              if (kEarly && qdone) umma_commit(bar_qfree);
+            }
+          }
+          __syncwarp();
+        }
+        if (j < mine) pp ^= 1;
+        if (!kEarly && ok && more) {
+          ok = wait(bar_full + 8 * sk, pk);
+          if (ok && elect_one()) {
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+              if (j + 1 < mine) scores(h, k0);
+            release(sk, load0 + 2 * j + 2, j + 1 < mine);
+            if (qdone) umma_commit(bar_qfree);
+          }
+          __syncwarp();
+        }
+        if ((sv += 2) >= kSlots) {
+          sv -= kSlots;
+          pv ^= 1;
+        }
+        if (more) next_k();
       }
     }
   } else {
@@ -281,150 +301,157 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
     const bool used = __any_sync(0xffffffffu, row);  // a warp without rows only keeps step
     int32_t lim = row ? keys_seen(u, q0 + t * p.qpt + qi, p.causal) : 0;  // keys [0, lim) are seen
     lim = (lim < k_hi ? lim : k_hi) - k_lo - h * kCols;
-    float top = -INFINITY, sum = 0.f;  // top: the rounded product with c the sums refer to
     bool ok = true;
-    for (int j = 0; j < steps[t]; ++j) {
-      ok = mbar_wait_warp(bar_s + 8 * g, j & 1, p.err, p.wait_ns);
-      if (!ok) break;
-      tc_fence_after();
-      if (used) {
-        // The scores in registers: all of this thread's, or (four CTAs to an SM)
-        // 32 at a time, read from TMEM twice.
-        constexpr int kPart = L::kSmall ? 32 : kCols, kParts = kCols / kPart;
-        const int32_t seen = lim - j * kKeys;
-        const bool whole = __all_sync(0xffffffffu, seen >= kCols);
-        float x[kPart];
-        float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
-        auto load = [&](int q) {
-          tmem_ld(ts + q * kPart, x);
-          if (!whole) {
+    uint32_t ps = 0;
+    for (int head = 0; head < nheads && ok; ++head) {
+      const int hk = blockIdx.y + head * gridDim.y;
+      float top = -INFINITY, sum = 0.f;  // top: the rounded product with c the sums refer to
+      for (int j = 0; j < steps[t]; ++j) {
+        ok = mbar_wait_warp(bar_s + 8 * g, ps, p.err, p.wait_ns);
+        ps ^= 1;
+        if (!ok) break;
+        tc_fence_after();
+        if (used) {
+          // The scores in registers: all of this thread's, or (four CTAs to an SM)
+          // 32 at a time, read from TMEM twice.
+          constexpr int kPart = L::kSmall ? 32 : kCols, kParts = kCols / kPart;
+          const int32_t seen = lim - j * kKeys;
+          const bool whole = __all_sync(0xffffffffu, seen >= kCols);
+          float x[kPart];
+          float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
+          auto load = [&](int q) {
+            tmem_ld(ts + q * kPart, x);
+            if (!whole) {
 #pragma unroll
-            for (int i = 0; i < kPart; ++i)
-              if (q * kPart + i >= seen) x[i] = -INFINITY;
-          }
-        };
+              for (int i = 0; i < kPart; ++i)
+                if (q * kPart + i >= seen) x[i] = -INFINITY;
+            }
+          };
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) {
-          load(q);
+          for (int q = 0; q < kParts; ++q) {
+            load(q);
 #pragma unroll
-          for (int i = 0; i < kPart; i += 8) {
-            m0 = max3(m0, x[i], x[i + 1]);
-            m1 = max3(m1, x[i + 2], x[i + 3]);
-            m2 = max3(m2, x[i + 4], x[i + 5]);
-            m3 = max3(m3, x[i + 6], x[i + 7]);
-          }
-        }
-        const float m = __fmul_rn(fmaxf(max3(m0, m1, m2), m3), p.c);
-        const bool grown = m > top + 8.f || (top == -INFINITY && m > -INFINITY);
-        if (__any_sync(0xffffffffu, grown)) {
-          const float keep = grown ? exp2_fast(top - m) : 1.f;
-          if (grown) {
-            sum *= keep;
-            top = m;
-          }
-          if (j > 0) {  // the products so far are complete: these scores came after them
-#pragma unroll 1
-            for (int c0 = 0; c0 < DP; c0 += 16) {
-              float o[16];
-              uint32_t b[16];
-              tmem_ld(to + c0, o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) b[i] = __float_as_uint(o[i] * keep);
-              tmem_st(to + c0, b);
+            for (int i = 0; i < kPart; i += 8) {
+              m0 = max3(m0, x[i], x[i + 1]);
+              m1 = max3(m1, x[i + 2], x[i + 3]);
+              m2 = max3(m2, x[i + 4], x[i + 5]);
+              m3 = max3(m3, x[i + 6], x[i + 7]);
             }
           }
-        }
-        const float base = top == -INFINITY ? 0.f : top;
-        float2 sa = make_float2(0.f, 0.f), sb = sa;
-        const float2 c2 = make_float2(p.c, p.c), b2 = make_float2(-base, -base);
-#pragma unroll
-        for (int q = 0; q < kParts; ++q) {
-          if (kParts > 1) load(q);
-          constexpr int kWords = kPart >= 64 ? 32 : 16;
-#pragma unroll
-          for (int z = 0; z < kPart / (2 * kWords); ++z) {
-            uint32_t w[kWords];
-#pragma unroll
-            for (int i = 0; i < kWords; i += 2) {
-              const int e = z * 2 * kWords + 2 * i;
-              const float2 y0 = fma2(make_float2(x[e], x[e + 1]), c2, b2), y1 = fma2(make_float2(x[e + 2], x[e + 3]), c2, b2);
-              const float2 e0 = make_float2(exp2_fast(y0.x), exp2_fast(y0.y)), e1 = make_float2(exp2_fast(y1.x), exp2_fast(y1.y));
-              sa = add2(sa, e0);
-              sb = add2(sb, e1);
-              w[i] = pack2<T>(e0.x, e0.y);
-              w[i + 1] = pack2<T>(e1.x, e1.y);
+          const float m = __fmul_rn(fmaxf(max3(m0, m1, m2), m3), p.c);
+          const bool grown = m > top + 8.f || (top == -INFINITY && m > -INFINITY);
+          if (__any_sync(0xffffffffu, grown)) {
+            const float keep = grown ? exp2_fast(top - m) : 1.f;
+            if (grown) {
+              sum *= keep;
+              top = m;
             }
-            // over scores that are in registers, or used up
-            tmem_st(ts + (q * kPart / 2 + z * kWords), w);
-          }
-        }
-        sum += (sa.x + sa.y) + (sb.x + sb.y);
-        tmem_st_wait();
-        tc_fence_before();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_p + 8 * g);
-      __syncwarp();
-    }
-    // --------------------------------------------------------------- results
-    float2* s_ml = reinterpret_cast<float2*>(smem + L::kMl);
-    float weight = 1.f, weight2 = 0.f;  // of this half's accumulator, and the other's
-    if (kHalves == 2) {
-      s_ml[g * kRows + r] = make_float2(top, sum);
-      asm volatile("bar.sync %0, 256;" ::"r"(1 + t) : "memory");  // the tile's two groups
-      const float2 other = s_ml[(g ^ 1) * kRows + r];
-      const float m = fmaxf(top, other.x);
-      weight = top == -INFINITY ? 0.f : exp2_fast(top - m);
-      weight2 = other.x == -INFINITY ? 0.f : exp2_fast(other.x - m);
-      sum = sum * weight + other.y * weight2;
-      top = m;
-    }
-    if (ok && steps[t] > 0) {
-      ok = mbar_wait_warp(bar_o + 8 * t, 0, p.err, p.wait_ns);
-      tc_fence_after();
-    }
-    if (ok && used) {
-      const int64_t at = static_cast<int64_t>(u.q.begin + q0 + t * p.qpt + qi) * p.heads + hk * p.group + r % p.group;
-      const bool split = p.part_o != nullptr;
-      const int64_t slot = static_cast<int64_t>(u.split) * p.cut.n * p.heads + at;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum, f1 = split ? weight : weight * inv, f2 = split ? weight2 : weight2 * inv;
-      const uint32_t to2 = tmem + lanes + L::kO + (g ^ 1) * DP;
+            if (j > 0) {  // the products so far are complete: these scores came after them
 #pragma unroll 1
-      for (int c0 = h * (DP / kHalves); c0 < (h + 1) * (DP / kHalves); c0 += 32) {
-        if (c0 >= p.dim) break;
-        float o[32];
-        if (steps[t] > 0) {
-          tmem_ld(to + c0, o);
+              for (int c0 = 0; c0 < DP; c0 += 16) {
+                float o[16];
+                uint32_t b[16];
+                tmem_ld(to + c0, o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= f1;
-          if (kHalves == 2) {
-            float o2[32];
-            tmem_ld(to2 + c0, o2);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = fmaf(o2[i], f2, o[i]);
+                for (int i = 0; i < 16; ++i) b[i] = __float_as_uint(o[i] * keep);
+                tmem_st(to + c0, b);
+              }
+            }
           }
-        } else {
+          const float base = top == -INFINITY ? 0.f : top;
+          float2 sa = make_float2(0.f, 0.f), sb = sa;
+          const float2 c2 = make_float2(p.c, p.c), b2 = make_float2(-base, -base);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.f;
-        }
-        if (row && split) {
-          float4* d = reinterpret_cast<float4*>(p.part_o + slot * p.dim + c0);
+          for (int q = 0; q < kParts; ++q) {
+            if (kParts > 1) load(q);
+            constexpr int kWords = kPart >= 64 ? 32 : 16;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (c0 + 4 * i < p.dim) d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        } else if (row) {
-          uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * p.dim + c0);
+            for (int z = 0; z < kPart / (2 * kWords); ++z) {
+              uint32_t w[kWords];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (c0 + 8 * i < p.dim)
-              d[i] = make_uint4(pack2<T>(o[8 * i], o[8 * i + 1]), pack2<T>(o[8 * i + 2], o[8 * i + 3]),
-                                pack2<T>(o[8 * i + 4], o[8 * i + 5]), pack2<T>(o[8 * i + 6], o[8 * i + 7]));
+              for (int i = 0; i < kWords; i += 2) {
+                const int e = z * 2 * kWords + 2 * i;
+                const float2 y0 = fma2(make_float2(x[e], x[e + 1]), c2, b2), y1 = fma2(make_float2(x[e + 2], x[e + 3]), c2, b2);
+                const float2 e0 = make_float2(exp2_fast(y0.x), exp2_fast(y0.y)), e1 = make_float2(exp2_fast(y1.x), exp2_fast(y1.y));
+                sa = add2(sa, e0);
+                sb = add2(sb, e1);
+                w[i] = pack2<T>(e0.x, e0.y);
+                w[i + 1] = pack2<T>(e1.x, e1.y);
+              }
+              // over scores that are in registers, or used up
+              tmem_st(ts + (q * kPart / 2 + z * kWords), w);
+            }
+          }
+          sum += (sa.x + sa.y) + (sb.x + sb.y);
+          tmem_st_wait();
+          tc_fence_before();
         }
         __syncwarp();
+        if (lane == 0) mbar_arrive(bar_p + 8 * g);
+        __syncwarp();
       }
-      if (row && h == 0) {
-        if (split) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(top, sum);
-        else if (p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+      // --------------------------------------------------------------- results
+      float2* s_ml = reinterpret_cast<float2*>(smem + L::kMl);
+      float weight = 1.f, weight2 = 0.f;  // of this half's accumulator, and the other's
+      if (kHalves == 2) {
+        s_ml[g * kRows + r] = make_float2(top, sum);
+        asm volatile("bar.sync %0, 256;" ::"r"(1 + t) : "memory");  // the tile's two groups
+        const float2 other = s_ml[(g ^ 1) * kRows + r];
+        const float m = fmaxf(top, other.x);
+        weight = top == -INFINITY ? 0.f : exp2_fast(top - m);
+        weight2 = other.x == -INFINITY ? 0.f : exp2_fast(other.x - m);
+        sum = sum * weight + other.y * weight2;
+        top = m;
+      }
+      if (ok && steps[t] > 0) {
+        ok = mbar_wait_warp(bar_o + 8 * t, head & 1, p.err, p.wait_ns);
+        tc_fence_after();
+      }
+      if (ok && used) {
+        const int64_t at = static_cast<int64_t>(u.q.begin + q0 + t * p.qpt + qi) * p.heads + hk * p.group + r % p.group;
+        const bool split = p.part_o != nullptr;
+        const int64_t slot = static_cast<int64_t>(u.split) * p.cut.n * p.heads + at;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum, f1 = split ? weight : weight * inv, f2 = split ? weight2 : weight2 * inv;
+        const uint32_t to2 = tmem + lanes + L::kO + (g ^ 1) * DP;
+#pragma unroll 1
+        for (int c0 = h * (DP / kHalves); c0 < (h + 1) * (DP / kHalves); c0 += 32) {
+          if (c0 >= p.dim) break;
+          float o[32];
+          if (steps[t] > 0) {
+            tmem_ld(to + c0, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= f1;
+            if (kHalves == 2) {
+              float o2[32];
+              tmem_ld(to2 + c0, o2);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = fmaf(o2[i], f2, o[i]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+          }
+          if (row && split) {
+            float4* d = reinterpret_cast<float4*>(p.part_o + slot * p.dim + c0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (c0 + 4 * i < p.dim) d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          } else if (row) {
+            uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * p.dim + c0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (c0 + 8 * i < p.dim)
+                d[i] = make_uint4(pack2<T>(o[8 * i], o[8 * i + 1]), pack2<T>(o[8 * i + 2], o[8 * i + 3]),
+                                  pack2<T>(o[8 * i + 4], o[8 * i + 5]), pack2<T>(o[8 * i + 6], o[8 * i + 7]));
+          }
+          __syncwarp();
+        }
+        if (row && h == 0) {
+          if (split) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(top, sum);
+          else if (p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        }
+        __syncwarp();
+        tc_fence_before();  // the next head's products may overwrite O once P of its first step is there
       }
     }
   }
@@ -437,6 +464,7 @@ struct FwdPlan {
   int tiles;      // tiles of a CTA
   int64_t units;  // blocks along x
   int chunk;      // keys of a split, 0: all
+  int heads;      // key/value heads of a CTA
 };
 
 // One tile to a CTA where items are short on average: such a CTA's start and
@@ -449,6 +477,15 @@ FwdPlan fwd_plan(const AttnArgs& a, int sms) {
   const int per = s.tiles * qpt;
   const int64_t tiles = a.n / per + a.items, slots = static_cast<int64_t>(sms) * blocks;
   s.units = tiles;
+  // Short items: several heads to a CTA, as long as four waves of CTAs remain,
+  // since finding the block's share and the first loads' way are a third of a
+  // CTA's life there.  (Two-tile CTAs read each other's halves at the end, and
+  // their items are long.)
+  s.heads = 1;
+  if (s.tiles == 1) {
+    const int64_t most = tiles * a.kv_heads / (4 * slots);
+    s.heads = static_cast<int>(most < 1 ? 1 : most < a.kv_heads ? most : a.kv_heads);
+  }
   s.chunk = split_keys(a, per, slots);
   if (s.chunk) s.units += (a.n / per + 1) * (a.m / s.chunk);
   return s;
@@ -461,7 +498,7 @@ cudaError_t launch_tiles(const AttnArgs& a, const FwdParams& p, const FwdPlan& s
   auto kern = k_attn_fwd_tc<T, DP, kTiles>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L::kTotal));
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(s.units), a.kv_heads);
+  const dim3 grid(static_cast<unsigned>(s.units), static_cast<unsigned>((a.kv_heads + s.heads - 1) / s.heads));
   kern<<<grid, L::kThreads, L::kTotal, st>>>(maps[0], maps[1], maps[2], p);
   if (s.chunk) {
     launch_join<T>(a, p.cut, p.part_o, p.part_ml, st);

@@ -361,6 +361,44 @@ def test_attention_and_gradients(case, dtype):
     smc.status()
 
 
+# many short items: a block then works through several heads; long rows of few
+# items: keys (forward) and queries (gradients) are split between blocks
+MANY = [([i * 7 % 23 for i in range(1300)], None, 5, 5, 64, False), ([i * 11 % 190 for i in range(400)], None, 20, 20, 128, False),
+        ([i * 5 % 140 for i in range(700)], [i * 13 % 90 for i in range(700)], 16, 8, 40, True),
+        ([700], [6000], 4, 2, 64, False), ([5000, 3, 0, 64], None, 4, 1, 128, True), ([3000], [400], 2, 2, 64, True),
+        ([400], [3000], 2, 1, 72, True), ([6000, 10], [130, 0], 8, 1, 64, False)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_attention_many_items_and_splits(case, dtype):
+    ql, kl, h, hk, d, causal = MANY[case]
+    g = gen(100 + case)
+    qo, ko = offsets_of(ql), offsets_of(kl or ql)
+    q, dout = (normal(g, sum(ql), h, d, dtype=dtype) for _ in range(2))
+    k, v = (normal(g, sum(kl or ql), hk, d, dtype=dtype) for _ in range(2))
+    lse = torch.empty(sum(ql), h, device="cuda")
+    out = smc.attention(q, k, v, qo, ko, causal=causal, lse=lse)
+    got = smc.attention_backward(dout, q, k, v, out, lse, qo, ko, causal=causal)
+    smc.status()
+    few = len(ql) > 100  # the plain form goes item by item: take every 37th of many
+    for i in range(0, len(ql), 37 if few else 1):
+        (a, b), (c, e) = spans(qo[i:i + 2])[0], spans(ko[i:i + 2])[0]
+        if a == b or c == e:
+            assert not out[a:b].any() and bool((lse[a:b] == -math.inf).all())
+            assert not got[0][a:b].any() and not got[1][c:e].any() and not got[2][c:e].any()
+            continue
+        one = (q[a:b], k[c:e], v[c:e], offsets_of([b - a]), offsets_of([e - c]), d ** -0.5, causal)
+        r = attention_ref(*one)
+        close(out[a:b], r["out"], r["tout"], "out")
+        r = attention_ref(*one, dout[a:b], out[a:b], lse[a:b])
+        for x, y in zip(("dq", "dk", "dv"), (got[0][a:b], got[1][c:e], got[2][c:e])):
+            close(y, r[x], r["t" + x], x)
+    assert torch.equal(out, smc.attention(q, k, v, qo, ko, causal=causal))
+    again = smc.attention_backward(dout, q, k, v, out, lse, qo, ko, causal=causal)
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 @pytest.mark.parametrize("d", [64, 128, 20])
 def test_attention_rows_outside_items(dtype, d):
