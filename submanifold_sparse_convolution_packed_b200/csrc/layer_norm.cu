@@ -39,8 +39,9 @@ template <typename T> __device__ __forceinline__ float sigmoid(float z) {
 // Two of them with one reciprocal: 1/a = b * 1/(ab).  The special-function unit
 // otherwise bounds 16-bit rows (an exponential and a reciprocal for each value
 // at 16 lanes a clock).  The exponent is cut at 62 (z = -43), so that ab stays
-// in range; what is behind it is below 1e-17 either way.  A NaN passes the cut
-// and comes back with the product by z.
+// in range, and so is the z that the sigmoid is multiplied by (silu_arg): what is
+// behind the cut is below 1e-17 either way.  A NaN leaves its neighbour alone
+// and comes back with its own z.
 template <typename T> __device__ __forceinline__ void sigmoid2(float z0, float z1, float* s0, float* s1) {
   if (std::is_same<T, float>::value) {
     *s0 = sigmoid<T>(z0);
@@ -53,6 +54,10 @@ template <typename T> __device__ __forceinline__ void sigmoid2(float z0, float z
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
   *s0 = r * b;
   *s1 = r * a;
+}
+
+__device__ __forceinline__ float2 silu_arg(float z0, float z1) {
+  return make_float2(z0 < -43.f ? -43.f : z0, z1 < -43.f ? -43.f : z1);
 }
 
 template <typename T> __device__ __forceinline__ float act_value(float z, int act) {
@@ -78,7 +83,7 @@ template <typename T, int N> __device__ __forceinline__ void act_values(float (&
     for (int i = 0; i + 1 < N; i += 2) {
       float2 s;
       sigmoid2<T>(z[i], z[i + 1], &s.x, &s.y);
-      s = mul2(make_float2(z[i], z[i + 1]), s);
+      s = mul2(silu_arg(z[i], z[i + 1]), s);
       z[i] = s.x;
       z[i + 1] = s.y;
     }
@@ -94,7 +99,7 @@ template <typename T, int N> __device__ __forceinline__ void act_slopes(float (&
     for (int i = 0; i + 1 < N; i += 2) {
       float2 s;
       sigmoid2<T>(z[i], z[i + 1], &s.x, &s.y);
-      const float2 zz = make_float2(z[i], z[i + 1]), one = make_float2(1.f, 1.f);
+      const float2 zz = silu_arg(z[i], z[i + 1]), one = make_float2(1.f, 1.f);
       // s (1 + z (1 - s))
       const float2 t = mul2(s, fma2(zz, add2(one, make_float2(-s.x, -s.y)), one));
       z[i] = t.x;
@@ -107,9 +112,12 @@ template <typename T, int N> __device__ __forceinline__ void act_slopes(float (&
 }
 
 // Blocks that an SM should hold, by the elements a lane holds: more rows in
-// flight for short rows, registers for long ones.
+// flight for short rows, registers for long ones.  (Forward, 8 elements: 3, 4,
+// 5, 6 blocks took 86, 75, 82, 90 us on 1.3M x 64 fp16; backward: 2, 3, 4 took
+// 37, 33, 34 us on 133450 x 128 bf16, where fetching the next row ahead, as the
+// forward pass does, cost 3 us in registers.)
 constexpr int fwd_blocks(int elems) { return elems <= 8 ? 4 : elems <= 16 ? 2 : 1; }
-constexpr int bwd_blocks(int elems) { return elems <= 8 ? 2 : elems <= 16 ? 2 : 1; }
+constexpr int bwd_blocks(int elems) { return elems <= 8 ? 3 : elems <= 16 ? 2 : 1; }
 
 template <typename T>
 struct NormArgs {
@@ -301,7 +309,6 @@ template <typename T, int EPC, int NCH, int TPR, bool kWhole>
 __global__ void __launch_bounds__(kThreads, bwd_blocks(EPC* NCH)) k_layer_norm_bwd(const NormArgs<T> a) {
   using C = Chunk<T, EPC>;
   constexpr int kRows = kThreads / TPR, N = NCH * EPC;
-  constexpr bool kAhead = N <= 8;  // the next row is fetched before this one is worked on
   extern __shared__ float s_sum[];  // [warps, c]
   const int l = threadIdx.x % TPR, chunks = a.c / EPC;
   const C* x = reinterpret_cast<const C*>(a.x);
@@ -325,13 +332,11 @@ __global__ void __launch_bounds__(kThreads, bwd_blocks(EPC* NCH)) k_layer_norm_b
     at += jump;
   };
   dx += row * chunks;
-  if (kAhead) fetch(row);
   for (; base < a.n; base += step, row += step, dx += jump) {
-    if (!kAhead) fetch(row);
+    fetch(row);
     cx.values(xh);
     cd.values(g);
     const float mean = cs.x, rstd = cs.y;
-    if (kAhead) fetch(row + step);
     shift_scale(xh, -mean, rstd);
     float gam[N];  // gamma and beta come from the cache each time: registers are scarcer
     parameter<T, EPC, NCH, TPR, kWhole>(a.gamma, 1.f, l, chunks, gam);

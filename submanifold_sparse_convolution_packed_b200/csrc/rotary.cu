@@ -34,7 +34,7 @@ struct RotArgs {
   const int32_t* pos;
   const double* freqs;
   int64_t n, xs_row, xs_head, os_row, os_head, ps_row, ps_axis;
-  int heads, dim, axes, nfreq, run;
+  int heads, dim, axes, nfreq, runs;  // runs: threads that share a chunk's heads
   float scale;
   bool inverse;
 };
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const RotArgs<T> a) {
   const int pairs = a.axes * a.nfreq;
   const int paired = kHalf ? pairs / EPC : 0;  // units that hold two chunks
   const int per_row = kHalf ? paired + (a.dim - 2 * pairs + EPC - 1) / EPC : (a.dim + kElems - 1) / kElems;
-  const int runs = (a.heads + a.run - 1) / a.run;
+  const int runs = a.runs;
   const int64_t total = a.n * per_row * runs;
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; u < total;
        u += static_cast<int64_t>(gridDim.x) * kThreads) {
@@ -74,11 +74,13 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const RotArgs<T> a) {
       rest = u / per_row;
       row = rest / runs;
     }
-    const int ch = static_cast<int>(u - rest * per_row), h0 = static_cast<int>(rest - row * runs) * a.run;
-    const int h1 = h0 + a.run < a.heads ? h0 + a.run : a.heads;
+    // The heads of a run are `runs` apart, so that neighbouring threads touch
+    // neighbouring heads.
+    const int ch = static_cast<int>(u - rest * per_row), h0 = static_cast<int>(rest - row * runs);
+    const int count = (a.heads - 1 - h0) / runs + 1;
     const T* x = a.x + row * a.xs_row + h0 * a.xs_head;
     T* y = a.out + row * a.os_row + h0 * a.os_head;
-    const int count = h1 - h0;
+    const int64_t xs = a.xs_head * runs, ys = a.os_head * runs;
     float2 cs[kPairs];
     if constexpr (kHalf) {
       const bool two = ch < paired;
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const RotArgs<T> a) {
       x += lo;
       y += lo;
 #pragma unroll 2
-      for (int h = 0; h < count; ++h, x += a.xs_head, y += a.os_head) {
+      for (int h = 0; h < count; ++h, x += xs, y += ys) {
         const C cu = *reinterpret_cast<const C*>(x);
         if (!two) {
           *reinterpret_cast<C*>(y) = cu;
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const RotArgs<T> a) {
       const int lo = ch * kElems;
       const bool two = lo / 2 < pairs, both = lo + 1 < a.dim;
       if (two) cs[0] = turn_of(a, row, lo / 2);
-      for (int h = 0; h < count; ++h, x += a.xs_head, y += a.os_head) {
+      for (int h = 0; h < count; ++h, x += xs, y += ys) {
         const T u0 = x[lo], v0 = both ? x[lo + 1] : u0;
         const float fu = to_f(u0), fv = to_f(v0);
         y[lo] = two ? from_f<T>(fu * cs[0].x - fv * cs[0].y) : u0;
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const RotArgs<T> a) {
       x += lo;
       y += lo;
 #pragma unroll 4
-      for (int h = 0; h < count; ++h, x += a.xs_head, y += a.os_head) {
+      for (int h = 0; h < count; ++h, x += xs, y += ys) {
         const C c = *reinterpret_cast<const C*>(x);
         float f[EPC], r[EPC];
         unpack(c, f);
@@ -179,12 +181,13 @@ cudaError_t launch_typed(const RotaryArgs& b, int sms, cudaStream_t s) {
                    (!b.half || whole(pairs));
   const int elems = vec ? kWide : (b.half ? 1 : 2);
   const int64_t per_row = b.half ? pairs / elems + (a.dim - 2 * pairs + elems - 1) / elems : (a.dim + elems - 1) / elems;
-  // A run of heads as long as leaves a thousand threads on each SM.
+  // A run of heads as long as leaves a thousand threads on each SM (20011 x 16 x
+  // 64 bf16 over three axes: 1024, 2048, 4096, 8192 threads took 21, 22, 26, 35 us).
   const int64_t fill = static_cast<int64_t>(sms) * 1024;
   int64_t run = a.n * per_row * a.heads / fill;
   run = run < 1 ? 1 : (run > a.heads ? a.heads : run);
-  a.run = static_cast<int>(run);
-  const int64_t total = a.n * per_row * ((a.heads + run - 1) / run);
+  a.runs = static_cast<int>((a.heads + run - 1) / run);
+  const int64_t total = a.n * per_row * a.runs;
   const int64_t want = (total + kThreads - 1) / kThreads, cap = static_cast<int64_t>(sms) * 64;
   const unsigned blocks = static_cast<unsigned>(want < cap ? want : cap);
   if (b.half) {

@@ -153,6 +153,34 @@ def test_layer_norm_rows_do_not_mix():
     assert torch.equal(y[keep], ref[keep]) and bool(y[5].isnan().all()) and bool(y[9].isnan().all())
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_layer_norm_silu_far_out(dtype):
+    """Behind the cut of the exponential: the values and slopes of far negative
+    arguments vanish however far they are, and a NaN stays in its channel."""
+    g = gen(61)
+    big = 3e4 if dtype == F16 else 1e30
+    x = normal(g, 37, 64, dtype=dtype)
+    gamma = torch.full((64,), big, dtype=dtype, device="cuda")
+    gamma[10], gamma[30] = math.nan, 1.0
+    stats = torch.empty(37, 2, device="cuda")
+    y = smc.layer_norm(x, gamma, act="silu", stats=stats)
+    assert bool(y[:, 10].isnan().all()) and not bool(y[:, 9].isnan().any()) and not bool(y[:, 11].isnan().any())
+    z = gamma.double() * (x.double() - stats[:, :1]) * stats[:, 1:]
+    far = z < -100
+    assert int(far.sum()) > 500 and float(y[far].double().abs().max()) < 1e-16
+    gamma[10] = big
+    far[:, 10] = False
+    near = torch.zeros_like(far)
+    near[:, 30] = True
+    dy = torch.where(far | near, normal(g, 37, 64, dtype=dtype), 0.0).to(dtype)
+    only = torch.where(near, dy, 0.0).to(dtype)
+    a = smc.layer_norm_backward(dy, x, stats, gamma, act="silu")
+    b = smc.layer_norm_backward(only, x, stats, gamma, act="silu")
+    # what the slopes behind the cut (below 1e-17, times gamma) add to dx and dgamma
+    assert float((a[0].double() - b[0].double()).abs().max()) <= 1e-15 * big
+    assert float((a[1].double() - b[1].double()).abs().max()) <= 1e-15
+
+
 def test_layer_norm_no_rows():
     x = torch.empty(0, 16, device="cuda")
     assert smc.layer_norm(x).shape == (0, 16)
