@@ -421,6 +421,10 @@ SMC_API int smc_rotary(const void* x, const int64_t x_stride[2], int64_t n, int3
  * mask hides from a query must be finite, as in any product by zero.
  * Offsets that descend or leave [0, n] / [0, m] are cut to the buffers and
  * reported by smc_status as SMC_E_RANGE; the results are then undefined.
+ * Every block looks its share up in the offsets: up to a few thousand items
+ * cost one or two reads of them, more items grow with their number.
+ * Scratch (partial results, where the keys are split between blocks) comes from
+ * the library's stream-ordered pool.
  * Asynchronous on `stream`.  Errors: SMC_E_ARG, SMC_E_DTYPE, SMC_E_SHAPE (dim
  * above 128, heads not a multiple of kv_heads or over 64 of them sharing one,
  * rows beyond 2^31), SMC_E_ALIGN, SMC_E_ALIAS, SMC_E_OOM, SMC_E_CUDA.
@@ -439,10 +443,13 @@ SMC_API int smc_attention(const void* q, const int64_t q_stride[2], const void* 
  * out (dense) and lse as smc_attention wrote them; the other arguments as
  * there.  dout: device [n, heads, dim] with dout_stride.  dq: device [n, heads, dim], dk and dv:
  * device [m, kv_heads, dim], each with its strides (views of one packed
- * buffer may interleave); they must not overlap the inputs.  Gradients of
+ * buffer may interleave); they must not overlap the inputs or each other.  Gradients of
  * queries and keys that nothing pairs with are zero; rows outside every item
  * are left as they were.  No atomics: the same call gives the same bits.
- * Scratch (fp32 [n, heads]) comes from the library's stream-ordered pool.
+ * bf16 / fp16 inputs round P and dS to the input type for their products
+ * (fp16 under a power of two that keeps them in range).  Scratch (fp32 [n, heads]
+ * twice, and partial sums where the queries are split between blocks) comes
+ * from the library's stream-ordered pool.
  * Asynchronous on `stream`.  Errors as smc_attention.
  */
 SMC_API int smc_attention_backward(const void* dout, const int64_t dout_stride[2], const void* q,

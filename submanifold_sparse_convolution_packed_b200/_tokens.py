@@ -253,6 +253,8 @@ def _attention_shapes(q, k, v, offsets, k_offsets, scale):
         raise TypeError("q, k and v must share one dtype")
     if k.shape != v.shape or k.shape[2] != q.shape[2]:
         raise ValueError("k and v must be [M, kv_heads, D] with q's D")
+    if q.shape[2] < 1:
+        raise ValueError("a head must have channels")
     if q.shape[1] < 1 or k.shape[1] < 1 or q.shape[1] % k.shape[1] != 0:
         raise ValueError("the heads of q must be a multiple of those of k and v")
     if k_offsets is None:

@@ -79,13 +79,27 @@ uint32_t* g_status[kMaxDevices] = {};
 cudaMemPool_t g_pool[kMaxDevices] = {};
 std::mutex g_dev_mu;
 
+// A device's first call may come under a stream capture: what the library makes
+// for the device then is no part of it (and touches no stream that could be).
+struct Relaxed {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  Relaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~Relaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
 uint32_t* device_status(int dev) {
   if (dev < 0 || dev >= kMaxDevices) return nullptr;
   std::lock_guard<std::mutex> lk(g_dev_mu);
   if (!g_status[dev]) {
+    const Relaxed relaxed;
     void* p = nullptr;
-    if (cudaMalloc(&p, 256) != cudaSuccess) return nullptr;
-    if (cudaMemset(p, 0, 256) != cudaSuccess) return nullptr;
+    cudaStream_t s = nullptr;
+    bool ok = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) == cudaSuccess;
+    ok = ok && cudaMalloc(&p, 256) == cudaSuccess;
+    ok = ok && cudaMemsetAsync(p, 0, 256, s) == cudaSuccess && cudaStreamSynchronize(s) == cudaSuccess;
+    if (s) cudaStreamDestroy(s);
+    if (!ok && p) cudaFree(p);
+    if (!ok) return nullptr;
     g_status[dev] = static_cast<uint32_t*>(p);
   }
   return g_status[dev];
@@ -95,6 +109,7 @@ cudaMemPool_t device_pool(int dev) {
   if (dev < 0 || dev >= kMaxDevices) return nullptr;
   std::lock_guard<std::mutex> lk(g_dev_mu);
   if (!g_pool[dev]) {
+    const Relaxed relaxed;
     cudaMemPoolProps props;
     std::memset(&props, 0, sizeof(props));
     props.allocType = cudaMemAllocationTypePinned;
@@ -1198,8 +1213,8 @@ int smc_status(void* stream) {
   uint32_t h = 0;
   if (cudaMemcpy(&h, st, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return SMC_E_CUDA;
   if (h) cudaMemset(st, 0, sizeof(uint32_t));
-  if (h & smc::kErrRange) return SMC_E_RANGE;
-  return (h & smc::kErrTimeout) ? SMC_E_TIMEOUT : SMC_OK;
+  if (h & smc::kErrTimeout) return SMC_E_TIMEOUT;
+  return (h & smc::kErrRange) ? SMC_E_RANGE : SMC_OK;
 }
 
 }  // extern "C"

@@ -317,8 +317,18 @@ int smc_attention_backward(const void* dout, const int64_t dout_stride[2], const
   for (const Bytes& o : outs)
     for (const Bytes& i : ins)
       if (overlap(o, i)) return SMC_E_ALIAS;
-  // the three gradients may interleave (views of one packed buffer), but not start at the same place
-  if ((n > 0 && m > 0 && (dq == dk || dq == dv)) || (m > 0 && dk == dv)) return SMC_E_ALIAS;
+  // The three gradients may interleave (views of one packed buffer), but share
+  // no place: checked for their first heads, and for dense ones as a whole.
+  auto dense_rows = [&](const int64_t st[2], int64_t h) { return st[1] == dim && st[0] == h * dim; };
+  const uintptr_t head_bytes = static_cast<uintptr_t>(dim) * esz;
+  const bool whole[3] = {dense_rows(a.dq_stride, heads), dense_rows(a.dk_stride, kv_heads),
+                         dense_rows(a.dv_stride, kv_heads)};
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < i; ++j) {
+      if (outs[i].lo == outs[i].hi || outs[j].lo == outs[j].hi) continue;
+      const uintptr_t apart = outs[i].lo > outs[j].lo ? outs[i].lo - outs[j].lo : outs[j].lo - outs[i].lo;
+      if (apart < head_bytes || (whole[i] && whole[j] && overlap(outs[i], outs[j]))) return SMC_E_ALIAS;
+    }
   if (smc::pending_error() != SMC_OK) return SMC_E_CUDA;
   Device dev;
   if (!dev.ok()) return outcome(cudaErrorUnknown);
@@ -334,7 +344,7 @@ int smc_attention_backward(const void* dout, const int64_t dout_stride[2], const
   // scratch: delta and the scaled lse, [n, heads] each, two words, partial sums
   const bool tc = smc::attn_bwd_tc_supported(a);
   const int64_t count = n * heads, part = (2 * count + 2 + 63) / 64 * 64;
-  const int64_t floats = tc ? part + smc::attn_bwd_tc_scratch(a, dev.sms) : count;
+  const int64_t floats = part + (tc ? smc::attn_bwd_tc_scratch(a, dev.sms) : smc::attn_simt_bwd_scratch(a, dev.sms));
   void* scratch = nullptr;
   if (n > 0 && smc::scratch_alloc(&scratch, static_cast<size_t>(floats) * sizeof(float), dev.id, s) != cudaSuccess) {
     cudaGetLastError();
@@ -342,7 +352,7 @@ int smc_attention_backward(const void* dout, const int64_t dout_stride[2], const
   }
   a.delta = static_cast<float*>(scratch);
   const smc::BwdScratch x = {a.delta + count, reinterpret_cast<uint32_t*>(a.delta + 2 * count), a.delta + part};
-  const cudaError_t e = tc ? smc::launch_attn_bwd_tc(a, x, dev.sms, s) : smc::launch_attn_simt(a, true, nullptr, dev.sms, s);
+  const cudaError_t e = tc ? smc::launch_attn_bwd_tc(a, x, dev.sms, s) : smc::launch_attn_simt(a, true, x.part, dev.sms, s);
   if (scratch) cudaFreeAsync(scratch, s);
   return outcome(e);
 }

@@ -61,7 +61,7 @@ template <int DP, bool kDQ> struct BwdLayout {
   // there is room, the resident operands as 16-bit pairs.  From TMEM they cost
   // no shared-memory reads: with 64-column products those reads alone took 48
   // clocks an MMA where the MMA takes 32, and more beside the other traffic.
-  static constexpr bool kTmemA = kDQ || DP == 64;
+  static constexpr bool kTmemA = kDQ || DP == 64;  // else K and V in shared memory
   static constexpr int kBufs = kDQ && DP == 64 ? 3 : 2;
   static constexpr uint32_t kAcc = kBufs * 2 * kStep, kAt = kAcc + (kDQ ? 1 : 2) * DP;
   static_assert(kAt + (kTmemA ? DP : 0) <= 512, "TMEM columns");
@@ -82,11 +82,15 @@ __device__ __forceinline__ float ds_factor(const uint32_t* norms) {
   return exp2f(static_cast<float>(e));
 }
 
+// Maps of the passing operands and, where the resident ones are read from
+// shared memory, of those.
+struct BwdMaps {
+  CUtensorMap b1, b2, a1, a2;
+};
+
 template <typename T, int DP, bool kDQ>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_attn_bwd_tc(const __grid_constant__ CUtensorMap a1map, const __grid_constant__ CUtensorMap a2map,
-                  const __grid_constant__ CUtensorMap b1map, const __grid_constant__ CUtensorMap b2map,
-                  const BwdParams p) {
+    k_attn_bwd_tc(const __grid_constant__ BwdMaps maps, const BwdParams p) {
   using L = BwdLayout<DP, kDQ>;
   constexpr int kSlots = L::kSlots, kPanels = DP / 64, kBufs = L::kBufs;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -126,10 +130,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int nsteps = b_hi > b_lo ? (b_hi - b_lo + per_step - 1) / per_step : 0;
   if (tid == 0) {
-    prefetch_tmap(&a1map);
-    prefetch_tmap(&a2map);
-    prefetch_tmap(&b1map);
-    prefetch_tmap(&b2map);
+    prefetch_tmap(&maps.b1);
+    prefetch_tmap(&maps.b2);
     mbar_init(bar_a, L::kTmemA ? 16 : 1);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar_full + 8 * s, kDQ ? 1 : 33);
@@ -165,13 +167,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 17) {
     // ------------------------------------------------------------- TMA loads
     if (nsteps > 0) {
-      if (!L::kTmemA && lane == 0) {
-        const uint32_t rows = kDQ ? p.group * p.qpt : kRows;
-        mbar_arrive_expect_tx(bar_a, 2 * kPanels * rows * 128u);
-        const int head = kDQ ? hk * p.group : hk, row = (kDQ ? u.q.begin : u.k.begin) + r0;
+      if (!L::kTmemA && lane == 0) {  // K and V
+        mbar_arrive_expect_tx(bar_a, 2 * L::kResident);
         for (int c = 0; c < kPanels; ++c) {
-          tma_load_3d(sbase + L::kA + c * kPanel, &a1map, bar_a, c * 64, head, row);
-          tma_load_3d(sbase + L::kA + L::kResident + c * kPanel, &a2map, bar_a, c * 64, head, row);
+          tma_load_3d(sbase + L::kA + c * kPanel, &maps.a1, bar_a, c * 64, hk, u.k.begin + r0);
+          tma_load_3d(sbase + L::kA + L::kResident + c * kPanel, &maps.a2, bar_a, c * 64, hk, u.k.begin + r0);
         }
       }
       __syncwarp();
@@ -188,8 +188,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           mbar_arrive_expect_tx(bar, 2 * kPanels * static_cast<uint32_t>(rows_step) * 128u);
           for (int c = 0; c < kPanels; ++c) {
-            tma_load_3d(dst + c * kStepPanel, &b1map, bar, c * 64, head, base_row + b0);
-            tma_load_3d(dst + L::kPass + c * kStepPanel, &b2map, bar, c * 64, head, base_row + b0);
+            tma_load_3d(dst + c * kStepPanel, &maps.b1, bar, c * 64, head, base_row + b0);
+            tma_load_3d(dst + L::kPass + c * kStepPanel, &maps.b2, bar, c * 64, head, base_row + b0);
           }
         }
         if (!kDQ) {  // rows that are not there get 0: their S, dP and dO are 0 too, so they add nothing
@@ -587,7 +587,7 @@ BwdPlan bwd_plan(const AttnArgs& a, int sms) {
 }
 
 template <typename T, int DP>
-cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const CUtensorMap* maps, int sms, const BwdScratch& x, cudaStream_t st) {
+cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const BwdMaps* maps, int sms, const BwdScratch& x, cudaStream_t st) {
   float* lse2 = x.lse2;
   uint32_t* norms = a.dtype == kF16 ? x.norms : nullptr;
   const BwdPlan plan = bwd_plan(a, sms);
@@ -616,8 +616,7 @@ cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const CUtensorMap* maps
   resident(a.q, a.q_stride, a.dout, a.dout_stride);
   p.d1 = a.dq;
   for (int i = 0; i < 2; ++i) p.s1[i] = a.dq_stride[i];
-  kq<<<dim3(static_cast<unsigned>(a.n / p.qpt + a.items), a.kv_heads), kThreads, kSmemQ, st>>>(maps[0], maps[1], maps[2],
-                                                                                              maps[3], p);
+  kq<<<dim3(static_cast<unsigned>(a.n / p.qpt + a.items), a.kv_heads), kThreads, kSmemQ, st>>>(maps[0], p);
   resident(a.k, a.k_stride, a.v, a.v_stride);
   p.cut.per_tile = divisor(kRows);
   p.cut.by_keys = true;
@@ -630,7 +629,7 @@ cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const CUtensorMap* maps
     p.s2[i] = a.dv_stride[i];
   }
   const dim3 kgrid(static_cast<unsigned>(plan.units), a.kv_heads);
-  kk<<<kgrid, kThreads, kSmemK, st>>>(maps[4], maps[5], maps[6], maps[7], p);
+  kk<<<kgrid, kThreads, kSmemK, st>>>(maps[1], p);
   if (plan.chunk) {
     Cut tiles = p.cut;
     tiles.chunk = 0;
@@ -663,18 +662,18 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs& a, const BwdScratch& x, int sms, 
   BwdParams p = {};
   p.qpt = kRows / group;
   p.qps = kStep / group;
-  CUtensorMap maps[8];
+  BwdMaps maps[2] = {};  // dQ; dK and dV
   auto queries = [&](CUtensorMap* m, const void* t, const int64_t s[2], int per) {
     return make_map(m, t, a.dtype, a.n, a.heads, a.dim, s, group, per);
   };
   auto keys = [&](CUtensorMap* m, const void* t, const int64_t s[2], int per) {
     return make_map(m, t, a.dtype, a.m, a.kv_heads, a.dim, s, 1, per);
   };
-  if (!queries(&maps[0], a.q, a.q_stride, p.qpt) || !queries(&maps[1], a.dout, a.dout_stride, p.qpt) ||
-      !keys(&maps[2], a.k, a.k_stride, kStep) || !keys(&maps[3], a.v, a.v_stride, kStep) ||
-      !keys(&maps[4], a.k, a.k_stride, kRows) || !keys(&maps[5], a.v, a.v_stride, kRows) ||
-      !queries(&maps[6], a.q, a.q_stride, p.qps) || !queries(&maps[7], a.dout, a.dout_stride, p.qps))
-    return cudaErrorInvalidValue;
+  bool ok = keys(&maps[0].b1, a.k, a.k_stride, kStep) && keys(&maps[0].b2, a.v, a.v_stride, kStep) &&
+            queries(&maps[1].b1, a.q, a.q_stride, p.qps) && queries(&maps[1].b2, a.dout, a.dout_stride, p.qps);
+  if (ok && !BwdLayout<128, false>::kTmemA && a.dim > 64)
+    ok = keys(&maps[1].a1, a.k, a.k_stride, kRows) && keys(&maps[1].a2, a.v, a.v_stride, kRows);
+  if (!ok) return cudaErrorInvalidValue;
   p.cut = {a.q_off, a.k_off, static_cast<int32_t>(a.n), static_cast<int32_t>(a.m), a.items, 0, divisor(p.qpt), false};
   p.heads = a.heads;
   p.kv_heads = a.kv_heads;

@@ -27,8 +27,6 @@ inline int64_t split_words(const AttnArgs& a, int chunk) {
   return chunk ? ((a.m - 1) / chunk + 1) * a.n * a.heads * (a.dim + 2) : 0;
 }
 
-constexpr float kJoinLn2 = 0.6931471805599453f;
-
 struct JoinParams {
   Cut tiles;  // of queries, no splits
   int chunk, heads, dim, group;
@@ -82,7 +80,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const JoinParams p) {
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const float r4[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
     if (mine) *reinterpret_cast<Chunk<T, 4>*>(static_cast<T*>(p.out) + at * p.dim + 4 * lane) = pack<T, 4>(r4);
-    if (lane == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kJoinLn2;
+    if (lane == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
   }
 }
 

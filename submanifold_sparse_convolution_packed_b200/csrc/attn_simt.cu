@@ -17,7 +17,13 @@
 //
 // 64 x 64 tiles, 256 threads, each with 4 x 4 scores and 4 rows of the
 // accumulator; operands are fp32 in shared memory, rows padded by 16 bytes so
-// that the float4 reads along a row meet no bank twice.
+// that the float4 reads along a row meet no bank twice.  Bound by the FMA pipe in
+// principle (75 TFLOP/s), in fact by what stands between the products: the
+// exponentials, the passes of P through shared memory, and its reads (12
+// clocks of a warp's 64 in a product, four warps at once).  Where tiles leave the
+// machine idle, what passes is split between blocks.
+// fp32, items of 3000 and 1200 rows, 8 heads over 4, 32 / 64 / 128 channels:
+// forward 24 / 29 / 33 TFLOP/s, backward 18 / 22 / 21.
 #include "attn_join.cuh"
 #include "kernels.h"
 #include "tokens.cuh"
@@ -28,7 +34,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTile = 64;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ void cp_async16(float* dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
@@ -65,13 +70,15 @@ __device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t row_
   }
 }
 
-// acc[i][j] = A[4 ty + i] . B[tx + 16 j]
+// acc[i][j] = A[4 ty + i] . B[tx + 16 j], as pairs of channels (fma2: half of the
+// instructions for the same rate of the FMA pipe, which leaves room for the loads).
 template <int DP>
 __device__ __forceinline__ void mm_nt(const float* A, const float* B, int ty, int tx, float (&acc)[4][4]) {
+  float2 t[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) t[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
   for (int d = 0; d < DP; d += 4) {
     float4 a[4], b[4];
@@ -82,22 +89,38 @@ __device__ __forceinline__ void mm_nt(const float* A, const float* B, int ty, in
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[i][j] = fmaf(a[i].w, b[j].w, fmaf(a[i].z, b[j].z, fmaf(a[i].y, b[j].y, fmaf(a[i].x, b[j].x, acc[i][j]))));
+      for (int j = 0; j < 4; ++j) t[i][j] = fma2(make_float2(a[i].x, a[i].y), make_float2(b[j].x, b[j].y), t[i][j]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t[i][j] = fma2(make_float2(a[i].z, a[i].w), make_float2(b[j].z, b[j].w), t[i][j]);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = t[i][j].x + t[i][j].y;
 }
 
-// Column of the accumulator's element j of thread tx: runs of up to 4.
+// Column of the accumulator's element j of thread tx: runs of 2 or 4.
+constexpr int run_of(int dp) { return dp / 16 % 4 == 0 ? 4 : 2; }
+
 template <int DP>
 __device__ __forceinline__ int col_of(int tx, int j) {
-  constexpr int kRun = DP / 16 < 4 ? DP / 16 : 4;
+  constexpr int kRun = run_of(DP);
   return j / kRun * 16 * kRun + tx * kRun + j % kRun;
 }
 
-// acc[i][j] += sum_k P[4 ty + i][k] * B[k][col_of(tx, j)]
+// acc[i][j] += sum_k P[4 ty + i][k] * B[k][col_of(tx, j)].  The tile's sum is formed
+// by itself: a long item's sum is then two sums of about its root, where one
+// running sum was off by twice the plain products' error at 10,000 rows.
 template <int DP>
 __device__ __forceinline__ void mm_nn(const float* P, const float* B, int ty, int tx, float (&acc)[4][DP / 16]) {
-  constexpr int W = DP / 16, kRun = W < 4 ? W : 4;
+  constexpr int W = DP / 16, kRun = run_of(DP);
+  float2 t[4][W / 2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < W / 2; ++j) t[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 2
   for (int k = 0; k < kTile; k += 4) {
     float4 p[4];
@@ -110,28 +133,28 @@ __device__ __forceinline__ void mm_nn(const float* P, const float* B, int ty, in
       for (int j = 0; j < W; j += kRun) {
         const float* at = B + (k + kk) * (DP + 4) + col_of<DP>(tx, j);
         if constexpr (kRun == 4) {
-          const float4 t = *reinterpret_cast<const float4*>(at);
-          b[j] = t.x, b[j + 1] = t.y, b[j + 2] = t.z, b[j + 3] = t.w;
+          const float4 x = *reinterpret_cast<const float4*>(at);
+          b[j] = x.x, b[j + 1] = x.y, b[j + 2] = x.z, b[j + 3] = x.w;
         } else {
-          const float2 t = *reinterpret_cast<const float2*>(at);
-          b[j] = t.x, b[j + 1] = t.y;
+          const float2 x = *reinterpret_cast<const float2*>(at);
+          b[j] = x.x, b[j + 1] = x.y;
         }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float s = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
 #pragma unroll
-        for (int j = 0; j < W; ++j) acc[i][j] = fmaf(s, b[j], acc[i][j]);
+        for (int j = 0; j < W; j += 2) t[i][j / 2] = fma2(make_float2(s, s), make_float2(b[j], b[j + 1]), t[i][j / 2]);
       }
     }
   }
-}
-
-// Keys that query `qi` of an item sees: the first `seen` ones.
-__device__ __forceinline__ int32_t keys_seen(const Unit& u, int32_t qi, bool causal) {
-  if (!causal) return u.k.count;
-  const int64_t s = static_cast<int64_t>(qi) + u.k.count - u.q.count + 1;
-  return s < 0 ? 0 : (s > u.k.count ? u.k.count : static_cast<int32_t>(s));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < W; j += 2) {
+      acc[i][j] += t[i][j / 2].x;
+      acc[i][j + 1] += t[i][j / 2].y;
+    }
 }
 
 template <typename T, int DP>
@@ -256,7 +279,8 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
 // kDQ: a tile of packed queries against all its keys -> dQ.  Otherwise a tile
 // of keys against all its packed queries -> dK, dV.  A1, A2 stay; B1, B2 pass.
 template <typename T, int DP, bool kDQ>
-__global__ void __launch_bounds__(kThreads) k_attn_bwd(const AttnArgs a, const Cut cut, bool vec) {
+__global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) k_attn_bwd(const AttnArgs a, const Cut cut, bool vec,
+                                                                                    float* part) {
   extern __shared__ float sm[];
   __shared__ Unit unit;
   __shared__ float s_lse[kTile], s_delta[kTile];
@@ -304,21 +328,23 @@ __global__ void __launch_bounds__(kThreads) k_attn_bwd(const AttnArgs a, const C
     t0 = u.tile * per_tile * group;
     rows = all - t0 < per_tile * group ? all - t0 : per_tile * group;
     load_q(a1, a2, t0, rows);
-    first = 0;
+    first = u.split * cut.chunk;
     t1 = keys_seen(u, (t0 + rows - 1) / group, a.causal);
+    if (u.splits > 1 && t1 - first > cut.chunk) t1 = first + cut.chunk;
   } else {
     t0 = u.tile * kTile;
     rows = u.k.count - t0 < kTile ? u.k.count - t0 : kTile;
     load_k(a1, a2, t0);
     // the first query that sees key t0
     const int64_t f = a.causal ? static_cast<int64_t>(t0) + u.q.count - u.k.count : 0;
-    first = (f < 0 ? 0 : static_cast<int32_t>(f)) * group;
-    t1 = all;
+    const int32_t q_lo = u.split * cut.chunk;
+    first = (f < q_lo ? q_lo : static_cast<int32_t>(f)) * group;
+    t1 = u.splits > 1 && u.q.count - q_lo > cut.chunk ? (q_lo + cut.chunk) * group : all;
   }
   for (int32_t b0 = first; b0 < t1; b0 += kTile) {
     __syncthreads();
     if constexpr (kDQ) load_k(b1, b2, b0);
-    else load_q(b1, b2, b0, all - b0 < kTile ? all - b0 : kTile);
+    else load_q(b1, b2, b0, t1 - b0 < kTile ? t1 - b0 : kTile);
     cp_commit();
     cp_wait<0>();
     __syncthreads();
@@ -332,7 +358,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_bwd(const AttnArgs a, const C
         const int r = 4 * ty + i, x = tx + 16 * j;
         const int lr = kDQ ? r : x;  // the query's place in the tile
         const int32_t pq = (kDQ ? t0 + r : b0 + x), key = kDQ ? b0 + x : t0 + r;
-        const bool see = pq < all && key < keys_seen(u, pq / group, a.causal);
+        const bool see = pq < (kDQ ? all : t1) && key < keys_seen(u, pq / group, a.causal);
         const float p = see ? exp2f(s[i][j] * c - s_lse[lr]) : 0.f;
         s[i][j] = p;
         dp[i][j] = see ? p * (dp[i][j] - s_delta[lr]) : 0.f;
@@ -363,7 +389,16 @@ __global__ void __launch_bounds__(kThreads) k_attn_bwd(const AttnArgs a, const C
     for (int j = 0; j < W; ++j) {
       const int cc = col_of<DP>(tx, j);
       if (cc >= a.dim) continue;
-      if constexpr (kDQ) {
+      if (part) {  // a split: k_attn_bwd_sum adds them up
+        if constexpr (kDQ) {
+          const int64_t at = static_cast<int64_t>(u.q.begin + (t0 + r) / group) * a.heads + hk * group + (t0 + r) % group;
+          part[(u.split * a.n * a.heads + at) * a.dim + cc] = acc1[i][j] * a.scale;
+        } else {
+          const int64_t at = (u.split * a.m + u.k.begin + t0 + r) * a.kv_heads + hk;
+          part[2 * at * a.dim + cc] = acc1[i][j] * a.scale;
+          part[(2 * at + 1) * a.dim + cc] = acc2[i][j];
+        }
+      } else if constexpr (kDQ) {
         const int pr = t0 + r;
         static_cast<T*>(a.dq)[static_cast<int64_t>(u.q.begin + pr / group) * a.dq_stride[0] +
                               (hk * group + pr % group) * a.dq_stride[1] + cc] = from_f<T>(acc1[i][j] * a.scale);
@@ -373,6 +408,33 @@ __global__ void __launch_bounds__(kThreads) k_attn_bwd(const AttnArgs a, const C
         static_cast<T*>(a.dv)[row * a.dv_stride[0] + hk * a.dv_stride[1] + cc] = from_f<T>(acc2[i][j]);
       }
     }
+  }
+}
+
+// Adds up the splits of a tile's gradients, in order.
+template <typename T, bool kDQ>
+__global__ void __launch_bounds__(kThreads) k_attn_bwd_sum(const AttnArgs a, const Cut tiles, int chunk, const float* part) {
+  __shared__ Unit unit;
+  find_unit<kThreads>(tiles, blockIdx.x, &unit, a.err);
+  const Unit u = unit;
+  if (u.item < 0) return;
+  const int hk = blockIdx.y, group = kDQ ? a.heads / a.kv_heads : 1, per = static_cast<int>(tiles.per_tile.d);
+  const Span own = kDQ ? u.q : u.k;
+  const int32_t other = kDQ ? u.k.count : u.q.count, t0 = u.tile * per;
+  const int splits = other > chunk ? (other - 1) / chunk + 1 : 1;
+  const int rows = (own.count - t0 < per ? own.count - t0 : per) * group, width = (kDQ ? 1 : 2) * a.dim;
+  const int64_t step = (kDQ ? a.n * a.heads : a.m * a.kv_heads) * width;
+  for (int i = blockIdx.z * kThreads + threadIdx.x; i < rows * width; i += gridDim.z * kThreads) {
+    const int r = i / width, c = i - r * width;
+    const int64_t row = static_cast<int64_t>(own.begin) + t0 + r / group;
+    const int head = hk * group + r % group;
+    const float* from = part + (row * (kDQ ? a.heads : a.kv_heads) + head) * width + c;
+    float t = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) t += from[s * step];
+    if (kDQ) static_cast<T*>(a.dq)[row * a.dq_stride[0] + head * a.dq_stride[1] + c] = from_f<T>(t);
+    else if (c < a.dim) static_cast<T*>(a.dk)[row * a.dk_stride[0] + head * a.dk_stride[1] + c] = from_f<T>(t);
+    else static_cast<T*>(a.dv)[row * a.dv_stride[0] + head * a.dv_stride[1] + c - a.dim] = from_f<T>(t);
   }
 }
 
@@ -414,50 +476,88 @@ int split_of(const AttnArgs& a, int sms) {
   return fits ? attn::split_keys(a, kTile / (a.heads / a.kv_heads), 6ll * sms) : 0;
 }
 
+// Backward: rows of a split of what passes (keys for dQ, queries for dK and dV),
+// or 0: where the tiles leave half of the machine's places idle, for about two
+// and a half blocks to each, whole tiles of packed rows, at least two.
+int bwd_split(const AttnArgs& a, int sms, bool dq) {
+  const int group = a.heads / a.kv_heads, per = dq ? kTile / group : kTile;
+  const int64_t places = static_cast<int64_t>(sms) * (a.dim <= 64 ? 2 : 1);
+  const int64_t blocks = ((dq ? a.n : a.m) / per + a.items) * a.kv_heads, other = dq ? a.m : a.n;
+  if (2 * blocks > 3 * places || a.items == 0) return 0;
+  const int64_t runs = (5 * places / 2 + blocks - 1) / blocks, whole = dq ? kTile : kTile / group;
+  int64_t chunk = (other / runs + whole - 1) / whole * whole;
+  if (chunk < 2 * whole) chunk = 2 * whole;
+  return other <= chunk ? 0 : static_cast<int>(chunk);
+}
+
+// fp32 words of the splits' sums, of one of the launches.
+int64_t bwd_words(const AttnArgs& a, int sms, bool dq) {
+  const int chunk = bwd_split(a, sms, dq);
+  if (!chunk) return 0;
+  return dq ? ((a.m - 1) / chunk + 1) * a.n * a.heads * a.dim : ((a.n - 1) / chunk + 1) * a.m * a.kv_heads * 2 * a.dim;
+}
+
+// One of the backward pass's two launches and, where it is split, its sum.
+template <typename T, int DP, bool kDQ>
+cudaError_t launch_bwd(const AttnArgs& a, float* part, int sms, cudaStream_t s) {
+  const size_t bytes = (4 * kTile * (DP + 4) + kTile * (kTile + 4)) * sizeof(float);
+  const cudaError_t e = allow_smem(k_attn_bwd<T, DP, kDQ>, bytes);
+  if (e != cudaSuccess) return e;
+  const int per = kDQ ? kTile / (a.heads / a.kv_heads) : kTile, chunk = bwd_split(a, sms, kDQ);
+  const int64_t rows = kDQ ? a.n : a.m, other = kDQ ? a.m : a.n, tiles = rows / per + a.items;
+  const int64_t units = chunk ? tiles + (rows / per + 1) * (other / chunk) : tiles;
+  Cut cut = {a.q_off, a.k_off, static_cast<int32_t>(a.n), static_cast<int32_t>(a.m), a.items, chunk, divisor(per), !kDQ};
+  k_attn_bwd<T, DP, kDQ><<<dim3(static_cast<unsigned>(units), a.kv_heads), kThreads, bytes, s>>>(
+      a, cut, whole_pieces(a, true), chunk ? part : nullptr);
+  if (chunk) {
+    cut.chunk = 0;
+    k_attn_bwd_sum<T, kDQ><<<dim3(static_cast<unsigned>(tiles), a.kv_heads, 8), kThreads, 0, s>>>(a, cut, chunk, part);
+  }
+  count_launches(chunk ? 2 : 1);
+  return cudaGetLastError();
+}
+
 template <typename T, int DP>
-cudaError_t launch_dim(const AttnArgs& a, bool backward, float* scratch, int chunk, cudaStream_t s) {
+cudaError_t launch_dim(const AttnArgs& a, bool backward, float* scratch, int chunk, int sms, cudaStream_t s) {
   const int per_tile = kTile / (a.heads / a.kv_heads);
   int64_t units = a.n / per_tile + a.items;
   if (chunk) units += (a.n / per_tile + 1) * (a.m / chunk);
   const dim3 qgrid(static_cast<unsigned>(units), a.kv_heads);
   Cut cut = {a.q_off, a.k_off, static_cast<int32_t>(a.n), static_cast<int32_t>(a.m), a.items, chunk, divisor(per_tile), false};
-  const bool vec = whole_pieces(a, backward);
-  const size_t tile = kTile * (DP + 4) * sizeof(float), extra = kTile * (kTile + 4) * sizeof(float);
-  cudaError_t e;
   if (!backward) {
-    if ((e = allow_smem(k_attn<T, DP>, 3 * tile + extra)) != cudaSuccess) return e;
+    const size_t bytes = (3 * kTile * (DP + 4) + kTile * (kTile + 4)) * sizeof(float);
+    const cudaError_t e = allow_smem(k_attn<T, DP>, bytes);
+    if (e != cudaSuccess) return e;
     float* part_ml = chunk ? scratch + ((a.m - 1) / chunk + 1) * a.n * a.heads * a.dim : nullptr;
-    k_attn<T, DP><<<qgrid, kThreads, 3 * tile + extra, s>>>(a, cut, vec, chunk ? scratch : nullptr, part_ml);
+    k_attn<T, DP><<<qgrid, kThreads, bytes, s>>>(a, cut, whole_pieces(a, false), chunk ? scratch : nullptr, part_ml);
     if (chunk) attn::launch_join<T>(a, cut, scratch, part_ml, s);
     count_launches(chunk ? 2 : 1);
     return cudaGetLastError();
   }
-  if ((e = allow_smem(k_attn_bwd<T, DP, true>, 4 * tile + extra)) != cudaSuccess) return e;
-  if ((e = allow_smem(k_attn_bwd<T, DP, false>, 4 * tile + extra)) != cudaSuccess) return e;
-  const int64_t warps = a.n * a.heads, want = (warps + 7) / 8;
+  const int64_t want = (a.n * a.heads + 7) / 8;
   if (a.n > 0) {
     k_attn_delta<T><<<static_cast<unsigned>(want < 4096 ? want : 4096), kThreads, 0, s>>>(a);
-    k_attn_bwd<T, DP, true><<<qgrid, kThreads, 4 * tile + extra, s>>>(a, cut, vec);
-    count_launches(2);
-  }
-  if (a.m > 0) {
-    const dim3 kgrid(static_cast<unsigned>(a.m / kTile + a.items), a.kv_heads);
-    cut.per_tile = divisor(kTile);
-    cut.by_keys = true;
-    k_attn_bwd<T, DP, false><<<kgrid, kThreads, 4 * tile + extra, s>>>(a, cut, vec);
     count_launches(1);
+    const cudaError_t e = launch_bwd<T, DP, true>(a, scratch, sms, s);
+    if (e != cudaSuccess) return e;
   }
-  return cudaGetLastError();
+  return a.m > 0 ? launch_bwd<T, DP, false>(a, scratch, sms, s) : cudaSuccess;
 }
 
 template <typename T>
-cudaError_t launch_typed(const AttnArgs& a, bool backward, float* scratch, int chunk, cudaStream_t s) {
-  if (a.dim <= 32) return launch_dim<T, 32>(a, backward, scratch, chunk, s);
-  if (a.dim <= 64) return launch_dim<T, 64>(a, backward, scratch, chunk, s);
-  return launch_dim<T, 128>(a, backward, scratch, chunk, s);
+cudaError_t launch_typed(const AttnArgs& a, bool backward, float* scratch, int chunk, int sms, cudaStream_t s) {
+  if (a.dim <= 32) return launch_dim<T, 32>(a, backward, scratch, chunk, sms, s);
+  if (a.dim <= 64) return launch_dim<T, 64>(a, backward, scratch, chunk, sms, s);
+  if (a.dim <= 96) return launch_dim<T, 96>(a, backward, scratch, chunk, sms, s);
+  return launch_dim<T, 128>(a, backward, scratch, chunk, sms, s);
 }
 
 }  // namespace
+
+int64_t attn_simt_bwd_scratch(const AttnArgs& a, int sms) {
+  const int64_t q = bwd_words(a, sms, true), k = bwd_words(a, sms, false);
+  return q > k ? q : k;  // one after the other
+}
 
 int64_t attn_simt_scratch(const AttnArgs& a, int sms) {
   return attn::split_words(a, split_of(a, sms)) * static_cast<int64_t>(sizeof(float));
@@ -466,9 +566,9 @@ int64_t attn_simt_scratch(const AttnArgs& a, int sms) {
 cudaError_t launch_attn_simt(const AttnArgs& a, bool backward, void* scratch, int sms, cudaStream_t s) {
   const int chunk = backward ? 0 : split_of(a, sms);
   float* x = static_cast<float*>(scratch);
-  if (a.dtype == kF32) return launch_typed<float>(a, backward, x, chunk, s);
-  if (a.dtype == kBF16) return launch_typed<__nv_bfloat16>(a, backward, x, chunk, s);
-  return launch_typed<__half>(a, backward, x, chunk, s);
+  if (a.dtype == kF32) return launch_typed<float>(a, backward, x, chunk, sms, s);
+  if (a.dtype == kBF16) return launch_typed<__nv_bfloat16>(a, backward, x, chunk, sms, s);
+  return launch_typed<__half>(a, backward, x, chunk, sms, s);
 }
 
 }  // namespace smc

@@ -1,5 +1,5 @@
-// Shared by the tensor-core attention kernels: packing of fp32 pairs, the
-// causal limit, the TMA maps of [rows, heads, dim] tensors.
+// Shared by the tensor-core attention kernels: packing of fp32 pairs,
+// stores of whole rows, the TMA maps of [rows, heads, dim] tensors.
 #pragma once
 
 #include <cuda.h>
@@ -13,7 +13,6 @@
 namespace smc {
 namespace attn {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kRows = 128;                // rows of a resident tile
 constexpr uint32_t kPanel = kRows * 128;  // 128 rows of 64 16-bit channels
 
@@ -25,13 +24,6 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, f
 template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Keys that query `qi` of an item sees: the first ones, this many.
-__device__ __forceinline__ int32_t keys_seen(const Unit& u, int64_t qi, bool causal) {
-  if (!causal) return u.k.count;
-  const int64_t s = qi + u.k.count - u.q.count + 1;
-  return s < 0 ? 0 : (s > u.k.count ? u.k.count : static_cast<int32_t>(s));
 }
 
 // Stores 32 columns of a warp's 32 rows, one row per lane in o, through 2 KB of

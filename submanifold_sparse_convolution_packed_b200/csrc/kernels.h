@@ -217,8 +217,9 @@ struct AttnArgs {
   int64_t dq_stride[2], dk_stride[2], dv_stride[2];
 };
 // FMA kernels: every dtype, dim <= 128, heads / kv_heads <= 64; scratch of
-// attn_simt_scratch bytes (forward).
+// attn_simt_scratch bytes (forward) or attn_simt_bwd_scratch fp32 words.
 int64_t attn_simt_scratch(const AttnArgs& a, int sms);
+int64_t attn_simt_bwd_scratch(const AttnArgs& a, int sms);
 cudaError_t launch_attn_simt(const AttnArgs& a, bool backward, void* scratch, int sms, cudaStream_t s);
 
 // tcgen05 kernels (attn_tc.cu): bf16 / fp16, dim a multiple of 8, 16-byte

@@ -27,7 +27,6 @@ namespace smc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr float kLog2e = 1.4426950408889634f;
 
 // 1 / (1 + exp(-z)).  fp32 rows take the accurate exponential and a division;
 // the others the fast exponential (an error of a few fp32 ulp, far below the

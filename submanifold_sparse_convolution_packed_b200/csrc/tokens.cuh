@@ -12,6 +12,8 @@
 
 namespace smc {
 
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -154,6 +156,13 @@ struct Unit {
   int32_t item, tile, split, splits;
   Span q, k;
 };
+
+// Keys that query `qi` of an item sees: the first ones, this many.
+__device__ __forceinline__ int32_t keys_seen(const Unit& u, int64_t qi, bool causal) {
+  if (!causal) return u.k.count;
+  const int64_t s = qi + u.k.count - u.q.count + 1;
+  return s < 0 ? 0 : (s > u.k.count ? u.k.count : static_cast<int32_t>(s));
+}
 
 // How the items' rows are cut into units: tiles of per_tile.d rows (queries, or
 // keys with by_keys) x splits of `chunk` rows of the other side (0: one split).

@@ -3,6 +3,10 @@ forms.  Tolerances count roundings: u = eps / 2 of the type relative to the
 value for its one rounding, and multiples of 2^-24 of the magnitudes that enter
 for the fp32 arithmetic before it."""
 import math
+import os
+import subprocess
+import sys
+import threading
 
 import pytest
 import torch
@@ -427,6 +431,46 @@ def test_attention_many_items_and_splits(case, dtype):
     assert all(torch.equal(x, y) for x, y in zip(got, again))
 
 
+# splits of the FMA kernels: groups that do not divide a tile, odd widths, items
+# of different lengths, keys that no query sees
+@pytest.mark.parametrize("ql, kl, h, hk, d, causal, dtype", [
+    ([1000, 7], [300, 900], 3, 1, 33, False, F32), ([1000, 7], [300, 900], 3, 1, 33, True, BF16),
+    ([500], [2000], 5, 1, 20, True, F16), ([2000, 0, 90], [500, 30, 0], 7, 1, 128, True, F32),
+    ([63], [129], 1, 1, 96, False, F32), ([1], [4000], 2, 2, 64, False, F32), ([4000], [1], 2, 2, 16, True, F32)])
+def test_attention_gradients_of_split_rows(ql, kl, h, hk, d, causal, dtype):
+    g = gen(300 + d)
+    qo, ko = offsets_of(ql), offsets_of(kl)
+    q, dout = (normal(g, sum(ql), h, d, dtype=dtype) for _ in range(2))
+    k, v = (normal(g, sum(kl), hk, d, dtype=dtype) for _ in range(2))
+    lse = torch.empty(sum(ql), h, device="cuda")
+    out = smc.attention(q, k, v, qo, ko, causal=causal, lse=lse)
+    got = smc.attention_backward(dout, q, k, v, out, lse, qo, ko, causal=causal)
+    r = attention_ref(q, k, v, qo, ko, d ** -0.5, causal, dout, out, lse)
+    for x, y in zip(("dq", "dk", "dv"), got):
+        close(y, r[x], r["t" + x], x)
+    again = smc.attention_backward(dout, q, k, v, out, lse, qo, ko, causal=causal)
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
+    smc.status()
+
+
+def test_attention_gradients_of_long_sums():
+    """12,000 packed rows in one fp32 sum: 188 sums of 64.  Each term is off by
+    about 8 x 2^-24 (its score's and its exponent's rounding), independently of
+    the others; the roundings of the sums of 64 and of their sum add, as a random
+    walk over growing partial sums, at most sqrt(64) and sqrt(188) times 2^-24 of
+    them: sqrt(8^2 + 8^2 + 14^2) = 18 x 2^-24 in the norm."""
+    g = gen(330)
+    o = offsets_of([3000])
+    q, dout = normal(g, 3000, 4, 64), normal(g, 3000, 4, 64)
+    k, v = normal(g, 3000, 1, 64), normal(g, 3000, 1, 64)
+    lse = torch.empty(3000, 4, device="cuda")
+    out = smc.attention(q, k, v, o, causal=True, lse=lse)
+    got = smc.attention_backward(dout, q, k, v, out, lse, o, causal=True)
+    r = attention_ref(q, k, v, o, o, 64 ** -0.5, True, dout, out, lse)
+    for x, y in zip(("dq", "dk", "dv"), got):
+        assert float((y.double() - r[x]).norm() / r[x].norm()) <= 18 * E, x
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 @pytest.mark.parametrize("d", [64, 128, 20])
 def test_attention_rows_outside_items(dtype, d):
@@ -588,6 +632,65 @@ def test_streams_and_graphs(dtype):
                 gr.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(outs[0] + outs[1], ra + rb))
+    smc.status()
+
+
+FIRST_CALL = """
+import torch
+import submanifold_sparse_convolution_packed_b200 as smc
+g = torch.Generator(device="cuda").manual_seed(1)
+q, k, v, d = (torch.randn(300, 2, 64, generator=g, device="cuda").bfloat16() for _ in range(4))
+x, w = q.view(300, 128), torch.ones(128, dtype=torch.bfloat16, device="cuda")
+o = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+st, lse = torch.empty(300, 2, device="cuda"), torch.empty(300, 2, device="cuda")
+torch.cuda.synchronize()
+
+def calls():
+    out = smc.attention(q, k, v, o, lse=lse)
+    y = smc.layer_norm(x, w, w, stats=st)
+    return [out, y, *smc.attention_backward(d, q, k, v, out, lse, o), *smc.layer_norm_backward(x, x, st, w, w)]
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = calls()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, calls()))
+smc.status()
+print("ok")
+"""
+
+
+def test_first_call_of_a_process_may_be_captured():
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, timeout=120,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]
+
+
+def test_two_threads_at_once():
+    sets = [_chain_inputs(s) for s in (20, 21)]
+    refs = [_chain(*i) for i in sets]
+    torch.cuda.synchronize()
+    outs, errors = [None, None], []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    outs[i] = _chain(*sets[i])
+            s.synchronize()
+        except Exception as e:  # the main thread reports it
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for got, ref in zip(outs, refs):
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
     smc.status()
 
 

@@ -113,6 +113,17 @@ def test_attention_backward_refuses(code, call):
     assert attn_bwd(**call) == code
 
 
+def test_attention_backward_refuses_gradients_that_overlap():
+    def place(k, more):
+        return P(4096 + k * 64 * MB + more)
+
+    # dense gradients of 8 rows: dq 4096 bytes, dk and dv 2048
+    assert attn_bwd(dk=place(8, 4094)) == ALIAS and attn_bwd(dv=place(9, 2046)) == ALIAS
+    # views of packed rows that are half a head apart
+    assert attn_bwd(dqs=s2(512, 64), dk=place(8, 64), dks=s2(512, 64)) == ALIAS
+    assert attn_bwd(dks=s2(512, 64), dv=place(9, 126), dvs=s2(512, 64)) == ALIAS
+
+
 def test_nothing_to_do_is_fine():
     assert norm(n=0, x=None, out=None) == 0
     assert norm_bwd(n=0, dy=None, x=None, stats=None, dx=None) == 0
