@@ -59,13 +59,16 @@ def _result(out: Optional[torch.Tensor], shape, dtype, device, what: str, dense:
 
 
 def _last_dense(t: torch.Tensor) -> torch.Tensor:
-    return t if t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
+    return t if t.is_contiguous() or t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
 
 
 _Two = ctypes.c_int64 * 2
 
 
 def _strides(t: torch.Tensor):
+    """Of rows and heads; None (dense) spares the conversion."""
+    if t.is_contiguous():
+        return None
     s = t.stride()
     return _Two(s[0], s[1])
 
@@ -233,42 +236,42 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, layout
         with _On(dev, stream):
             return rotary(x, positions, freqs, layout, scale, inverse, out)
     x, freqs = _last_dense(x), freqs.contiguous()
-    out_stride = None  # dense
     if out is None:
-        out = torch.empty((n, h, d), dtype=x.dtype, device=x.device)
-    else:
-        out_stride = _strides(out)
+        out = x.new_empty((n, h, d))
     axes, f = freqs.shape
     _check(lib().smc_rotary(x.data_ptr(), _strides(x), n, h, d, positions.data_ptr(), _strides(positions),
                             freqs.data_ptr(), axes, f, ROTARY_LAYOUTS[layout], scale, 1 if inverse else 0,
-                            out.data_ptr(), out_stride, _DTYPES[x.dtype], _current_stream(dev)), "smc_rotary")
+                            out.data_ptr(), _strides(out), _DTYPES[x.dtype], _current_stream(dev)), "smc_rotary")
     return out
 
 
-def _attention_shapes(q, k, v, offsets, k_offsets, scale):
-    for t in (q, k, v):
-        if t.dtype not in _DTYPES or t.dim() != 3:
-            raise TypeError("q, k and v must be 3-D float32 / bfloat16 / float16 tensors [rows, heads, dim]")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+def _attention_sizes(q, k, v, offsets, k_offsets, scale):
+    """The checked sizes (n, h, d, m, hk, items), k_offsets and scale."""
+    dtype = q.dtype
+    if dtype not in _DTYPES or q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise TypeError("q, k and v must be 3-D float32 / bfloat16 / float16 tensors [rows, heads, dim]")
+    if k.dtype != dtype or v.dtype != dtype:
         raise TypeError("q, k and v must share one dtype")
-    if k.shape != v.shape or k.shape[2] != q.shape[2]:
+    n, h, d = q.shape
+    m, hk, dk = ks = k.shape
+    if v.shape != ks or dk != d:
         raise ValueError("k and v must be [M, kv_heads, D] with q's D")
-    if q.shape[2] < 1:
+    if d < 1:
         raise ValueError("a head must have channels")
-    if q.shape[1] < 1 or k.shape[1] < 1 or q.shape[1] % k.shape[1] != 0:
+    if h < 1 or hk < 1 or h % hk != 0:
         raise ValueError("the heads of q must be a multiple of those of k and v")
     if k_offsets is None:
-        if k.shape[0] != q.shape[0]:
+        if m != n:
             raise ValueError("k_offsets are needed where k has other rows than q")
         k_offsets = offsets
-    for o in (offsets, k_offsets):
+    for o in (offsets,) if k_offsets is offsets else (offsets, k_offsets):
         if o.dtype != torch.int32 or o.dim() != 1 or o.shape[0] < 1 or o.shape != offsets.shape:
             raise ValueError("offsets must be int32 [items + 1], the same items for q and k")
     if scale is None:
-        scale = q.shape[2] ** -0.5
+        scale = d ** -0.5
     if not (0.0 < scale < math.inf):
         raise ValueError("scale must be positive and finite")
-    return k_offsets, float(scale)
+    return (n, h, d, m, hk, offsets.shape[0] - 1), k_offsets, float(scale)
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor,
@@ -284,8 +287,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.
     `lse` (float32 [N, H]), if given, receives the log sum of exponentials,
     which attention_backward takes.  A query without keys gets zeros; rows
     outside every item are left as they were (unset in a new tensor)."""
-    k_offsets, scale = _attention_shapes(q, k, v, offsets, k_offsets, scale)
-    n, h, d = q.shape
+    (n, h, d, m, hk, items), k_offsets, scale = _attention_sizes(q, k, v, offsets, k_offsets, scale)
     if out is not None:
         _result(out, (n, h, d), q.dtype, q.device, "out")
     if lse is not None:
@@ -297,10 +299,9 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.
     q, k, v = _last_dense(q), _last_dense(k), _last_dense(v)
     offsets, k_offsets = offsets.contiguous(), k_offsets.contiguous()
     if out is None:
-        out = torch.empty((n, h, d), dtype=q.dtype, device=q.device)
-    m, hk, _ = k.shape
+        out = q.new_empty((n, h, d))
     _check(lib().smc_attention(q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), v.data_ptr(), _strides(v),
-                               offsets.data_ptr(), k_offsets.data_ptr(), offsets.shape[0] - 1, n, m, h, hk, d, scale,
+                               offsets.data_ptr(), k_offsets.data_ptr(), items, n, m, h, hk, d, scale,
                                1 if causal else 0, out.data_ptr(), _ptr(lse), _DTYPES[q.dtype], _current_stream(dev)),
            "smc_attention")
     return out
@@ -315,9 +316,7 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     [N, H, D], with the forward call's arguments, its out and its lse.  The
     gradients of shared key/value heads are summed.  dq, dk, dv may be given,
     also as views of one packed buffer.  Deterministic."""
-    k_offsets, scale = _attention_shapes(q, k, v, offsets, k_offsets, scale)
-    n, h, d = q.shape
-    m, hk = k.shape[:2]
+    (n, h, d, m, hk, items), k_offsets, scale = _attention_sizes(q, k, v, offsets, k_offsets, scale)
     if dout.shape != q.shape or dout.dtype != q.dtype or out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("dout and out must be [N, H, D] of q's dtype")
     if lse.shape != (n, h) or lse.dtype != torch.float32:
@@ -334,15 +333,14 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     out, lse = out.contiguous(), lse.contiguous()
     offsets, k_offsets = offsets.contiguous(), k_offsets.contiguous()
     if dq is None:
-        dq = torch.empty((n, h, d), dtype=q.dtype, device=q.device)
+        dq = q.new_empty((n, h, d))
     if dk is None:
-        dk = torch.empty((m, hk, d), dtype=q.dtype, device=q.device)
+        dk = q.new_empty((m, hk, d))
     if dv is None:
-        dv = torch.empty((m, hk, d), dtype=q.dtype, device=q.device)
+        dv = q.new_empty((m, hk, d))
     _check(lib().smc_attention_backward(dout.data_ptr(), _strides(dout), q.data_ptr(), _strides(q), k.data_ptr(),
                                         _strides(k), v.data_ptr(), _strides(v), out.data_ptr(), lse.data_ptr(),
-                                        offsets.data_ptr(), k_offsets.data_ptr(), offsets.shape[0] - 1, n, m, h, hk,
-                                        d, scale, 1 if causal else 0, dq.data_ptr(), _strides(dq), dk.data_ptr(),
+                                        offsets.data_ptr(), k_offsets.data_ptr(), items, n, m, h, hk, d, scale, 1 if causal else 0, dq.data_ptr(), _strides(dq), dk.data_ptr(),
                                         _strides(dk), dv.data_ptr(), _strides(dv), _DTYPES[q.dtype],
                                         _current_stream(dev)), "smc_attention_backward")
     return dq, dk, dv

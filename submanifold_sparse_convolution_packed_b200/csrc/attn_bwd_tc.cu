@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = mbar_wait_warp(bar_o, 0, p.err, p.wait_ns);
       tc_fence_after();
     }
-    if (ok && (kDQ || !p.part || nsteps > 0)) {  // (k_attn_bwd_join leaves out the splits without a step)
+    const bool split = !kDQ && u.splits > 1;
+    if (ok && (!split || nsteps > 0)) {  // (k_attn_bwd_join leaves out the splits without a step)
       // dQ: 32 columns each (64 channels: the first two groups); dK: groups 0
       // and 2, dV: 1 and 3, half of the columns each
       const int c_lo = kDQ ? 32 * w : half * (DP / 2), c_hi = kDQ ? (c_lo + 32 < DP ? c_lo + 32 : DP) : c_lo + DP / 2;
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] *= mul;
-        if (!kDQ && p.part) {  // a split: k_attn_bwd_join adds them up
+        if (split) {  // k_attn_bwd_join adds them up
           if (row) {
             float4* d = reinterpret_cast<float4*>(
                 p.part + (((static_cast<int64_t>(u.split) * p.cut.m + out_row) * p.kv_heads + hk) * 2 + (second ? 1 : 0)) * p.dim + c0);
@@ -472,7 +473,8 @@ __global__ void __launch_bounds__(256) k_attn_bwd_join(const BwdParams p, const 
   if (u.item < 0) return;
   const int hk = blockIdx.y, r0 = u.tile * kRows, quads = p.dim / 4;
   const int rows = u.k.count - r0 < kRows ? u.k.count - r0 : kRows;
-  const int splits = u.q.count > 0 ? (u.q.count - 1) / p.cut.chunk + 1 : 0;
+  if (u.q.count <= p.cut.chunk) return;  // one split, written as it is
+  const int splits = (u.q.count - 1) / p.cut.chunk + 1;
   // splits without a step have written nothing: those before the first query
   // that sees a key of the tile
   int s0 = 0;

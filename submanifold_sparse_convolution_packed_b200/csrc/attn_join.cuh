@@ -11,11 +11,12 @@ namespace smc {
 namespace attn {
 
 // Keys of a run, or 0 for no split: when tiles of `per` queries leave half of the
-// machine's `slots` for blocks idle, runs of about (keys x tiles) / slots, at
-// least 256 keys.
-inline int split_keys(const AttnArgs& a, int per, int64_t slots) {
+// machine's `slots` for blocks idle and there are `least` keys, runs of about
+// (keys x tiles) / slots, at least 256 keys.  Items of one run are written as they
+// are; the join passes over them.
+inline int split_keys(const AttnArgs& a, int per, int64_t slots, int64_t least) {
   const int64_t tiles = a.n / per + a.items;  // upper bound
-  if (2 * tiles * a.kv_heads > slots) return 0;
+  if (2 * tiles * a.kv_heads > slots || a.m < least) return 0;
   int64_t chunk = a.m * (a.n / per + 1) * a.kv_heads / slots;
   chunk = (chunk < 256 ? 256 : chunk + 127) / 128 * 128;
   return a.m <= chunk ? 0 : static_cast<int>(chunk);  // no item is longer than one run
@@ -48,9 +49,10 @@ __global__ void __launch_bounds__(256) k_attn_join(const JoinParams p) {
   const int hk = blockIdx.y, lane = threadIdx.x & 31;
   const int32_t per = static_cast<int32_t>(p.tiles.per_tile.d), q0 = u.tile * per;
   const int32_t queries = u.q.count - q0 < per ? u.q.count - q0 : per;
-  const int splits = u.k.count > p.chunk ? (u.k.count - 1) / p.chunk + 1 : 1;
+  if (u.k.count <= p.chunk) return;  // one run
+  const int splits = (u.k.count - 1) / p.chunk + 1;
   const int64_t step = static_cast<int64_t>(p.tiles.n) * p.heads;
-  for (int r = threadIdx.x >> 5; r < queries * p.group; r += 8) {
+  for (int r = blockIdx.z * 8 + (threadIdx.x >> 5); r < queries * p.group; r += gridDim.z * 8) {
     const int64_t at = static_cast<int64_t>(u.q.begin + q0 + r / p.group) * p.heads + hk * p.group + r % p.group;
     float top = -INFINITY;
     for (int s = lane; s < splits; s += 32) top = fmaxf(top, p.part_ml[2 * (at + s * step)]);
@@ -98,7 +100,9 @@ void launch_join(const AttnArgs& a, Cut cut, const float* part_o, const float* p
   p.out = a.out_w;
   p.lse = a.lse_w;
   p.err = a.err;
-  k_attn_join<T><<<dim3(static_cast<unsigned>(a.n / cut.per_tile.d + a.items), a.kv_heads), 256, 0, s>>>(p);
+  // a row takes a warp a microsecond, most of it latency: one or two rows to a warp
+  const unsigned rows = cut.per_tile.d * p.group, parts = rows < 16 ? 1 : rows / 16;
+  k_attn_join<T><<<dim3(static_cast<unsigned>(a.n / cut.per_tile.d + a.items), a.kv_heads, parts), 256, 0, s>>>(p);
 }
 
 }  // namespace attn

@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
     if (r >= rows) continue;
     const int64_t at = static_cast<int64_t>(u.q.begin + q0 + r / group) * a.heads + hk * group + r % group;
     const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];
-    if (part_o) {  // a split: unnormalised
+    if (u.splits > 1) {  // a split: unnormalised
       const int64_t slot = static_cast<int64_t>(u.split) * a.n * a.heads + at;
 #pragma unroll
       for (int j = 0; j < W; ++j) {
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) k_attn_bwd(const A
     for (int j = 0; j < W; ++j) {
       const int cc = col_of<DP>(tx, j);
       if (cc >= a.dim) continue;
-      if (part) {  // a split: k_attn_bwd_sum adds them up
+      if (u.splits > 1) {  // k_attn_bwd_sum adds the splits up
         if constexpr (kDQ) {
           const int64_t at = static_cast<int64_t>(u.q.begin + (t0 + r) / group) * a.heads + hk * group + (t0 + r) % group;
           part[(u.split * a.n * a.heads + at) * a.dim + cc] = acc1[i][j] * a.scale;
@@ -421,7 +421,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_bwd_sum(const AttnArgs a, con
   const int hk = blockIdx.y, group = kDQ ? a.heads / a.kv_heads : 1, per = static_cast<int>(tiles.per_tile.d);
   const Span own = kDQ ? u.q : u.k;
   const int32_t other = kDQ ? u.k.count : u.q.count, t0 = u.tile * per;
-  const int splits = other > chunk ? (other - 1) / chunk + 1 : 1;
+  if (other <= chunk) return;  // one split, written as it is
+  const int splits = (other - 1) / chunk + 1;
   const int rows = (own.count - t0 < per ? own.count - t0 : per) * group, width = (kDQ ? 1 : 2) * a.dim;
   const int64_t step = (kDQ ? a.n * a.heads : a.m * a.kv_heads) * width;
   for (int i = blockIdx.z * kThreads + threadIdx.x; i < rows * width; i += gridDim.z * kThreads) {
@@ -469,11 +470,12 @@ bool whole_pieces(const AttnArgs& a, bool backward) {
          (!backward || ok(a.dout, a.dout_stride));
 }
 
-// Runs of keys (attn_join.cuh), for three blocks to each of an SM's two places; the
-// join moves four channels at a time.
+// Runs of keys (attn_join.cuh), for three blocks to each of an SM's two places (one
+// query: 37 us split, 35 and 59 us whole over 300 and 600 keys); the join moves four
+// channels at a time.
 int split_of(const AttnArgs& a, int sms) {
   const bool fits = a.dim % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out_w) & 15u) == 0;
-  return fits ? attn::split_keys(a, kTile / (a.heads / a.kv_heads), 6ll * sms) : 0;
+  return fits ? attn::split_keys(a, kTile / (a.heads / a.kv_heads), 6ll * sms, 384) : 0;
 }
 
 // Backward: rows of a split of what passes (keys for dQ, queries for dK and dV),

@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
       }
       if (ok && used) {
         const int64_t at = static_cast<int64_t>(u.q.begin + q0 + t * p.qpt + qi) * p.heads + hk * p.group + r % p.group;
-        const bool split = p.part_o != nullptr;
+        const bool split = u.splits > 1;
         const int64_t slot = static_cast<int64_t>(u.split) * p.cut.n * p.heads + at;
         const float inv = sum == 0.f ? 0.f : 1.f / sum, f1 = split ? weight : weight * inv, f2 = split ? weight2 : weight2 * inv;
         const uint32_t to2 = tmem + lanes + L::kO + (g ^ 1) * DP;
@@ -486,7 +486,10 @@ FwdPlan fwd_plan(const AttnArgs& a, int sms) {
     const int64_t most = tiles * a.kv_heads / (4 * slots);
     s.heads = static_cast<int>(most < 1 ? 1 : most < a.kv_heads ? most : a.kv_heads);
   }
-  s.chunk = split_keys(a, per, slots);
+  // The join and its scratch cost 8 us of the device: one query of 8 heads of 64
+  // took 21 us split and 14, 21, 27 us whole over 300, 600, 1000 keys, 300 queries
+  // 25 to 29 us split and 17, 18, 25, 30 us whole over 300, 600, 1000, 1500 keys.
+  s.chunk = split_keys(a, per, slots, 1024);
   if (s.chunk) s.units += (a.n / per + 1) * (a.m / s.chunk);
   return s;
 }
