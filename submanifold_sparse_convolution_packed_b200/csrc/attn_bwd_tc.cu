@@ -6,10 +6,10 @@
 //
 // Two launches of one kernel.  A CTA keeps 128 rows of two operands in TMEM (or
 // shared memory; queries: Q and dO, for dQ; keys: K and V, for dK and dV) and
-// passes 64 rows of the other two through a ring in shared memory, so every sum over the passing rows
-// stays in one TMEM accumulator: no atomics, no fp32 copy of dQ in memory, and
-// the same bits every time, at the price of computing S and dP twice (7
-// products instead of 5).  The scores of the dK / dV launch are computed
+// passes 64 rows of the other two through a ring in shared memory, so every sum
+// over the passing rows stays in one TMEM accumulator: no atomics, no fp32 copy
+// of dQ in memory, and the same bits every time, at the price of computing S and
+// dP twice (7 products instead of 5).  The scores of the dK / dV launch are computed
 // transposed (keys are the rows), so that P^T and dS^T, written to TMEM by the
 // threads that hold their rows, are the A operands of the products as they
 // lie; Q, dO, K are read a second time from the same shared memory, MN-major.
@@ -23,6 +23,12 @@
 // norms of dO and V rows (|dP|, |delta| <= |dO| |V|), undone on the fp32
 // accumulators, so that the P of a long context do not fall below fp16's
 // range and dS cannot leave it.
+//
+// What bounds it: the chain of a step (products, scores of the step that takes
+// its buffer, TMEM to registers, exponentials, back to TMEM); the tensor cores work
+// about half of the time.  Measured, whole calls: 9,973 and 8,111 rows, 8 heads of
+// 64, bf16: 1.44 ms, 590 TFLOP/s of the five products (dQ 0.58, dK and dV 0.85 ms);
+// 6,007 rows, causal, 8 heads of 128 over 2, fp16: 0.33 ms, 560 TFLOP/s.
 #include <type_traits>
 
 #include "attn_tc.cuh"
@@ -501,9 +507,10 @@ __global__ void __launch_bounds__(256) k_attn_bwd_join(const BwdParams p, const 
 }
 
 // delta[row, head] = -sum of dO * O, and lse2 = -lse log2e, or -infinity for a
-// row that saw no key, whose P = exp2(S + lse2) is then 0; fp16: also the largest squared norms of
-// the rows of dO and of V that belong to items (as bits: they are not
-// negative).  LPR lanes hold a row of up to 8 LPR channels.
+// row that saw no key, whose P = exp2(S + lse2) is then 0; fp16: also the largest
+// squared norms of the rows of dO and of V that belong to items (as bits: they are
+// not negative; the order of the atomic maxima changes nothing).  LPR lanes hold a
+// row of up to 8 LPR channels.  Bound by HBM: one read of O and dO (and V).
 template <typename T, int LPR>
 __global__ void __launch_bounds__(256) k_attn_delta_tc(const AttnArgs a, float* lse2, uint32_t* norms) {
   using C = Chunk<T, 8>;

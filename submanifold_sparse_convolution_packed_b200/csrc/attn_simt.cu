@@ -21,7 +21,8 @@
 // principle (75 TFLOP/s), in fact by what stands between the products: the
 // exponentials, the passes of P through shared memory, and its reads (12
 // clocks of a warp's 64 in a product, four warps at once).  Where tiles leave the
-// machine idle, what passes is split between blocks.
+// machine idle, what passes is split between blocks.  A warp whose rows are not there
+// only loads: one query over 300 keys takes 25 us, 33 us with all warps at work.
 // fp32, items of 3000 and 1200 rows, 8 heads over 4, 32 / 64 / 128 channels:
 // forward 24 / 29 / 33 TFLOP/s, backward 18 / 22 / 21.
 #include "attn_join.cuh"
@@ -176,6 +177,7 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
   const T* v = static_cast<const T*>(a.v) + u.k.begin * a.v_stride[0] + hk * a.v_stride[1];
   load_tile<T, DP>(sq, q, a.q_stride[0], a.q_stride[1], hk * group, group, q0 * group, rows, a.dim, vec);
   const float c = a.scale * kLog2e;
+  const bool live = (ty & ~1) * 4 < rows;  // a warp without rows only loads (single tokens)
   int32_t seen[4];
   float top[4], sum[4], o[4][W];
 #pragma unroll
@@ -210,43 +212,45 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
     cp_wait<1>();
     __syncthreads();
     float s[4][4];
-    mm_nt<DP>(sq, sk, ty, tx, s);
+    if (live) mm_nt<DP>(sq, sk, ty, tx, s);
     __syncthreads();
     load_k(k0 + kTile);
+    if (live) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float m = -INFINITY;
+      for (int i = 0; i < 4; ++i) {
+        float m = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (k0 + tx + 16 * j >= seen[i]) s[i][j] = -INFINITY;
-        m = fmaxf(m, s[i][j]);
+        for (int j = 0; j < 4; ++j) {
+          if (k0 + tx + 16 * j >= seen[i]) s[i][j] = -INFINITY;
+          m = fmaxf(m, s[i][j]);
+        }
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        // top is the rounded product with c, so that an unchanged maximum keeps
+        // the sums by exactly 1 (a fused difference would be off by an ulp of
+        // the product, tile after tile)
+        m = fmaxf(__fmul_rn(m, c), top[i]);
+        const float base = m == -INFINITY ? 0.f : m;  // nothing seen yet: every term is exp2(-inf) = 0
+        const float keep = exp2f(top[i] - base);
+        float t = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = exp2f(fmaf(s[i][j], c, -base));
+          t += s[i][j];
+        }
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
+        sum[i] = sum[i] * keep + t;
+        top[i] = m;
+#pragma unroll
+        for (int j = 0; j < W; ++j) o[i][j] *= keep;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sp[(4 * ty + i) * (kTile + 4) + tx + 16 * j] = s[i][j];
       }
-#pragma unroll
-      for (int x = 8; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-      // top is the rounded product with c, so that an unchanged maximum keeps
-      // the sums by exactly 1 (a fused difference would be off by an ulp of
-      // the product, tile after tile)
-      m = fmaxf(__fmul_rn(m, c), top[i]);
-      const float base = m == -INFINITY ? 0.f : m;  // nothing seen yet: every term is exp2(-inf) = 0
-      const float keep = exp2f(top[i] - base);
-      float t = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[i][j] = exp2f(fmaf(s[i][j], c, -base));
-        t += s[i][j];
-      }
-#pragma unroll
-      for (int x = 8; x > 0; x >>= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
-      sum[i] = sum[i] * keep + t;
-      top[i] = m;
-#pragma unroll
-      for (int j = 0; j < W; ++j) o[i][j] *= keep;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sp[(4 * ty + i) * (kTile + 4) + tx + 16 * j] = s[i][j];
     }
     cp_wait<1>();
     __syncthreads();
-    mm_nn<DP>(sp, sv, ty, tx, o);
+    if (live) mm_nn<DP>(sp, sv, ty, tx, o);
     __syncthreads();
     load_v(k0 + kTile);
   }
@@ -348,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) k_attn_bwd(const A
     cp_commit();
     cp_wait<0>();
     __syncthreads();
+    if ((ty & ~1) * 4 >= rows) continue;  // a warp without rows only loads
     float s[4][4], dp[4][4];
     mm_nt<DP>(a1, b1, ty, tx, s);
     mm_nt<DP>(a2, b2, ty, tx, dp);
@@ -470,9 +475,9 @@ bool whole_pieces(const AttnArgs& a, bool backward) {
          (!backward || ok(a.dout, a.dout_stride));
 }
 
-// Runs of keys (attn_join.cuh), for three blocks to each of an SM's two places (one
-// query: 37 us split, 35 and 59 us whole over 300 and 600 keys); the join moves four
-// channels at a time.
+// Runs of keys (attn_join.cuh), for three blocks to each of an SM's two places (64
+// queries, 8 heads of 64 over 2: 39 us split, 35 and 59 us whole over 300 and 600
+// keys); the join moves four channels at a time.
 int split_of(const AttnArgs& a, int sms) {
   const bool fits = a.dim % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out_w) & 15u) == 0;
   return fits ? attn::split_keys(a, kTile / (a.heads / a.kv_heads), 6ll * sms, 384) : 0;

@@ -7,9 +7,9 @@
 // key/value head against a run of the item's keys, 128 (or 64) at a time.  Its
 // warps:
 //   softmax    four for each tile and, with two tiles of up to 64 channels, for
-//              each half of a step's columns: one thread per row, its scores in registers,
-//              running maximum and sum in fp32, P rounded to the input type
-//              into the TMEM columns its scores came from;
+//              each half of a step's columns: one thread per row, its scores in
+//              registers, running maximum and sum in fp32, P rounded to the input
+//              type into the TMEM columns its scores came from;
 //   MMA        one for each tile: S = Q K^T (both from shared memory), then
 //              O += P V with P in TMEM and V read MN-major as it lies;
 //   TMA        the Q tiles once, then K and V tiles into a ring.
@@ -25,6 +25,12 @@
 // With few queries over many keys the keys are split between CTAs; each writes
 // its unnormalised fp32 O, maximum and sum, and k_attn_join adds them up in
 // order.
+//
+// What bounds it: at 64 channels the exponentials (16 a clock and SM: 0.71 ms of
+// the first figure), not the products (0.50 ms); a chain's own latency for the rest.
+// Measured: 20,011 rows, 8 heads of 64, bf16: 1.08 ms, 760 TFLOP/s; 512 items of 1 to
+// 512 rows, fp16: 0.26 ms; 8 single queries over 1,000 to 32,768 keys, 16 heads of
+// 128 over 4: 61 us, 3.9 TB/s.
 #include <type_traits>
 
 #include "attn_join.cuh"

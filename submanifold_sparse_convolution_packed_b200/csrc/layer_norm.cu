@@ -10,9 +10,14 @@
 //
 // Both are bound by HBM: each row is read once into registers (two passes over
 // the registers for mean and variance, fp32) and written once.  A group of
-// TPR lanes holds a row as 16-byte chunks; blocks are persistent and fetch the
-// next row before they work on the current one, and gamma and beta stay in
-// registers.  The backward pass keeps the channel sums of its rows in
+// TPR lanes holds a row as 16-byte chunks; blocks are persistent, and the forward
+// pass fetches the next row before it works on the current one and keeps gamma and
+// beta in registers.  16-bit rows with SiLU come near the special-function unit's
+// bound as well (an exponential and half a reciprocal for each value).
+// Measured: 1,300,007 x 64 fp16 with SiLU 77 us (4.5 TB/s), 410 x 16 fp32 1.7 us;
+// gradients of 133,450 x 128 bf16 with SiLU 34 us (3.1 TB/s: the sums over the rows
+// take the registers that more loads in flight would need), of 20,011 x 512 fp32
+// 23 us (5.3 TB/s).  The backward pass keeps the channel sums of its rows in
 // registers (fp32, a few hundred rows each), adds them up per block in a fixed
 // order and leaves one partial row per block, which k_ln_fold adds in fp64:
 // no atomics, so the same call gives the same bits.
