@@ -94,9 +94,9 @@ struct BwdMaps {
   CUtensorMap b1, b2, a1, a2;
 };
 
+// Unit `ux` of the dQ (kDQ) or of the dK / dV blocks.
 template <typename T, int DP, bool kDQ>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_attn_bwd_tc(const __grid_constant__ BwdMaps maps, const BwdParams p) {
+__device__ __forceinline__ void gradients(const BwdMaps& maps, const BwdParams& p, int64_t ux) {
   using L = BwdLayout<DP, kDQ>;
   constexpr int kSlots = L::kSlots, kPanels = DP / 64, kBufs = L::kBufs;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -110,7 +110,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar_s = bar_empty + 8 * kSlots, bar_p = bar_s + 8 * kBufs, bar_o = bar_p + 8 * kBufs, bar_tail = bar_o + 8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  const int64_t ux = kDQ && p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
   find_unit<kThreads>(p.cut, ux, &s_unit, p.err);
   if (s_unit.item < 0) return;
   const Unit u = s_unit;
@@ -468,6 +467,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
+// The dK / dV blocks first, which take longer, then those of dQ (causal: from the
+// tiles with the most keys down): one grid, so that neither waits for the other's
+// last blocks.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attn_bwd_tc(const __grid_constant__ BwdMaps kmaps, const __grid_constant__ BwdParams pk, uint32_t kunits,
+                  const __grid_constant__ BwdMaps qmaps, const __grid_constant__ BwdParams pq) {
+  if (blockIdx.x < kunits)
+    gradients<T, DP, false>(kmaps, pk, blockIdx.x);
+  else
+    gradients<T, DP, true>(qmaps, pq, pq.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x - kunits);
+}
+
 // Adds up the splits of a tile's dK and dV, in order; kJoinParts blocks to a tile.
 constexpr int kJoinParts = 8;
 
@@ -608,43 +620,43 @@ cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const BwdMaps* maps, in
     if (e != cudaSuccess) return e;
   }
   k_attn_delta_tc<T, DP / 8><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, lse2, norms);
-  constexpr int kSmemQ = static_cast<int>(BwdLayout<DP, true>::kTotal), kSmemK = static_cast<int>(BwdLayout<DP, false>::kTotal);
-  auto kq = k_attn_bwd_tc<T, DP, true>;
-  auto kk = k_attn_bwd_tc<T, DP, false>;
-  cudaError_t e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemQ);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemK);
+  constexpr uint32_t kSmemQ = BwdLayout<DP, true>::kTotal, kSmemK = BwdLayout<DP, false>::kTotal;
+  constexpr int kSmem = static_cast<int>(kSmemQ > kSmemK ? kSmemQ : kSmemK);
+  auto kern = k_attn_bwd_tc<T, DP>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  auto resident = [&](const void* x, const int64_t xs[2], const void* y, const int64_t ys[2]) {
-    p.a1 = x;
-    p.a2 = y;
+  BwdParams k = p;
+  auto resident = [](BwdParams& t, const void* x, const int64_t xs[2], const void* y, const int64_t ys[2]) {
+    t.a1 = x;
+    t.a2 = y;
     for (int i = 0; i < 2; ++i) {
-      p.a1s[i] = xs[i];
-      p.a2s[i] = ys[i];
+      t.a1s[i] = xs[i];
+      t.a2s[i] = ys[i];
     }
   };
-  resident(a.q, a.q_stride, a.dout, a.dout_stride);
+  resident(p, a.q, a.q_stride, a.dout, a.dout_stride);
   p.d1 = a.dq;
   for (int i = 0; i < 2; ++i) p.s1[i] = a.dq_stride[i];
-  kq<<<dim3(static_cast<unsigned>(a.n / p.qpt + a.items), a.kv_heads), kThreads, kSmemQ, st>>>(maps[0], p);
-  resident(a.k, a.k_stride, a.v, a.v_stride);
-  p.cut.per_tile = divisor(kRows);
-  p.cut.by_keys = true;
-  p.cut.chunk = plan.chunk;
-  p.part = plan.chunk ? x.part : nullptr;
-  p.d1 = a.dk;
-  p.d2 = a.dv;
+  resident(k, a.k, a.k_stride, a.v, a.v_stride);
+  k.cut.per_tile = divisor(kRows);
+  k.cut.by_keys = true;
+  k.cut.chunk = plan.chunk;
+  k.part = plan.chunk ? x.part : nullptr;
+  k.d1 = a.dk;
+  k.d2 = a.dv;
   for (int i = 0; i < 2; ++i) {
-    p.s1[i] = a.dk_stride[i];
-    p.s2[i] = a.dv_stride[i];
+    k.s1[i] = a.dk_stride[i];
+    k.s2[i] = a.dv_stride[i];
   }
-  const dim3 kgrid(static_cast<unsigned>(plan.units), a.kv_heads);
-  kk<<<kgrid, kThreads, kSmemK, st>>>(maps[1], p);
+  const int64_t qunits = a.n / p.qpt + a.items;
+  kern<<<dim3(static_cast<unsigned>(plan.units + qunits), a.kv_heads), kThreads, kSmem, st>>>(
+      maps[1], k, static_cast<uint32_t>(plan.units), maps[0], p);
   if (plan.chunk) {
-    Cut tiles = p.cut;
+    Cut tiles = k.cut;
     tiles.chunk = 0;
-    k_attn_bwd_join<T><<<dim3(static_cast<unsigned>(a.m / kRows + a.items), a.kv_heads, kJoinParts), 256, 0, st>>>(p, tiles);
+    k_attn_bwd_join<T><<<dim3(static_cast<unsigned>(a.m / kRows + a.items), a.kv_heads, kJoinParts), 256, 0, st>>>(k, tiles);
   }
-  count_launches(plan.chunk ? 4 : 3);
+  count_launches(plan.chunk ? 3 : 2);
   return cudaGetLastError();
 }
 
