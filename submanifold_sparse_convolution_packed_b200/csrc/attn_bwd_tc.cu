@@ -584,10 +584,13 @@ __global__ void __launch_bounds__(256) k_attn_delta_tc(const AttnArgs a, float* 
   if (threadIdx.x < 2) atomicMax(norms + threadIdx.x, s_top[threadIdx.x]);
 }
 
-// Where the tiles of keys do not fill the machine (shared heads: the heads of
-// a group are rows of one tile; causal: the first keys have all the work), the
-// queries in runs, for about two and a half CTAs to an SM, each of at least
-// 512 packed rows.
+// Where the tiles of keys do not fill the machine (shared heads: the heads of a
+// group are rows of one tile; causal: the first keys have all the work), the
+// queries in runs, for one CTA to an SM, or one and a half where the mask leaves
+// them unequal, each of at least 1024 packed rows.  (One, one and a half, two and
+// a half CTAs: 6,000 rows, 2 heads of 128 over 1, took 156, 191, 199 us; 6,007
+// causal rows, 8 heads of 128 over 2, 318, 287, 287 us.  Runs of 512 rows: 700 rows,
+// 4 heads of 64, 31 us, whole 25 us.)
 struct BwdPlan {
   int64_t units;
   int chunk;  // queries of a run, 0: all
@@ -595,13 +598,12 @@ struct BwdPlan {
 
 BwdPlan bwd_plan(const AttnArgs& a, int sms) {
   const int group = a.heads / a.kv_heads;
-  const int64_t tiles = a.m / kRows + a.items;
+  const int64_t tiles = a.m / kRows + a.items, blocks = tiles * a.kv_heads;
   BwdPlan b = {tiles, 0};
-  if (2 * tiles * a.kv_heads > 3ll * sms || a.items == 0) return b;
-  const int64_t runs = (5ll * sms / 2 + tiles * a.kv_heads - 1) / (tiles * a.kv_heads) * (a.items < 2 ? 1 : 2);
+  const int64_t runs = ((a.causal ? 3ll * sms / 2 : sms) + blocks - 1) / blocks;
   int64_t chunk = a.n / runs;
-  if (chunk < 512 / group) chunk = 512 / group;
-  if (a.n <= chunk) return b;
+  if (chunk < 1024 / group) chunk = 1024 / group;
+  if (runs < 2 || a.n <= chunk) return b;
   b.chunk = static_cast<int>(chunk);
   b.units = tiles + (a.m / kRows + 1) * (a.n / chunk);
   return b;
