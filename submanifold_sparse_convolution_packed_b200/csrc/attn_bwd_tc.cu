@@ -4,12 +4,12 @@
 //   P = exp2(S log2e - lse log2e),  dS = P * (dP - delta),  dP = dO V^T
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO
 //
-// Two launches of one kernel.  A CTA keeps 128 rows of two operands in TMEM (or
+// Two kinds of blocks in one grid.  A CTA keeps 128 rows of two operands in TMEM (or
 // shared memory; queries: Q and dO, for dQ; keys: K and V, for dK and dV) and
 // passes 64 rows of the other two through a ring in shared memory, so every sum
 // over the passing rows stays in one TMEM accumulator: no atomics, no fp32 copy
 // of dQ in memory, and the same bits every time, at the price of computing S and
-// dP twice (7 products instead of 5).  The scores of the dK / dV launch are computed
+// dP twice (7 products instead of 5).  The scores of the dK / dV blocks are computed
 // transposed (keys are the rows), so that P^T and dS^T, written to TMEM by the
 // threads that hold their rows, are the A operands of the products as they
 // lie; Q, dO, K are read a second time from the same shared memory, MN-major.
@@ -27,8 +27,8 @@
 // What bounds it: the chain of a step (products, scores of the step that takes
 // its buffer, TMEM to registers, exponentials, back to TMEM); the tensor cores work
 // about half of the time.  Measured, whole calls: 9,973 and 8,111 rows, 8 heads of
-// 64, bf16: 1.44 ms, 590 TFLOP/s of the five products (dQ 0.58, dK and dV 0.85 ms);
-// 6,007 rows, causal, 8 heads of 128 over 2, fp16: 0.33 ms, 560 TFLOP/s.
+// 64, bf16: 1.39 ms, 610 TFLOP/s of the five products; 6,007 rows, causal, 8 heads of
+// 128 over 2, fp16: 0.28 ms, 670 TFLOP/s.
 #include <type_traits>
 
 #include "attn_tc.cuh"
@@ -187,7 +187,7 @@ __device__ __forceinline__ void gradients(const BwdMaps& maps, const BwdParams& 
         if (!mbar_wait_warp(bar_empty + 8 * slot, parity, p.err, p.wait_ns)) break;
         const int32_t b0 = b_lo + j * per_step;
         const int rows = (b_hi - b0 < per_step ? b_hi - b0 : per_step) * (kDQ ? 1 : p.group);
-        // in the dQ launch b_hi may be the causal limit: rows behind it are the item's own, but not seen
+        // for dQ b_hi may be the causal limit: rows behind it are the item's own, but not seen
         const bool tail = rows < rows_step;
         const uint32_t dst = sbase + L::kB + slot * 2 * L::kPass, bar = tail ? bar_tail : bar_full + 8 * slot;
         if (lane == 0) {

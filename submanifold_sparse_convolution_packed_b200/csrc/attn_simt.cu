@@ -11,8 +11,8 @@
 // (row = query * G + head of the group), so a tile's keys and values are
 // loaded once for all of them, and the gradients of shared heads add up in one
 // accumulator.  One pass over the keys with a running maximum and sum; the
-// backward pass recomputes P from the saved lse in two kernels, one tile of
-// queries (dQ) or of keys (dK, dV) per block, so nothing is added with atomics
+// backward pass recomputes P from the saved lse twice, one tile of queries
+// (dQ) or of keys (dK, dV) per block, so nothing is added with atomics
 // and a call gives the same bits every time.
 //
 // 64 x 64 tiles, 256 threads, each with 4 x 4 scores and 4 rows of the
@@ -24,7 +24,7 @@
 // machine idle, what passes is split between blocks.  A warp whose rows are not there
 // only loads: one query over 300 keys takes 25 us, 33 us with all warps at work.
 // fp32, items of 3000 and 1200 rows, 8 heads over 4, 32 / 64 / 128 channels:
-// forward 24 / 29 / 33 TFLOP/s, backward 18 / 22 / 21.
+// forward 23 / 30 / 31 TFLOP/s, backward 21 / 25 / 25.
 #include "attn_join.cuh"
 #include "kernels.h"
 #include "tokens.cuh"
@@ -283,15 +283,14 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
 // kDQ: a tile of packed queries against all its keys -> dQ.  Otherwise a tile
 // of keys against all its packed queries -> dK, dV.  A1, A2 stay; B1, B2 pass.
 template <typename T, int DP, bool kDQ>
-__global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) k_attn_bwd(const AttnArgs a, const Cut cut, bool vec,
-                                                                                    float* part) {
+__device__ __forceinline__ void gradients(const AttnArgs& a, const Cut& cut, bool vec, float* part, int64_t ux) {
   extern __shared__ float sm[];
   __shared__ Unit unit;
   __shared__ float s_lse[kTile], s_delta[kTile];
   constexpr int LD = DP + 4, W = DP / 16;
   float *a1 = sm, *a2 = a1 + kTile * LD, *b1 = a2 + kTile * LD, *b2 = b1 + kTile * LD, *sp = b2 + kTile * LD;
   const int group = a.heads / a.kv_heads, per_tile = kTile / group;
-  find_unit<kThreads>(cut, blockIdx.x, &unit, a.err);
+  find_unit<kThreads>(cut, ux, &unit, a.err);
   if (unit.item < 0) return;
   const Unit u = unit;
   const int hk = blockIdx.y, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -416,11 +415,28 @@ __global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) k_attn_bwd(const A
   }
 }
 
+// One of the backward pass's two halves: how its rows are cut into blocks, and
+// where the sums of its splits go.
+struct Half {
+  Cut cut;
+  float* part;
+};
+
+// The dK / dV blocks, then those of dQ, in one grid: neither waits for the other's last.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1)
+    k_attn_bwd(const __grid_constant__ AttnArgs a, const Half hk, const Half hq, uint32_t kunits, bool vec) {
+  if (blockIdx.x < kunits) gradients<T, DP, false>(a, hk.cut, vec, hk.part, blockIdx.x);
+  else gradients<T, DP, true>(a, hq.cut, vec, hq.part, blockIdx.x - kunits);
+}
+
 // Adds up the splits of a tile's gradients, in order.
 template <typename T, bool kDQ>
-__global__ void __launch_bounds__(kThreads) k_attn_bwd_sum(const AttnArgs a, const Cut tiles, int chunk, const float* part) {
+__device__ __forceinline__ void add_splits(const AttnArgs& a, Cut tiles, const float* part, int64_t ux) {
   __shared__ Unit unit;
-  find_unit<kThreads>(tiles, blockIdx.x, &unit, a.err);
+  const int chunk = tiles.chunk;
+  tiles.chunk = 0;
+  find_unit<kThreads>(tiles, ux, &unit, a.err);
   const Unit u = unit;
   if (u.item < 0) return;
   const int hk = blockIdx.y, group = kDQ ? a.heads / a.kv_heads : 1, per = static_cast<int>(tiles.per_tile.d);
@@ -442,6 +458,12 @@ __global__ void __launch_bounds__(kThreads) k_attn_bwd_sum(const AttnArgs a, con
     else if (c < a.dim) static_cast<T*>(a.dk)[row * a.dk_stride[0] + head * a.dk_stride[1] + c] = from_f<T>(t);
     else static_cast<T*>(a.dv)[row * a.dv_stride[0] + head * a.dv_stride[1] + c - a.dim] = from_f<T>(t);
   }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_attn_bwd_sum(const AttnArgs a, const Half hk, const Half hq, uint32_t ktiles) {
+  if (blockIdx.x < ktiles) add_splits<T, false>(a, hk.cut, hk.part, blockIdx.x);
+  else add_splits<T, true>(a, hq.cut, hq.part, blockIdx.x - ktiles);
 }
 
 // delta[row, head] = sum of dO * O over the head, one warp each.
@@ -484,8 +506,10 @@ int split_of(const AttnArgs& a, int sms) {
 }
 
 // Backward: rows of a split of what passes (keys for dQ, queries for dK and dV),
-// or 0: where the tiles leave half of the machine's places idle, for about two
-// and a half blocks to each, whole tiles of packed rows, at least two.
+// or 0: where there are fewer than one and a half blocks to each of the machine's
+// places, for about two and a half, whole tiles of packed rows, at least two.  (One,
+// one and a half, two and a half, four blocks: 2500 causal rows, 8 heads of 128 over 2,
+// took 3188, 3188, 2503, 2480 us, 3000 rows, 4 heads of 64, 975, 914, 930, 937 us.)
 int bwd_split(const AttnArgs& a, int sms, bool dq) {
   const int group = a.heads / a.kv_heads, per = dq ? kTile / group : kTile;
   const int64_t places = static_cast<int64_t>(sms) * (a.dim <= 64 ? 2 : 1);
@@ -497,30 +521,39 @@ int bwd_split(const AttnArgs& a, int sms, bool dq) {
   return other <= chunk ? 0 : static_cast<int>(chunk);
 }
 
-// fp32 words of the splits' sums, of one of the launches.
+// fp32 words of the splits' sums.
 int64_t bwd_words(const AttnArgs& a, int sms, bool dq) {
   const int chunk = bwd_split(a, sms, dq);
   if (!chunk) return 0;
   return dq ? ((a.m - 1) / chunk + 1) * a.n * a.heads * a.dim : ((a.n - 1) / chunk + 1) * a.m * a.kv_heads * 2 * a.dim;
 }
 
-// One of the backward pass's two launches and, where it is split, its sum.
-template <typename T, int DP, bool kDQ>
-cudaError_t launch_bwd(const AttnArgs& a, float* part, int sms, cudaStream_t s) {
+template <typename T, int DP>
+cudaError_t launch_bwd(const AttnArgs& a, float* scratch, int sms, cudaStream_t s) {
   const size_t bytes = (4 * kTile * (DP + 4) + kTile * (kTile + 4)) * sizeof(float);
-  const cudaError_t e = allow_smem(k_attn_bwd<T, DP, kDQ>, bytes);
+  const cudaError_t e = allow_smem(k_attn_bwd<T, DP>, bytes);
   if (e != cudaSuccess) return e;
-  const int per = kDQ ? kTile / (a.heads / a.kv_heads) : kTile, chunk = bwd_split(a, sms, kDQ);
-  const int64_t rows = kDQ ? a.n : a.m, other = kDQ ? a.m : a.n, tiles = rows / per + a.items;
-  const int64_t units = chunk ? tiles + (rows / per + 1) * (other / chunk) : tiles;
-  Cut cut = {a.q_off, a.k_off, static_cast<int32_t>(a.n), static_cast<int32_t>(a.m), a.items, chunk, divisor(per), !kDQ};
-  k_attn_bwd<T, DP, kDQ><<<dim3(static_cast<unsigned>(units), a.kv_heads), kThreads, bytes, s>>>(
-      a, cut, whole_pieces(a, true), chunk ? part : nullptr);
-  if (chunk) {
-    cut.chunk = 0;
-    k_attn_bwd_sum<T, kDQ><<<dim3(static_cast<unsigned>(tiles), a.kv_heads, 8), kThreads, 0, s>>>(a, cut, chunk, part);
+  int64_t tiles[2], units[2];  // of dK and dV, of dQ
+  Half half[2];
+  for (int x = 0; x < 2; ++x) {
+    const bool dq = x == 1;
+    const int per = dq ? kTile / (a.heads / a.kv_heads) : kTile, chunk = bwd_split(a, sms, dq);
+    const int64_t rows = dq ? a.n : a.m, other = dq ? a.m : a.n;
+    tiles[x] = rows > 0 ? rows / per + a.items : 0;
+    units[x] = chunk ? tiles[x] + (rows / per + 1) * (other / chunk) : tiles[x];
+    half[x].cut = {a.q_off, a.k_off, static_cast<int32_t>(a.n), static_cast<int32_t>(a.m), a.items, chunk, divisor(per), !dq};
+    half[x].part = dq ? scratch + bwd_words(a, sms, false) : scratch;
   }
-  count_launches(chunk ? 2 : 1);
+  k_attn_bwd<T, DP><<<dim3(static_cast<unsigned>(units[0] + units[1]), a.kv_heads), kThreads, bytes, s>>>(
+      a, half[0], half[1], static_cast<uint32_t>(units[0]), whole_pieces(a, true));
+  count_launches(1);
+  for (int x = 0; x < 2; ++x)
+    if (!half[x].cut.chunk) tiles[x] = 0;  // nothing to add up
+  if (tiles[0] + tiles[1] > 0) {
+    k_attn_bwd_sum<T><<<dim3(static_cast<unsigned>(tiles[0] + tiles[1]), a.kv_heads, 8), kThreads, 0, s>>>(
+        a, half[0], half[1], static_cast<uint32_t>(tiles[0]));
+    count_launches(1);
+  }
   return cudaGetLastError();
 }
 
@@ -545,10 +578,8 @@ cudaError_t launch_dim(const AttnArgs& a, bool backward, float* scratch, int chu
   if (a.n > 0) {
     k_attn_delta<T><<<static_cast<unsigned>(want < 4096 ? want : 4096), kThreads, 0, s>>>(a);
     count_launches(1);
-    const cudaError_t e = launch_bwd<T, DP, true>(a, scratch, sms, s);
-    if (e != cudaSuccess) return e;
   }
-  return a.m > 0 ? launch_bwd<T, DP, false>(a, scratch, sms, s) : cudaSuccess;
+  return launch_bwd<T, DP>(a, scratch, sms, s);
 }
 
 template <typename T>
@@ -562,8 +593,7 @@ cudaError_t launch_typed(const AttnArgs& a, bool backward, float* scratch, int c
 }  // namespace
 
 int64_t attn_simt_bwd_scratch(const AttnArgs& a, int sms) {
-  const int64_t q = bwd_words(a, sms, true), k = bwd_words(a, sms, false);
-  return q > k ? q : k;  // one after the other
+  return bwd_words(a, sms, true) + bwd_words(a, sms, false);
 }
 
 int64_t attn_simt_scratch(const AttnArgs& a, int sms) {
