@@ -28,9 +28,9 @@
 //
 // What bounds it: at 64 channels the exponentials (16 a clock and SM: 0.71 ms of
 // the first figure), not the products (0.50 ms); a chain's own latency for the rest.
-// Measured: 20,011 rows, 8 heads of 64, bf16: 1.08 ms, 760 TFLOP/s; 512 items of 1 to
+// Measured: 20,011 rows, 8 heads of 64, bf16: 1.09 ms, 750 TFLOP/s; 512 items of 1 to
 // 512 rows, fp16: 0.26 ms; 8 single queries over 1,000 to 32,768 keys, 16 heads of
-// 128 over 4: 61 us, 3.9 TB/s.
+// 128 over 4: 62 us, 3.9 TB/s.
 #include <type_traits>
 
 #include "attn_join.cuh"
