@@ -111,7 +111,10 @@ __device__ __forceinline__ void gradients(const BwdMaps& maps, const BwdParams& 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   find_unit<kThreads>(p.cut, ux, &s_unit, p.err);
-  if (s_unit.item < 0) return;
+  if (s_unit.item < 0) {
+    grid_wait();  // a grid is complete only behind the one before it
+    return;
+  }
   const Unit u = s_unit;
   const int hk = blockIdx.y;
   // resident rows [r0, r0 + count) (queries or keys), passing rows [b_lo, b_hi)
@@ -166,6 +169,7 @@ __device__ __forceinline__ void gradients(const BwdMaps& maps, const BwdParams& 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_misc[0];
+  grid_wait();  // for delta, lse2 and the norms
 
   // Every wait is bounded; a role that gives up leaves its loop, and the others
   // then run out of their own waits.
@@ -488,6 +492,7 @@ __global__ void __launch_bounds__(256) k_attn_bwd_join(const BwdParams p, const 
   __shared__ Unit s_unit;
   find_unit<256>(tiles, blockIdx.x, &s_unit, p.err);
   const Unit u = s_unit;
+  grid_wait();
   if (u.item < 0) return;
   const int hk = blockIdx.y, r0 = u.tile * kRows, quads = p.dim / 4;
   const int rows = u.k.count - r0 < kRows ? u.k.count - r0 : kRows;
@@ -526,6 +531,7 @@ __global__ void __launch_bounds__(256) k_attn_bwd_join(const BwdParams p, const 
 template <typename T, int LPR>
 __global__ void __launch_bounds__(256) k_attn_delta_tc(const AttnArgs a, float* lse2, uint32_t* norms) {
   using C = Chunk<T, 8>;
+  allow_next();
   const int l = threadIdx.x % LPR;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * (256 / LPR), first = static_cast<int64_t>(blockIdx.x) * (256 / LPR);
   const bool in = 8 * l < a.dim;
@@ -625,7 +631,7 @@ cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const BwdMaps* maps, in
   constexpr uint32_t kSmemQ = BwdLayout<DP, true>::kTotal, kSmemK = BwdLayout<DP, false>::kTotal;
   constexpr int kSmem = static_cast<int>(kSmemQ > kSmemK ? kSmemQ : kSmemK);
   auto kern = k_attn_bwd_tc<T, DP>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   BwdParams k = p;
   auto resident = [](BwdParams& t, const void* x, const int64_t xs[2], const void* y, const int64_t ys[2]) {
@@ -651,12 +657,15 @@ cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const BwdMaps* maps, in
     k.s2[i] = a.dv_stride[i];
   }
   const int64_t qunits = a.n / p.qpt + a.items;
-  kern<<<dim3(static_cast<unsigned>(plan.units + qunits), a.kv_heads), kThreads, kSmem, st>>>(
-      maps[1], k, static_cast<uint32_t>(plan.units), maps[0], p);
+  e = launch_after(kern, dim3(static_cast<unsigned>(plan.units + qunits), a.kv_heads), kThreads, kSmem, st, maps[1], k,
+                   static_cast<uint32_t>(plan.units), maps[0], p);
+  if (e != cudaSuccess) return e;
   if (plan.chunk) {
     Cut tiles = k.cut;
     tiles.chunk = 0;
-    k_attn_bwd_join<T><<<dim3(static_cast<unsigned>(a.m / kRows + a.items), a.kv_heads, kJoinParts), 256, 0, st>>>(k, tiles);
+    e = launch_after(k_attn_bwd_join<T>, dim3(static_cast<unsigned>(a.m / kRows + a.items), a.kv_heads, kJoinParts), 256, 0,
+                     st, k, tiles);
+    if (e != cudaSuccess) return e;
   }
   count_launches(plan.chunk ? 3 : 2);
   return cudaGetLastError();

@@ -45,6 +45,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const JoinParams p) {
   __shared__ Unit s_unit;
   find_unit<256>(p.tiles, blockIdx.x, &s_unit, p.err);
   const Unit u = s_unit;
+  grid_wait();
   if (u.item < 0) return;
   const int hk = blockIdx.y, lane = threadIdx.x & 31;
   const int32_t per = static_cast<int32_t>(p.tiles.per_tile.d), q0 = u.tile * per;
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const JoinParams p) {
 }
 
 template <typename T>
-void launch_join(const AttnArgs& a, Cut cut, const float* part_o, const float* part_ml, cudaStream_t s) {
+cudaError_t launch_join(const AttnArgs& a, Cut cut, const float* part_o, const float* part_ml, cudaStream_t s) {
   JoinParams p = {};
   p.chunk = cut.chunk;
   cut.chunk = 0;
@@ -102,7 +103,8 @@ void launch_join(const AttnArgs& a, Cut cut, const float* part_o, const float* p
   p.err = a.err;
   // a row takes a warp a microsecond, most of it latency: one or two rows to a warp
   const unsigned rows = cut.per_tile.d * p.group, parts = rows < 16 ? 1 : rows / 16;
-  k_attn_join<T><<<dim3(static_cast<unsigned>(a.n / cut.per_tile.d + a.items), a.kv_heads, parts), 256, 0, s>>>(p);
+  return launch_after(k_attn_join<T>, dim3(static_cast<unsigned>(a.n / cut.per_tile.d + a.items), a.kv_heads, parts), 256,
+                      0, s, p);
 }
 
 }  // namespace attn

@@ -291,6 +291,7 @@ __device__ __forceinline__ void gradients(const AttnArgs& a, const Cut& cut, boo
   float *a1 = sm, *a2 = a1 + kTile * LD, *b1 = a2 + kTile * LD, *b2 = b1 + kTile * LD, *sp = b2 + kTile * LD;
   const int group = a.heads / a.kv_heads, per_tile = kTile / group;
   find_unit<kThreads>(cut, ux, &unit, a.err);
+  grid_wait();  // for delta
   if (unit.item < 0) return;
   const Unit u = unit;
   const int hk = blockIdx.y, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -438,6 +439,7 @@ __device__ __forceinline__ void add_splits(const AttnArgs& a, Cut tiles, const f
   tiles.chunk = 0;
   find_unit<kThreads>(tiles, ux, &unit, a.err);
   const Unit u = unit;
+  grid_wait();
   if (u.item < 0) return;
   const int hk = blockIdx.y, group = kDQ ? a.heads / a.kv_heads : 1, per = static_cast<int>(tiles.per_tile.d);
   const Span own = kDQ ? u.q : u.k;
@@ -469,6 +471,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_bwd_sum(const AttnArgs a, con
 // delta[row, head] = sum of dO * O over the head, one warp each.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_attn_delta(const AttnArgs a) {
+  allow_next();
   const int64_t total = a.n * a.heads;
   const int lane = threadIdx.x & 31;
   for (int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5; w < total;
@@ -531,7 +534,7 @@ int64_t bwd_words(const AttnArgs& a, int sms, bool dq) {
 template <typename T, int DP>
 cudaError_t launch_bwd(const AttnArgs& a, float* scratch, int sms, cudaStream_t s) {
   const size_t bytes = (4 * kTile * (DP + 4) + kTile * (kTile + 4)) * sizeof(float);
-  const cudaError_t e = allow_smem(k_attn_bwd<T, DP>, bytes);
+  cudaError_t e = allow_smem(k_attn_bwd<T, DP>, bytes);
   if (e != cudaSuccess) return e;
   int64_t tiles[2], units[2];  // of dK and dV, of dQ
   Half half[2];
@@ -544,14 +547,22 @@ cudaError_t launch_bwd(const AttnArgs& a, float* scratch, int sms, cudaStream_t 
     half[x].cut = {a.q_off, a.k_off, static_cast<int32_t>(a.n), static_cast<int32_t>(a.m), a.items, chunk, divisor(per), !dq};
     half[x].part = dq ? scratch + bwd_words(a, sms, false) : scratch;
   }
-  k_attn_bwd<T, DP><<<dim3(static_cast<unsigned>(units[0] + units[1]), a.kv_heads), kThreads, bytes, s>>>(
-      a, half[0], half[1], static_cast<uint32_t>(units[0]), whole_pieces(a, true));
+  const dim3 grid(static_cast<unsigned>(units[0] + units[1]), a.kv_heads);
+  const uint32_t kunits = static_cast<uint32_t>(units[0]);
+  const bool vec = whole_pieces(a, true);
+  if (a.n > 0) {  // behind k_attn_delta
+    e = launch_after(k_attn_bwd<T, DP>, grid, kThreads, bytes, s, a, half[0], half[1], kunits, vec);
+    if (e != cudaSuccess) return e;
+  } else {
+    k_attn_bwd<T, DP><<<grid, kThreads, bytes, s>>>(a, half[0], half[1], kunits, vec);
+  }
   count_launches(1);
   for (int x = 0; x < 2; ++x)
     if (!half[x].cut.chunk) tiles[x] = 0;  // nothing to add up
   if (tiles[0] + tiles[1] > 0) {
-    k_attn_bwd_sum<T><<<dim3(static_cast<unsigned>(tiles[0] + tiles[1]), a.kv_heads, 8), kThreads, 0, s>>>(
-        a, half[0], half[1], static_cast<uint32_t>(tiles[0]));
+    e = launch_after(k_attn_bwd_sum<T>, dim3(static_cast<unsigned>(tiles[0] + tiles[1]), a.kv_heads, 8), kThreads, 0, s,
+                     a, half[0], half[1], static_cast<uint32_t>(tiles[0]));
+    if (e != cudaSuccess) return e;
     count_launches(1);
   }
   return cudaGetLastError();
@@ -570,9 +581,9 @@ cudaError_t launch_dim(const AttnArgs& a, bool backward, float* scratch, int chu
     if (e != cudaSuccess) return e;
     float* part_ml = chunk ? scratch + ((a.m - 1) / chunk + 1) * a.n * a.heads * a.dim : nullptr;
     k_attn<T, DP><<<qgrid, kThreads, bytes, s>>>(a, cut, whole_pieces(a, false), chunk ? scratch : nullptr, part_ml);
-    if (chunk) attn::launch_join<T>(a, cut, scratch, part_ml, s);
     count_launches(chunk ? 2 : 1);
-    return cudaGetLastError();
+    const cudaError_t launched = cudaGetLastError();
+    return chunk && launched == cudaSuccess ? attn::launch_join<T>(a, cut, scratch, part_ml, s) : launched;
   }
   const int64_t want = (a.n * a.heads + 7) / 8;
   if (a.n > 0) {

@@ -505,15 +505,13 @@ cudaError_t launch_tiles(const AttnArgs& a, const FwdParams& p, const FwdPlan& s
                          cudaStream_t st) {
   using L = FwdLayout<DP, kTiles>;
   auto kern = k_attn_fwd_tc<T, DP, kTiles>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L::kTotal));
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L::kTotal));
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(s.units), static_cast<unsigned>((a.kv_heads + s.heads - 1) / s.heads));
   kern<<<grid, L::kThreads, L::kTotal, st>>>(maps[0], maps[1], maps[2], p);
-  if (s.chunk) {
-    launch_join<T>(a, p.cut, p.part_o, p.part_ml, st);
-  }
   count_launches(s.chunk ? 2 : 1);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  return s.chunk && e == cudaSuccess ? launch_join<T>(a, p.cut, p.part_o, p.part_ml, st) : e;
 }
 
 template <typename T>

@@ -506,6 +506,7 @@ __global__ void __launch_bounds__(1024) k_ln_fold(const float* part, int parts, 
   __shared__ double s_run[32][33];
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, j = blockIdx.x * 32 + lane;
   double s = 0.0;
+  grid_wait();
   if (j < 2 * c)
 #pragma unroll 8
     for (int p = run; p < parts; p += 32) s += part[static_cast<int64_t>(p) * 2 * c + j];
@@ -624,7 +625,9 @@ cudaError_t launch_typed(const LayerNormArgs& b, int sms, cudaStream_t s) {
     launch_width<T, 16 / sizeof(T)>(a, backward, p.blocks, p.tpr, s);
   }
   if (backward && a.part) {
-    k_ln_fold<T><<<(2 * b.c + 31) / 32, 1024, 0, s>>>(a.part, parts, b.c, a.dgamma, a.dbeta);
+    const cudaError_t e = launch_after(k_ln_fold<T>, dim3((2 * b.c + 31) / 32), 1024, 0, s, a.part, parts, b.c,
+                                       a.dgamma, a.dbeta);
+    if (e != cudaSuccess) return e;
     ++launches;
   }
   count_launches(launches);
