@@ -12,12 +12,13 @@ namespace attn {
 
 // Keys of a run, or 0 for no split: when tiles of `per` queries leave half of the
 // machine's `slots` for blocks idle and there are `least` keys, runs of about
-// (keys x tiles) / slots, at least 256 keys.  Items of one run are written as they
-// are; the join passes over them.
-inline int split_keys(const AttnArgs& a, int per, int64_t slots, int64_t least) {
+// (keys x tiles) / slots, at least 256 keys; within: as short as keep all blocks, the
+// items' last runs among them, within the slots.  Items of one run are written as
+// they are; the join passes over them.
+inline int split_keys(const AttnArgs& a, int per, int64_t slots, int64_t least, bool within) {
   const int64_t tiles = a.n / per + a.items;  // upper bound
   if (2 * tiles * a.kv_heads > slots || a.m < least) return 0;
-  int64_t chunk = a.m * (a.n / per + 1) * a.kv_heads / slots;
+  int64_t chunk = a.m * (a.n / per + 1) / (slots / a.kv_heads - (within ? tiles : 0));
   chunk = (chunk < 256 ? 256 : chunk + 127) / 128 * 128;
   return a.m <= chunk ? 0 : static_cast<int>(chunk);  // no item is longer than one run
 }

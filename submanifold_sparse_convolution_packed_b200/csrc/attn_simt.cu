@@ -500,12 +500,13 @@ bool whole_pieces(const AttnArgs& a, bool backward) {
          (!backward || ok(a.dout, a.dout_stride));
 }
 
-// Runs of keys (attn_join.cuh), for three blocks to each of an SM's two places (64
-// queries, 8 heads of 64 over 2: 39 us split, 35 and 59 us whole over 300 and 600
-// keys); the join moves four channels at a time.
+// Runs of keys (attn_join.cuh), for three blocks and more to each of an SM's two
+// places (1500 and 903 rows over 1374 and 700 keys, 4 heads of 64: 121 us, three at
+// most: 140 us; 64 queries, 8 heads of 64 over 2: 39 us split, 35 and 59 us whole over
+// 300 and 600 keys); the join moves four channels at a time.
 int split_of(const AttnArgs& a, int sms) {
   const bool fits = a.dim % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out_w) & 15u) == 0;
-  return fits ? attn::split_keys(a, kTile / (a.heads / a.kv_heads), 6ll * sms, 384) : 0;
+  return fits ? attn::split_keys(a, kTile / (a.heads / a.kv_heads), 6ll * sms, 384, false) : 0;
 }
 
 // Backward: rows of a split of what passes (keys for dQ, queries for dK and dV),

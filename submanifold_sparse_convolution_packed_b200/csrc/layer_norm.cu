@@ -15,7 +15,7 @@
 // beta in registers.  16-bit rows with SiLU come near the special-function unit's
 // bound as well (an exponential and half a reciprocal for each value).
 // Measured: 1,300,007 x 64 fp16 with SiLU 77 us (4.5 TB/s), 410 x 16 fp32 1.7 us;
-// gradients of 133,450 x 128 bf16 with SiLU 34 us (3.1 TB/s: the sums over the rows
+// gradients of 133,450 x 128 bf16 with SiLU 33 us (3.1 TB/s: the sums over the rows
 // take the registers that more loads in flight would need), of 20,011 x 512 fp32
 // 23 us (5.3 TB/s).  The backward pass keeps the channel sums of its rows in
 // registers (fp32, a few hundred rows each), adds them up per block in a fixed
