@@ -483,13 +483,14 @@ FwdPlan fwd_plan(const AttnArgs& a, int sms) {
   const int per = s.tiles * qpt;
   const int64_t tiles = a.n / per + a.items, slots = static_cast<int64_t>(sms) * blocks;
   s.units = tiles;
-  // Short items: several heads to a CTA, as long as four waves of CTAs remain,
+  // Short items: several heads to a CTA, as long as three waves of CTAs remain,
   // since finding the block's share and the first loads' way are a third of a
-  // CTA's life there.  (Two-tile CTAs read each other's halves at the end, and
+  // CTA's life there.  (Two, three, four, eight waves: 512 items of 1 to 512 rows, 8
+  // heads of 64: 275, 259, 260, 274 us; 1000 of 1 to 216, 8 of 32: 167, 166, 175, 189.)  (Two-tile CTAs read each other's halves at the end, and
   // their items are long.)
   s.heads = 1;
   if (s.tiles == 1) {
-    const int64_t most = tiles * a.kv_heads / (4 * slots);
+    const int64_t most = tiles * a.kv_heads / (3 * slots);
     s.heads = static_cast<int>(most < 1 ? 1 : most < a.kv_heads ? most : a.kv_heads);
   }
   // The join and its scratch cost 8 us of the device: one query of 8 heads of 64
