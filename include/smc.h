@@ -447,9 +447,12 @@ SMC_API int smc_attention(const void* q, const int64_t q_stride[2], const void* 
  * queries and keys that nothing pairs with are zero; rows outside every item
  * are left as they were.  No atomics: the same call gives the same bits.
  * bf16 / fp16 inputs round P and dS to the input type for their products
- * (fp16 under a power of two that keeps them in range).  Scratch (fp32 [n, heads]
- * twice, and partial sums where the queries are split between blocks) comes
- * from the library's stream-ordered pool.
+ * (fp16: P under 2^14, dS under a power of two for each row of dq and dk, from
+ * what bounds that row's dS: the query's own dout and the values of its item and
+ * key/value head, or the key's value and the dout of the queries that one block
+ * passes.  Other items and heads do not enter).  Scratch (fp32 [n, heads] twice, in
+ * fp16 four times and [m, kv_heads] once, and partial sums where the queries are
+ * split between blocks) comes from the library's stream-ordered pool.
  * Asynchronous on `stream`.  Errors as smc_attention.
  */
 SMC_API int smc_attention_backward(const void* dout, const int64_t dout_stride[2], const void* q,

@@ -341,9 +341,9 @@ int smc_attention_backward(const void* dout, const int64_t dout_stride[2], const
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  // scratch: delta and the scaled lse, [n, heads] each, two words, partial sums
-  const bool tc = smc::attn_bwd_tc_supported(a);
-  const int64_t count = n * heads, part = (2 * count + 2 + 63) / 64 * 64;
+  // scratch: delta and the scaled lse, [n, heads] each, the bounds of fp16, partial sums
+  const bool tc = smc::attn_bwd_tc_supported(a), bounds = tc && dtype == SMC_F16;
+  const int64_t count = n * heads, part = (2 * count + (bounds ? 2 * count + m * kv_heads : 0) + 63) / 64 * 64;
   const int64_t floats = part + (tc ? smc::attn_bwd_tc_scratch(a, dev.sms) : smc::attn_simt_bwd_scratch(a, dev.sms));
   void* scratch = nullptr;
   if (n > 0 && smc::scratch_alloc(&scratch, static_cast<size_t>(floats) * sizeof(float), dev.id, s) != cudaSuccess) {
@@ -351,7 +351,8 @@ int smc_attention_backward(const void* dout, const int64_t dout_stride[2], const
     return SMC_E_OOM;
   }
   a.delta = static_cast<float*>(scratch);
-  const smc::BwdScratch x = {a.delta + count, reinterpret_cast<uint32_t*>(a.delta + 2 * count), a.delta + part};
+  const smc::BwdScratch x = {a.delta + count, bounds ? reinterpret_cast<float2*>(a.delta + 2 * count) : nullptr,
+                             bounds ? a.delta + 4 * count : nullptr, a.delta + part};
   const cudaError_t e = tc ? smc::launch_attn_bwd_tc(a, x, dev.sms, s) : smc::launch_attn_simt(a, true, x.part, dev.sms, s);
   if (scratch) cudaFreeAsync(scratch, s);
   return outcome(e);

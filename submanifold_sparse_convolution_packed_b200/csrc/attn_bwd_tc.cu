@@ -19,10 +19,14 @@
 //              that takes over its TMEM buffer (two or three steps ahead), as
 //              one batch: this warp's waits are what there is to save;
 //   warps 0-15 P and dS, one thread per row and 16 of the step's 64 columns.
-// fp16: P carries a factor 2^14 and dS a power of two taken from the largest
-// norms of dO and V rows (|dP|, |delta| <= |dO| |V|), undone on the fp32
-// accumulators, so that the P of a long context do not fall below fp16's
-// range and dS cannot leave it.
+// fp16: P carries a factor 2^14 and dS a power of two, undone on the fp32
+// accumulators, so that the P of a long context do not fall below fp16's range
+// and dS cannot leave it.  The power of two is each accumulator row's own, from
+// |dS| <= |dO| |V| + |delta|: for dQ the query's |dO| and delta and the largest |V|
+// of the keys it passes, for dK the key's |V| and the largest |dO| and delta of the
+// queries that pass.  So neither another item, nor another head, nor (dQ) another
+// query sets the precision of a row; a key's dK is held to 2^-39 of what the largest
+// dO among its block's queries could make it.
 //
 // What bounds it: the chain of a step (products, scores of the step that takes
 // its buffer, TMEM to registers, exponentials, back to TMEM); the tensor cores work
@@ -50,7 +54,8 @@ struct BwdParams {
   float scale;
   bool causal;
   const float *lse, *delta;  // as k_attn_delta_tc leaves them: -lse log2e (-inf for a row that saw no key), -delta
-  const uint32_t* norms;  // fp16: bits of max |dO|^2, max |V|^2
+  const float2* qbound;  // fp16: (|dO|^2, |delta|), [heads, n]
+  const float* vbound;   // fp16: |V|^2, [kv_heads, m]
   const void *a1, *a2;    // the resident operands: Q, dO or K, V
   int64_t a1s[2], a2s[2];
   void *d1, *d2;          // dQ, -- or dK, dV
@@ -78,10 +83,8 @@ template <int DP, bool kDQ> struct BwdLayout {
   static constexpr uint32_t kMisc = kBar + 8 * (2 * kSlots + 2 * kBufs + 3), kTotal = kMisc + 32 + 1024;
 };
 
-// The power of two that dS carries in fp16.
-__device__ __forceinline__ float ds_factor(const uint32_t* norms) {
-  if (!norms) return 1.f;
-  const float bound = 2.f * sqrtf(__uint_as_float(norms[0])) * sqrtf(__uint_as_float(norms[1]));
+// The power of two that a row's dS carry in fp16, |dS| <= bound.
+__device__ __forceinline__ float ds_factor(float bound) {
   if (!(bound > 0.f) || !(bound < 1e37f)) return 1.f;
   int e = 15 - (ilogbf(bound) + 1);  // |dS| <= bound, so |dS| 2^e <= 2^15
   e = e < -60 ? -60 : (e > 60 ? 60 : e);
@@ -103,6 +106,7 @@ __device__ __forceinline__ void gradients(const BwdMaps& maps, const BwdParams& 
   constexpr float kShift = kBf16 || kDQ ? 0.f : 14.f;  // P carries 2^kShift
   extern __shared__ uint8_t smem_raw[];
   __shared__ Unit s_unit;
+  __shared__ uint32_t s_bound[2];  // fp16: bits of the largest passing |V|^2, or |dO|^2 and |delta|
   const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - raw);
   volatile uint32_t* s_misc = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);  // [0] tmem
@@ -151,6 +155,7 @@ __device__ __forceinline__ void gradients(const BwdMaps& maps, const BwdParams& 
     }
     mbar_init(bar_o, 1);
     mbar_init(bar_tail, 1);
+    s_bound[0] = s_bound[1] = 0;
     fence_mbarrier_init();
   }
   const int rows_step = kDQ ? kStep : p.qps * p.group;  // rows of a step that the TMA writes
@@ -305,9 +310,7 @@ __device__ __forceinline__ void gradients(const BwdMaps& maps, const BwdParams& 
     // columns 16 w .. 16 w + 15 of every step; par, half: of the results
     const int w = warp >> 2, r = (warp & 3) * 32 + lane, par = w & 1, half = w >> 1;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const float factor = ds_factor(p.norms);
     const float2 c2 = make_float2(p.scale * kLog2e, p.scale * kLog2e);
-    const float2 f2 = make_float2(factor * exp2f(-kShift), factor * exp2f(-kShift));
     const int32_t qi = kDQ ? r / p.group : 0;
     const bool row = kDQ ? qi < count : r < count;
     float l = -INFINITY, e = 0.f;  // dQ: of this thread's query; exp2(s - inf) = 0
@@ -323,6 +326,10 @@ __device__ __forceinline__ void gradients(const BwdMaps& maps, const BwdParams& 
       const int64_t first = static_cast<int64_t>(r0) + r + u.q.count - u.k.count;  // the first query that sees this key
       lim = first < 0 ? 0 : static_cast<int32_t>(first < u.q.count ? first : u.q.count) * p.group;
     }
+    float factor = 1.f, own = 0.f;  // fp16: of this thread's row
+    if (!kBf16 && row)
+      own = kDQ ? p.qbound[static_cast<int64_t>(hk * p.group + r % p.group) * p.cut.n + u.q.begin + r0 + qi].x
+                : p.vbound[static_cast<int64_t>(hk) * p.cut.m + u.k.begin + r0 + r];
     if (L::kTmemA) {  // this thread's row of the resident operands: 32 words for each of the DP / 32 groups
       if (w < DP / 32) {
         constexpr int kPer = DP / 64;  // groups to an operand
@@ -347,6 +354,35 @@ __device__ __forceinline__ void gradients(const BwdMaps& maps, const BwdParams& 
       if (lane == 0) mbar_arrive(bar_a);
       __syncwarp();
     }
+    if (!kBf16) {  // while the first scores are on their way
+      float top = 0.f, top2 = 0.f;  // a NaN is passed over: its row's gradients are NaN under any factor
+      if (kDQ) {
+        const float* v2 = p.vbound + static_cast<int64_t>(hk) * p.cut.m + u.k.begin;
+#pragma unroll 4
+        for (int32_t i = tid; i < b_hi; i += 512) top = fmaxf(top, v2[i]);
+      } else {
+        for (int g = 0; g < p.group; ++g) {
+          const float2* d2 = p.qbound + static_cast<int64_t>(hk * p.group + g) * p.cut.n + u.q.begin;
+#pragma unroll 4
+          for (int32_t i = b_lo + tid; i < b_hi; i += 512) {
+            const float2 x = d2[i];
+            top = fmaxf(top, x.x);
+            top2 = fmaxf(top2, x.y);
+          }
+        }
+      }
+      // not negative: ordered as their bits
+      const uint32_t t1 = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+      const uint32_t t2 = __reduce_max_sync(0xffffffffu, __float_as_uint(top2));
+      if (lane == 0) {
+        atomicMax(&s_bound[0], t1);
+        atomicMax(&s_bound[1], t2);
+      }
+      asm volatile("bar.sync 1, 512;" ::: "memory");  // these 16 warps
+      if (row)
+        factor = ds_factor(sqrtf(own) * sqrtf(__uint_as_float(s_bound[0])) + (kDQ ? fabsf(e) : __uint_as_float(s_bound[1])));
+    }
+    const float2 f2 = make_float2(factor * exp2f(-kShift), factor * exp2f(-kShift));
     int slot = 0, b = 0;
     uint32_t fparity = 0, sparity = 0;
     bool ok = true, ready = false;  // ready: this step's scores were there before the last step's were worked on
@@ -524,12 +560,12 @@ __global__ void __launch_bounds__(256) k_attn_bwd_join(const BwdParams p, const 
 }
 
 // delta[row, head] = -sum of dO * O, and lse2 = -lse log2e, or -infinity for a
-// row that saw no key, whose P = exp2(S + lse2) is then 0; fp16: also the largest
-// squared norms of the rows of dO and of V that belong to items (as bits: they are
-// not negative; the order of the atomic maxima changes nothing).  LPR lanes hold a
-// row of up to 8 LPR channels.  Bound by HBM: one read of O and dO (and V).
+// row that saw no key, whose P = exp2(S + lse2) is then 0; fp16: also what bounds dS,
+// (|dO|^2, |delta|) and |V|^2 of the rows that belong to items, by head, so that a
+// block reads its rows' as runs.  LPR lanes hold a row of up to 8 LPR channels.  Bound
+// by HBM: one read of O and dO (and V).
 template <typename T, int LPR>
-__global__ void __launch_bounds__(256) k_attn_delta_tc(const AttnArgs a, float* lse2, uint32_t* norms) {
+__global__ void __launch_bounds__(256) k_attn_delta_tc(const AttnArgs a, float* lse2, float2* qbound, float* vbound) {
   using C = Chunk<T, 8>;
   allow_next();
   const int l = threadIdx.x % LPR;
@@ -543,7 +579,6 @@ __global__ void __launch_bounds__(256) k_attn_delta_tc(const AttnArgs a, float* 
   };
   int64_t lo, hi;
   bounds(a.q_off, a.items, a.n, lo, hi);
-  float top = 0.f, vtop = 0.f;
   const T* O = static_cast<const T*>(a.out);
   const T* D = static_cast<const T*>(a.dout);
   for (int64_t b = lo * a.heads + first; b < hi * a.heads; b += stride) {
@@ -561,33 +596,29 @@ __global__ void __launch_bounds__(256) k_attn_delta_tc(const AttnArgs a, float* 
       }
     }
     s = group_sum<LPR>(s);
+    if (qbound) q = group_sum<LPR>(q);
     if (there && l == 0) {
       a.delta[i] = -s;
       lse2[i] = a.lse[i] == -INFINITY ? -INFINITY : a.lse[i] * -kLog2e;
+      if (qbound) qbound[(i - row * a.heads) * a.n + row] = make_float2(q, fabsf(s));
     }
-    if (norms) top = fmaxf(top, group_sum<LPR>(q));
   }
-  if (!norms) return;
+  if (!qbound) return;
   bounds(a.k_off, a.items, a.m, lo, hi);
   const T* V = static_cast<const T*>(a.v);
   for (int64_t b = lo * a.kv_heads + first; b < hi * a.kv_heads; b += stride) {
     const int64_t i = b + threadIdx.x / LPR, row = i / a.kv_heads;
+    const bool there = i < hi * a.kv_heads;
     float q = 0.f;
-    if (i < hi * a.kv_heads && in) {
+    if (there && in) {
       float v[8];
       unpack(*reinterpret_cast<const C*>(V + row * a.v_stride[0] + (i - row * a.kv_heads) * a.v_stride[1] + 8 * l), v);
 #pragma unroll
       for (int x = 0; x < 8; ++x) q += v[x] * v[x];
     }
-    vtop = fmaxf(vtop, group_sum<LPR>(q));
+    q = group_sum<LPR>(q);
+    if (there && l == 0) vbound[(i - row * a.kv_heads) * a.m + row] = q;
   }
-  __shared__ uint32_t s_top[2];
-  if (threadIdx.x < 2) s_top[threadIdx.x] = 0;
-  __syncthreads();
-  atomicMax(&s_top[0], __float_as_uint(top));
-  atomicMax(&s_top[1], __float_as_uint(vtop));
-  __syncthreads();
-  if (threadIdx.x < 2) atomicMax(norms + threadIdx.x, s_top[threadIdx.x]);
 }
 
 // Where the tiles of keys do not fill the machine (shared heads: the heads of a
@@ -617,17 +648,11 @@ BwdPlan bwd_plan(const AttnArgs& a, int sms) {
 
 template <typename T, int DP>
 cudaError_t launch_typed(const AttnArgs& a, BwdParams p, const BwdMaps* maps, int sms, const BwdScratch& x, cudaStream_t st) {
-  float* lse2 = x.lse2;
-  uint32_t* norms = a.dtype == kF16 ? x.norms : nullptr;
   const BwdPlan plan = bwd_plan(a, sms);
   const int64_t rows = a.n * a.heads, per = DP == 64 ? 32 : 16;
   int64_t blocks = (rows + per - 1) / per;
   blocks = blocks < 8ll * sms ? (blocks < 1 ? 1 : blocks) : 8ll * sms;
-  if (norms) {
-    const cudaError_t e = cudaMemsetAsync(norms, 0, 2 * sizeof(uint32_t), st);
-    if (e != cudaSuccess) return e;
-  }
-  k_attn_delta_tc<T, DP / 8><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, lse2, norms);
+  k_attn_delta_tc<T, DP / 8><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, x.lse2, x.qbound, x.vbound);
   constexpr uint32_t kSmemQ = BwdLayout<DP, true>::kTotal, kSmemK = BwdLayout<DP, false>::kTotal;
   constexpr int kSmem = static_cast<int>(kSmemQ > kSmemK ? kSmemQ : kSmemK);
   auto kern = k_attn_bwd_tc<T, DP>;
@@ -715,7 +740,8 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs& a, const BwdScratch& x, int sms, 
   p.causal = a.causal;
   p.lse = x.lse2;
   p.delta = a.delta;
-  p.norms = a.dtype == kF16 ? x.norms : nullptr;
+  p.qbound = x.qbound;
+  p.vbound = x.vbound;
   p.err = a.err;
   // never below 100 ms, so that no CTA leaves with its loads in flight
   p.wait_ns = scan_wait_limit_ns() > 100000000ull ? scan_wait_limit_ns() : 100000000ull;

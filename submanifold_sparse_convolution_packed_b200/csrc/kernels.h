@@ -230,9 +230,10 @@ cudaError_t launch_attn_tc(const AttnArgs& a, void* scratch, int sms, cudaStream
 // Backward pass (attn_bwd_tc.cu): the same shapes, gradients and dout aligned
 // too.
 struct BwdScratch {
-  float* lse2;      // [n, heads]
-  uint32_t* norms;  // two words
-  float* part;      // attn_bwd_tc_scratch floats, 16-byte aligned
+  float* lse2;     // [n, heads]
+  float2* qbound;  // fp16: [heads, n], else null
+  float* vbound;   // fp16: [kv_heads, m], else null
+  float* part;     // attn_bwd_tc_scratch floats, 16-byte aligned
 };
 bool attn_bwd_tc_supported(const AttnArgs& a);
 int64_t attn_bwd_tc_scratch(const AttnArgs& a, int sms);

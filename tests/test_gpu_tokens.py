@@ -582,6 +582,84 @@ def test_layer_norm_far_rows():
     assert torch.equal(y[-1000:], smc.layer_norm(tail))
 
 
+# fp16 gradients of parts of a call whose dout differ by up to 10^6: per item, per
+# key/value head, per query
+def _scaled_case(h, hk, d, rows, causal, seed):
+    g = gen(seed)
+    o = offsets_of(rows)
+    n = sum(rows)
+    q, dout = normal(g, n, h, d, dtype=F16), normal(g, n, h, d)
+    k, v = normal(g, n, hk, d, dtype=F16), normal(g, n, hk, d, dtype=F16)
+    lse = torch.empty(n, h, device="cuda")
+    return q, k, v, dout, smc.attention(q, k, v, o, causal=causal, lse=lse), lse, o
+
+
+def _within(got, ref, what):
+    """One rounding of dS or P to fp16 under each sum and one of the result: 2 u
+    in the norm (the roundings of a sum's terms are independent of each other), and
+    half of fp16's smallest step for each element."""
+    fits = ref.abs() < 65_000.0  # what leaves fp16's range is infinite
+    got, ref = got.double()[fits], ref[fits]
+    err, size = float((got - ref).norm()), float(ref.norm())
+    assert err <= 2 * u_of(F16) * size + 2.0 ** -25 * math.sqrt(ref.numel()), (what, err / size)
+
+
+@pytest.mark.parametrize("h, hk, d, rows, causal", [
+    (2, 2, 64, [1000, 900], False), (4, 1, 128, [700, 600], True), (2, 2, 64, [40, 30], False),
+    (8, 2, 128, [3000, 1000], False), (3, 1, 40, [500, 400], True)])
+@pytest.mark.parametrize("small", [1e4, 1.0, 1e-2])
+def test_fp16_gradients_of_items_on_their_own_scale(h, hk, d, rows, causal, small):
+    q, k, v, dout, out, lse, o = _scaled_case(h, hk, d, rows, causal, 400 + d)
+    a = rows[0]
+    dout[:a] *= 1e4
+    dout[a:] *= small
+    dout = dout.clamp(-6e4, 6e4).to(F16)
+    got = smc.attention_backward(dout, q, k, v, out, lse, o, causal=causal)
+    r = attention_ref(q, k, v, o, o, d ** -0.5, causal, dout, out, lse)
+    for x, y in zip(("dq", "dk", "dv"), got):
+        _within(y[:a], r[x][:a], x + " of the first item")
+        _within(y[a:], r[x][a:], x + " of the second item")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp16_gradients_of_heads_and_queries_on_their_own_scale(d):
+    q, k, v, dout, out, lse, o = _scaled_case(4, 2, d, [1000], False, 410 + d)
+    by_head = dout * torch.tensor([1e4, 1e4, 1e-2, 1e-2], device="cuda")[:, None]
+    by_head = by_head.clamp(-6e4, 6e4).to(F16)
+    got = smc.attention_backward(by_head, q, k, v, out, lse, o)
+    r = attention_ref(q, k, v, o, o, d ** -0.5, False, by_head, out, lse)
+    for x, y in zip(("dq", "dk", "dv"), got):
+        per = y.shape[1] // 2
+        _within(y[:, :per], r[x][:, :per], x + " of the first head")
+        _within(y[:, per:], r[x][:, per:], x + " of the second head")
+    # by query: dq is each query's own (dk and dv are sums over the queries)
+    by_row = dout.clone()
+    by_row[::2] *= 1e4
+    by_row[1::2] *= 1e-2
+    by_row = by_row.clamp(-6e4, 6e4).to(F16)
+    got = smc.attention_backward(by_row, q, k, v, out, lse, o)
+    r = attention_ref(q, k, v, o, o, d ** -0.5, False, by_row, out, lse)
+    _within(got[0][::2], r["dq"][::2], "dq of large rows")
+    _within(got[0][1::2], r["dq"][1::2], "dq of small rows")
+    _within(got[1], r["dk"], "dk")
+    _within(got[2], r["dv"], "dv")
+
+
+def test_fp16_gradients_with_a_value_row_far_larger():
+    """|V| of one item does not reach the other's scale either."""
+    q, k, v, dout, _, _, o = _scaled_case(2, 2, 64, [600, 500], False, 420)
+    v[:600] *= 5e3
+    v[600:] *= 1e-2
+    dout = dout.to(F16)
+    lse = torch.empty(1100, 2, device="cuda")
+    out = smc.attention(q, k, v, o, lse=lse)
+    got = smc.attention_backward(dout, q, k, v, out, lse, o)
+    r = attention_ref(q, k, v, o, o, 64 ** -0.5, False, dout, out, lse)
+    for x, y in zip(("dq", "dk", "dv"), got):
+        _within(y[:600], r[x][:600], x + " of the first item")
+        _within(y[600:], r[x][600:], x + " of the second item")
+
+
 # ------------------------------------------------ streams, graphs, failures
 def _chain(q, k, v, dout, o, pos, freqs, gamma, beta, stream=None):
     n, h, d = q.shape
