@@ -416,7 +416,9 @@ SMC_API int smc_rotary(const void* x, const int64_t x_stride[2], int64_t n, int3
  *              query that sees no key gets zeros and lse = -infinity.
  * lse        : device fp32 [n, heads] or NULL.
  * Scores, softmax and sums are fp32; bf16 / fp16 inputs round the (unnormalised)
- * probabilities to the input type for the product with v.  Keys outside an
+ * probabilities to the input type for the product with v (fp16: under 2^7, so that
+ * one is off by at most 2^-32 of its row's largest where it lies below fp16's
+ * normal range).  Keys outside an
  * item never reach its rows, whatever they hold.  A key that only the causal
  * mask hides from a query must be finite, as in any product by zero.
  * Offsets that descend or leave [0, n] / [0, m] are cut to the buffers and

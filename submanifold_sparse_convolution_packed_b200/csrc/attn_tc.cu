@@ -19,8 +19,10 @@
 // the others keep the special-function unit busy (up to 64 channels an SM runs
 // four chains: two tiles with two halves, or four one-tile CTAs).
 // An accumulator is rescaled in TMEM only when a row's maximum has grown by
-// more than 2^8 (P stays below 256, far inside fp16's range); the sums use the
-// unrounded P.  Keys behind the item's end are masked, and V rows there are
+// more than 2^8; the sums use the unrounded P.  In fp16 P carries 2^7 besides: it
+// stays below 2^15, and a key counts down to 2^-32 of its row's largest (without, down
+// to 2^-25: 40,000 equal keys 17.5 below one other were lost, 1e-3 of the output).  A
+// P below 2^-21 of the largest is rounded in steps of 2^-31 of it.  Keys behind the item's end are masked, and V rows there are
 // zeroed in shared memory, since P = 0 does not undo a NaN.
 // With few queries over many keys the keys are split between CTAs; each writes
 // its unnormalised fp32 O, maximum and sum, and k_attn_join adds them up in
@@ -85,6 +87,7 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
   constexpr int kSlots = L::kSlots, kPanels = DP / 64, kHalves = L::kHalves, kKeys = L::kKeys, kCols = kKeys / kHalves;
   constexpr int kMmaWarp = 4 * L::kGroups, kTmaWarp = kMmaWarp + kTiles;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr float kShift = kBf16 ? 0.f : 7.f;  // P carries 2^kShift: it cancels in O / sum and is part of top
   extern __shared__ uint8_t smem_raw[];
   __shared__ Unit s_unit;
   const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
@@ -311,7 +314,8 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
     uint32_t ps = 0;
     for (int head = 0; head < nheads && ok; ++head) {
       const int hk = blockIdx.y + head * gridDim.y;
-      float top = -INFINITY, sum = 0.f;  // top: the rounded product with c the sums refer to
+      // top: the exponent that the sums refer to, a row's rounded largest score times c, less kShift
+      float top = -INFINITY, sum = 0.f;
       for (int j = 0; j < steps[t]; ++j) {
         ok = mbar_wait_warp(bar_s + 8 * g, ps, p.err, p.wait_ns);
         ps ^= 1;
@@ -345,12 +349,12 @@ __global__ void __launch_bounds__(FwdLayout<DP, kTiles>::kThreads, FwdLayout<DP,
             }
           }
           const float m = __fmul_rn(fmaxf(max3(m0, m1, m2), m3), p.c);
-          const bool grown = m > top + 8.f || (top == -INFINITY && m > -INFINITY);
+          const bool grown = m > top + (8.f + kShift) || (top == -INFINITY && m > -INFINITY);
           if (__any_sync(0xffffffffu, grown)) {
-            const float keep = grown ? exp2_fast(top - m) : 1.f;
+            const float next = m - kShift, keep = grown ? exp2_fast(top - next) : 1.f;
             if (grown) {
               sum *= keep;
-              top = m;
+              top = next;
             }
             if (j > 0) {  // the products so far are complete: these scores came after them
 #pragma unroll 1

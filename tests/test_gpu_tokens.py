@@ -660,6 +660,26 @@ def test_fp16_gradients_with_a_value_row_far_larger():
         _within(y[600:], r[x][600:], x + " of the second item")
 
 
+# One key far above tens of thousands of equal ones, whose probabilities lie at the
+# low end of fp16: P carries 2^7, so each is off by at most half of 2^-24 of 2^-7
+# of the row's largest, 2^-32, and the sum over the keys by that many times as much.
+@pytest.mark.parametrize("at", [0, 20_000, 39_999])
+@pytest.mark.parametrize("above", [17.5, 17.25, 12.0])
+@pytest.mark.parametrize("queries, h, hk, d", [(1, 4, 1, 128), (300, 2, 2, 64), (1300, 2, 1, 128), (2500, 1, 1, 64)])
+def test_fp16_attention_keeps_small_probabilities(queries, h, hk, d, above, at):
+    keys = 40_000
+    q = torch.zeros(queries, h, d, dtype=F16, device="cuda")
+    q[..., 0] = 4.0
+    k, v = torch.zeros(keys, hk, d, dtype=F16, device="cuda"), torch.ones(keys, hk, d, dtype=F16, device="cuda")
+    k[at, :, 0], v[at] = above / 4, 0.0  # exact in fp16
+    lse = torch.empty(queries, h, device="cuda")
+    out = smc.attention(q, k, v, offsets_of([queries]), offsets_of([keys]), scale=1.0, lse=lse)
+    low = (keys - 1) * math.exp(-above)
+    ref = low / (1 + low)
+    assert float((out.double() - ref).abs().max()) <= (u_of(F16) + 256 * E) * ref + keys * 2.0 ** -32
+    assert float((lse.double() - (above + math.log1p(low))).abs().max()) <= 64 * E * above
+
+
 # ------------------------------------------------ streams, graphs, failures
 def _chain(q, k, v, dout, o, pos, freqs, gamma, beta, stream=None):
     n, h, d = q.shape
