@@ -444,8 +444,10 @@ SMC_API int smc_attention(const void* q, const int64_t q_stride[2], const void* 
  * The gradients of shared key/value heads are summed over their query heads.
  * out (dense) and lse as smc_attention wrote them; the other arguments as
  * there.  dout: device [n, heads, dim] with dout_stride.  dq: device [n, heads, dim], dk and dv:
- * device [m, kv_heads, dim], each with its strides (views of one packed
- * buffer may interleave); they must not overlap the inputs or each other.  Gradients of
+ * device [m, kv_heads, dim], each with its strides; they must not overlap the
+ * inputs or each other.  Views of one packed buffer may interleave where a common
+ * distance shows that they never meet: packed rows, packed heads, or heads in turn
+ * (other interleaved strides are refused as SMC_E_ALIAS).  Gradients of
  * queries and keys that nothing pairs with are zero; rows outside every item
  * are left as they were.  No atomics: the same call gives the same bits.
  * bf16 / fp16 inputs round P and dS to the input type for their products

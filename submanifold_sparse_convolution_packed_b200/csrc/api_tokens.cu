@@ -6,6 +6,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <numeric>
 
 #include "smc.h"
 #include "common.cuh"
@@ -39,6 +40,40 @@ bool take_stride(const int64_t in[2], int64_t rows, int64_t heads, int64_t dim, 
 bool distinct(const int64_t st[2], int64_t rows, int64_t heads, int64_t dim) {
   return (st[1] >= dim && st[0] >= (heads - 1) * st[1] + dim) ||
          (st[0] >= dim && st[1] >= (rows - 1) * st[0] + dim);
+}
+
+// A strided output as its buffer sees it: [rows, heads, dim] at `p`.
+struct View {
+  const void* p;
+  int64_t rows, heads, dim;
+  const int64_t* st;
+};
+
+// Whether two outputs can be told apart: their bytes as a whole, or their places
+// modulo a distance that both repeat at, be it of rows (heads of packed rows), of
+// heads (rows of packed heads) or of both (interleaved heads).  Modulo m, each lies
+// in one interval that starts at its address; intervals apart on the circle of m
+// never meet.  An axis with one entry repeats at any distance.
+bool apart(const View& a, const View& b, size_t esz) {
+  if (a.rows < 1 || b.rows < 1) return true;
+  if (!overlap(bytes_of(a.p, a.rows, a.heads, a.dim, a.st, esz), bytes_of(b.p, b.rows, b.heads, b.dim, b.st, esz)))
+    return true;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  const bool b_first = pb < pa;
+  const uintptr_t bytes = b_first ? pa - pb : pb - pa;
+  if (bytes % esz) return false;
+  const View &lo = b_first ? b : a, &hi = b_first ? a : b;
+  const int64_t gap = static_cast<int64_t>(bytes / esz);
+  auto row = [](const View& v) { return v.rows > 1 ? v.st[0] : 0; };
+  auto head = [](const View& v) { return v.heads > 1 ? v.st[1] : 0; };
+  auto separate = [&](int64_t m, int64_t lo_size, int64_t hi_size) {
+    const int64_t at = m ? gap % m : 0;  // of hi's interval, lo's starts at 0
+    return m && at >= lo_size && at + hi_size <= m;
+  };
+  const int64_t rows = std::gcd(row(lo), row(hi)), heads = std::gcd(head(lo), head(hi));
+  return separate(rows, (lo.heads - 1) * head(lo) + lo.dim, (hi.heads - 1) * head(hi) + hi.dim) ||
+         separate(heads, (lo.rows - 1) * row(lo) + lo.dim, (hi.rows - 1) * row(hi) + hi.dim) ||
+         separate(std::gcd(rows, heads), lo.dim, hi.dim);
 }
 
 bool known_dtype(int32_t d) { return d == SMC_F32 || d == SMC_BF16 || d == SMC_F16; }
@@ -317,18 +352,12 @@ int smc_attention_backward(const void* dout, const int64_t dout_stride[2], const
   for (const Bytes& o : outs)
     for (const Bytes& i : ins)
       if (overlap(o, i)) return SMC_E_ALIAS;
-  // The three gradients may interleave (views of one packed buffer), but share
-  // no place: checked for their first heads, and for dense ones as a whole.
-  auto dense_rows = [&](const int64_t st[2], int64_t h) { return st[1] == dim && st[0] == h * dim; };
-  const uintptr_t head_bytes = static_cast<uintptr_t>(dim) * esz;
-  const bool whole[3] = {dense_rows(a.dq_stride, heads), dense_rows(a.dk_stride, kv_heads),
-                         dense_rows(a.dv_stride, kv_heads)};
+  // the three gradients may interleave (views of one packed buffer), but share no place
+  const View grads[3] = {{dq, n, heads, dim, a.dq_stride}, {dk, m, kv_heads, dim, a.dk_stride},
+                         {dv, m, kv_heads, dim, a.dv_stride}};
   for (int i = 0; i < 3; ++i)
-    for (int j = 0; j < i; ++j) {
-      if (outs[i].lo == outs[i].hi || outs[j].lo == outs[j].hi) continue;
-      const uintptr_t apart = outs[i].lo > outs[j].lo ? outs[i].lo - outs[j].lo : outs[j].lo - outs[i].lo;
-      if (apart < head_bytes || (whole[i] && whole[j] && overlap(outs[i], outs[j]))) return SMC_E_ALIAS;
-    }
+    for (int j = 0; j < i; ++j)
+      if (!apart(grads[i], grads[j], esz)) return SMC_E_ALIAS;
   if (smc::pending_error() != SMC_OK) return SMC_E_CUDA;
   Device dev;
   if (!dev.ok()) return outcome(cudaErrorUnknown);

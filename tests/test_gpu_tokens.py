@@ -680,6 +680,26 @@ def test_fp16_attention_keeps_small_probabilities(queries, h, hk, d, above, at):
     assert float((lse.double() - (above + math.log1p(low))).abs().max()) <= 64 * E * above
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("layout", ["packed rows", "heads in turn", "packed heads"])
+def test_attention_gradients_into_one_buffer(layout, dtype):
+    g = gen(440)
+    n, h, d = 500, 3, 64
+    q, k, v, dout = (normal(g, n, h, d, dtype=dtype) for _ in range(4))
+    o = offsets_of([300, 200])
+    lse = torch.empty(n, h, device="cuda")
+    out = smc.attention(q, k, v, o, lse=lse)
+    ref = smc.attention_backward(dout, q, k, v, out, lse, o)
+    if layout == "packed rows":
+        views = torch.empty(n, 3 * h, d, dtype=dtype, device="cuda").split(h, 1)
+    elif layout == "heads in turn":
+        views = torch.empty(n, h, 3, d, dtype=dtype, device="cuda").unbind(2)
+    else:
+        views = [t.transpose(0, 1) for t in torch.empty(h, 3, n, d, dtype=dtype, device="cuda").unbind(1)]
+    got = smc.attention_backward(dout, q, k, v, out, lse, o, dq=views[0], dk=views[1], dv=views[2])
+    assert all(torch.equal(a, b) and a.data_ptr() == c.data_ptr() for a, b, c in zip(got, ref, views))
+
+
 # ------------------------------------------------ streams, graphs, failures
 def _chain(q, k, v, dout, o, pos, freqs, gamma, beta, stream=None):
     n, h, d = q.shape

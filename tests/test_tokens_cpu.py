@@ -124,6 +124,45 @@ def test_attention_backward_refuses_gradients_that_overlap():
     assert attn_bwd(dks=s2(512, 64), dv=place(9, 126), dvs=s2(512, 64)) == ALIAS
 
 
+
+def _places(p, rows, heads, dim, st):
+    return {p + r * st[0] + h * st[1] + d for r in range(rows) for h in range(heads) for d in range(dim)}
+
+
+# [rows, heads, dim] views of one buffer: (offset, (row stride, head stride)) of dq
+# [6, 4, 8], dk and dv [5, 2, 8], in elements
+GRADIENT_VIEWS = {
+    "packed rows": ((0, (64, 8)), (32, (64, 8)), (48, (64, 8)), True),
+    "packed rows, dk first": ((32, (64, 8)), (0, (64, 8)), (16, (64, 8)), True),
+    "heads in turn": ((0, (96, 24)), (8, (96, 24)), (16, (96, 24)), True),
+    "packed heads": ((0, (8, 200)), (48, (8, 200)), (88, (8, 200)), True),
+    "apart as a whole": ((0, (40, 8)), (300, (24, 8)), (500, (16, 8)), True),
+    "dk over the last head of dq": ((0, (64, 8)), (24, (64, 8)), (48, (64, 8)), False),
+    "dv over the second head of dk": ((0, (64, 8)), (32, (64, 8)), (40, (64, 8)), False),
+    "dq over dk's next row": ((48, (64, 8)), (0, (64, 8)), (16, (64, 8)), False),
+    "rows of different strides that meet later": ((0, (64, 8)), (32, (48, 8)), (1000, (16, 8)), False),
+    "heads that meet later": ((0, (96, 24)), (8, (96, 16)), (1000, (16, 8)), False),
+    "dv in dk's rows, one place too early": ((0, (64, 8)), (32, (64, 8)), (47, (64, 8)), False),
+    "heads that meet in a later row": ((0, (8, 200)), (40, (8, 200)), (88, (8, 200)), False),
+}
+
+
+@pytest.mark.parametrize("name", GRADIENT_VIEWS)
+def test_gradients_that_share_a_place_are_refused(name):
+    q, k, v, fine = GRADIENT_VIEWS[name]
+    sets = [_places(o, r, h, 8, st) for (o, st), (r, h) in zip((q, k, v), ((6, 4), (5, 2), (5, 2)))]
+    assert fine == (sum(map(len, sets)) == len(set.union(*sets)))  # the table itself, place by place
+    if fine and torch.cuda.is_available():
+        pytest.skip("a call that is not refused would follow the made-up addresses")
+    for dtype, size in ((0, 4), (1, 2)):
+        def where(view):
+            return P(4096 + 512 * MB + view[0] * size)
+
+        rc = attn_bwd(n=6, m=5, heads=4, kv_heads=2, dim=8, dq=where(q), dqs=s2(*q[1]), dk=where(k), dks=s2(*k[1]),
+                      dv=where(v), dvs=s2(*v[1]), dtype=dtype)
+        assert (rc == ALIAS) == (not fine), rc
+
+
 def test_nothing_to_do_is_fine():
     assert norm(n=0, x=None, out=None) == 0
     assert norm_bwd(n=0, dy=None, x=None, stats=None, dx=None) == 0
