@@ -179,10 +179,11 @@ def rotary_freqs(pairs: int, axes: int = 1, base: float = 10000.0, factor: float
     * "linear": every frequency divided by factor;
     * "ntk": the base raised to base * factor^(pairs / (pairs - 1)), which
       keeps the fastest pair and divides the slowest by factor;
-    * "yarn": pairs that turn more than 32 times over the `original` length
-      keep their frequency, those that turn less than once are divided by
-      factor, a linear ramp between (in the logarithm of the turns, i.e. the
-      pair index); scale = 0.1 ln(factor) + 1.
+    * "yarn": pairs up to the last that turns 32 times or more over the
+      `original` length (or the first pair) keep their frequency, those from
+      the first place at one turn or less on are divided by factor, a linear
+      ramp in the pair index between, also where no pair is that slow;
+      scale = 0.1 ln(factor) + 1.
     """
     if pairs < 1 or axes < 1 or not base > 1.0 or not factor >= 1.0:
         raise ValueError("need pairs >= 1, axes >= 1, base > 1 and factor >= 1")
@@ -199,11 +200,12 @@ def rotary_freqs(pairs: int, axes: int = 1, base: float = 10000.0, factor: float
         if not original or original < 1:
             raise ValueError("yarn needs the original length")
 
-        def index(turns):  # the pair that turns this often over the original length
+        def index(turns):  # the place, whole or not, of a pair that turns this often over the original length
             return pairs * math.log(original / (turns * 2 * math.pi)) / math.log(base)
 
-        lo, hi = max(math.floor(index(32.0)), 0), min(math.ceil(index(1.0)), pairs - 1)
-        stretch = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        # hi may lie behind the last pair; before the first, every pair turns less than once
+        lo, hi = max(math.floor(index(32.0)), 0), math.ceil(index(1.0))
+        stretch = ((i - lo) / (hi - lo)).clamp(0.0, 1.0) if hi > lo else torch.ones_like(i)
         f = f * (1 - stretch) + f / factor * stretch
         scale = 0.1 * math.log(factor) + 1.0
     return f.expand(axes, -1).contiguous().to(device), scale

@@ -246,3 +246,37 @@ def test_rotary_freqs():
                 dict(pairs=4, scaling="other"), dict(pairs=4, factor=2.0, scaling="yarn")):
         with pytest.raises(ValueError):
             smc.rotary_freqs(**bad)
+
+
+def _yarn_ratio(pairs, base, factor, original):
+    """By definition: pairs up to the last whole index at 32 turns or more over the
+    original length (pair 0 where none is) keep their frequency, from the first at
+    one turn or less it is divided by factor, a linear ramp in the index between."""
+    lo = max(math.floor(pairs * math.log(original / (2 * math.pi * 32)) / math.log(base)), 0)
+    hi = math.ceil(pairs * math.log(original / (2 * math.pi)) / math.log(base))
+    share = [1.0 if i >= hi else max((i - lo) / (hi - lo), 0.0) for i in range(pairs)]
+    return [1.0 / ((1 - s) + s / factor) for s in share]
+
+
+@pytest.mark.parametrize("original", [3, 6, 100, 4096, 65_536, 131_072, 1_048_576, 3_000_000, 100_000_000])
+@pytest.mark.parametrize("pairs, base, factor", [(64, 10_000.0, 8.0), (10, 10_000.0, 2.0), (1, 100.0, 4.0), (7, 500_000.0, 32.0)])
+def test_rotary_freqs_yarn_by_turns(pairs, base, factor, original):
+    ref, _ = smc.rotary_freqs(pairs, base=base)
+    yarn, _ = smc.rotary_freqs(pairs, base=base, factor=factor, scaling="yarn", original=original)
+    ratio = ref[0] / yarn[0]
+    want = torch.tensor(_yarn_ratio(pairs, base, factor, original), dtype=torch.float64)
+    assert torch.allclose(ratio, want, rtol=1e-12)
+    turns = original * ref[0] / (2 * math.pi)
+    assert bool((ratio[turns < 0.999] > factor * (1 - 1e-12)).all())
+    # more than a pair's step above one turn: no longer divided in full
+    assert bool((ratio[turns > 1.001 * base ** (1 / pairs)] < factor * (1 - 1e-3)).all())
+
+
+def test_rotary_freqs_yarn_of_a_long_original():
+    """The slowest of 64 pairs, place 63, turns 1.2, 2.4 and 19 times; the ramps run
+    over the places 40 to 65, 45 to 70 and 59 to 84."""
+    ref, _ = smc.rotary_freqs(64)
+    for original, share in ((65_536, 23 / 25), (131_072, 18 / 25), (1_048_576, 4 / 25)):
+        ratio = 1 / (1 - share + share / 8)
+        yarn, _ = smc.rotary_freqs(64, factor=8.0, scaling="yarn", original=original)
+        assert abs(float(ref[0, -1] / yarn[0, -1]) / ratio - 1) < 1e-12
