@@ -76,9 +76,13 @@ def _strides(t: torch.Tensor):
 class _On:
     """Makes a device and a stream the current ones: the stream then owns the
     tensors made inside, as the caching allocator needs.  Calls on the current
-    device and stream go without (a switch takes longer than a launch)."""
+    device and stream go without (a switch takes longer than a launch).  A
+    stream of another device is refused: the call would leave it for the
+    tensors' own."""
 
     def __init__(self, device: int, stream):
+        if stream is not None and stream.device.index != device:
+            raise ValueError("stream must belong to the tensors' device")
         self.inner = [torch.cuda.device(device)]
         if stream is not None:
             self.inner.append(torch.cuda.stream(stream))

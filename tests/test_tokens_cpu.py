@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import submanifold_sparse_convolution_packed_b200 as smc
+from submanifold_sparse_convolution_packed_b200 import _tokens
 
 ARG, DTYPE, SHAPE, ALIAS, ALIGN = -1, -4, -5, -6, -11
 P = ctypes.c_void_p
@@ -280,3 +281,22 @@ def test_rotary_freqs_yarn_of_a_long_original():
         ratio = 1 / (1 - share + share / 8)
         yarn, _ = smc.rotary_freqs(64, factor=8.0, scaling="yarn", original=original)
         assert abs(float(ref[0, -1] / yarn[0, -1]) / ratio - 1) < 1e-12
+
+
+class _StreamOf:
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+
+@pytest.mark.parametrize("call", [
+    lambda s: smc.layer_norm(torch.zeros(4, 8), stream=s),
+    lambda s: smc.layer_norm_backward(torch.zeros(4, 8), torch.zeros(4, 8), torch.zeros(4, 2), stream=s),
+    lambda s: smc.rotary(torch.zeros(4, 2, 16), torch.zeros(4, 1, dtype=torch.int32),
+                         torch.zeros(1, 8, dtype=torch.float64), stream=s),
+    lambda s: smc.attention(*[torch.zeros(4, 2, 16)] * 3, torch.tensor([0, 4], dtype=torch.int32), stream=s),
+    lambda s: smc.attention_backward(*[torch.zeros(4, 2, 16)] * 5, torch.zeros(4, 2),
+                                     torch.tensor([0, 4], dtype=torch.int32), stream=s)])
+def test_stream_of_another_device_is_refused(call, monkeypatch):
+    monkeypatch.setattr(_tokens, "_device_of", lambda *tensors: 0)  # as if the tensors were on cuda:0
+    with pytest.raises(ValueError, match="stream"):
+        call(_StreamOf(1))
