@@ -353,8 +353,9 @@ SMC_API int smc_layer_norm(const void* x, int64_t n, int64_t c, const void* gamm
  * dy, x : device [n, c]; stats: the forward call's [n, 2]; gamma, beta, act as
  * in the forward call.  dx: device [n, c]; may be dy or x itself.  dgamma,
  * dbeta: device [c] in dtype, overwritten, or NULL (either alone, or both
- * left out).  Sums in fp32, and over the rows in a fixed order: the same call
- * gives the same bits.  Scratch comes from the library's stream-ordered pool.
+ * left out).  Sums in fp32, over the rows at most 512 in one running sum (beyond
+ * 1024 channels: up to 33 million rows), those in fp64, in a fixed order: the same
+ * call gives the same bits.  Scratch comes from the library's stream-ordered pool.
  * n == 0 zeroes dgamma and dbeta.  Asynchronous on `stream`.  Errors as
  * smc_layer_norm, and SMC_E_OOM.
  */

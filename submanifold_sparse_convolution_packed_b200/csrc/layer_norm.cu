@@ -18,7 +18,7 @@
 // gradients of 133,450 x 128 bf16 with SiLU 33 us (3.1 TB/s: the sums over the rows
 // take the registers that more loads in flight would need), of 20,011 x 512 fp32
 // 23 us (5.3 TB/s).  The backward pass keeps the channel sums of its rows in
-// registers (fp32, a few hundred rows each), adds them up per block in a fixed
+// registers (fp32, at most kSumRows rows each), adds them up per block in a fixed
 // order and leaves one partial row per block, which k_ln_fold adds in fp64:
 // no atomics, so the same call gives the same bits.
 #include <type_traits>
@@ -122,6 +122,11 @@ template <typename T, int N> __device__ __forceinline__ void act_slopes(float (&
 // forward pass does, cost 3 us in registers.)
 constexpr int fwd_blocks(int elems) { return elems <= 8 ? 4 : elems <= 16 ? 2 : 1; }
 constexpr int bwd_blocks(int elems) { return elems <= 8 ? 3 : elems <= 16 ? 2 : 1; }
+
+// Rows in one running fp32 sum of the backward pass, at most: its roundings are
+// then below 2^-16 of it, whatever the values (4000 and 6250 rows of a constant were
+// off by 6e-5 and 8e-5).
+constexpr int kSumRows = 512;
 
 template <typename T>
 struct NormArgs {
@@ -560,6 +565,13 @@ struct NormPlan {
   int epc, tpr, blocks;  // epc 0: the long-row kernels
 };
 
+// Row slices of the long rows' channel sums.
+int64_t long_slices(int64_t n) {
+  constexpr int64_t kFew = 64, kMost = 65535;  // to fill the machine; a grid's y (33 million rows)
+  const int64_t few = n < kFew ? n : kFew, s = (n + kSumRows - 1) / kSumRows;
+  return s < few ? few : (s < kMost ? s : kMost);
+}
+
 NormPlan plan(int64_t n, int c, size_t esz, bool aligned, bool backward, int sms) {
   NormPlan p;
   const int wide = static_cast<int>(16 / esz);
@@ -576,6 +588,10 @@ NormPlan plan(int64_t n, int c, size_t esz, bool aligned, bool backward, int sms
   const int elems = (c + p.tpr - 1) / p.tpr;
   const int64_t most = static_cast<int64_t>(backward ? bwd_blocks(elems) : fwd_blocks(elems)) * sms;
   p.blocks = static_cast<int>(need < most ? need : most);
+  if (backward && need > most * kSumRows) {  // whole waves
+    const int64_t sums = most * kSumRows;
+    p.blocks = static_cast<int>((need + sums - 1) / sums * most);
+  }
   return p;
 }
 
@@ -585,8 +601,6 @@ bool aligned_to_chunks(const LayerNormArgs& a) {
                          reinterpret_cast<uintptr_t>(a.out);
   return (bits & 15u) == 0;
 }
-
-constexpr int kLongSlices = 64;  // row slices of the long rows' channel sums
 
 template <typename T>
 cudaError_t launch_typed(const LayerNormArgs& b, int sms, cudaStream_t s) {
@@ -613,7 +627,7 @@ cudaError_t launch_typed(const LayerNormArgs& b, int sms, cudaStream_t s) {
       k_layer_norm_long<T><<<p.blocks, kThreads, 0, s>>>(a);
     } else {
       if (a.part) {  // before dx, which may overwrite dy
-        parts = static_cast<int>(b.n < kLongSlices ? b.n : kLongSlices);
+        parts = static_cast<int>(long_slices(b.n));
         k_layer_norm_long_sums<T><<<dim3((b.c + kThreads - 1) / kThreads, parts), kThreads, 0, s>>>(a);
         ++launches;
       }
@@ -638,7 +652,7 @@ cudaError_t launch_typed(const LayerNormArgs& b, int sms, cudaStream_t s) {
 
 int64_t layer_norm_parts(const LayerNormArgs& a, int sms) {
   const NormPlan p = plan(a.n, a.c, a.dtype == kF32 ? 4 : 2, aligned_to_chunks(a), a.dy != nullptr, sms);
-  return p.epc == 0 ? (a.n < kLongSlices ? a.n : kLongSlices) : p.blocks;
+  return p.epc == 0 ? long_slices(a.n) : p.blocks;
 }
 
 cudaError_t launch_layer_norm(const LayerNormArgs& a, int sms, cudaStream_t s) {

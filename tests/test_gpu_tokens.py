@@ -120,6 +120,42 @@ def test_layer_norm_backward(n, c, dtype, act, affine):
               + 1e-7 * (dtype == F16), "sums")
 
 
+# dbeta of a constant dy whose fp32 running sum would lose nearly half a step with
+# each of its later rows: no more than 512 rows in one running sum of fp32, which
+# is then off by at most 512 / 2 times 2^-24 of itself (each addition by half a
+# step of the sum so far); a block's rows and warps add a few more.
+def test_layer_norm_gradient_sums_of_many_rows():
+    n, c = 114_000_000, 3  # 4000 rows to a group of lanes of a grid that fits the machine once
+    step = 1 + 2.0 ** -13 - 2.0 ** -23
+    x = torch.zeros(n, c, device="cuda")
+    x[:, 0] = 1.0
+    dy = torch.full((n, c), step, device="cuda")
+    st = torch.empty(n, 2, device="cuda")
+    smc.layer_norm(x, out=torch.empty_like(x), stats=st)
+    dbeta, dgamma = torch.empty(c, device="cuda"), torch.empty(c, device="cuda")
+    smc.layer_norm_backward(dy, x, st, dx=dy, dgamma=dgamma, dbeta=dbeta)
+    tol = (512 / 2 + 16) * E
+    assert float((dbeta.double() / (n * step) - 1).abs().max()) <= tol
+    xh = (x[0].double() - st[0, 0].double()) * st[0, 1].double()
+    assert float((dgamma.double() / (n * step * xh) - 1).abs().max()) <= tol + 8 * E
+
+
+def test_layer_norm_gradient_sums_of_many_wide_rows():
+    n, c = 400_000, 1030  # 6250 rows to each of 64 slices
+    step = 1 + 2.0 ** -12 - 2.0 ** -23
+    x = torch.zeros(n, c, device="cuda")
+    x[:, ::2] = 1.0
+    dy = torch.full((n, c), step, device="cuda")
+    st = torch.empty(n, 2, device="cuda")
+    smc.layer_norm(x, out=torch.empty_like(x), stats=st)
+    dbeta, dgamma = torch.empty(c, device="cuda"), torch.empty(c, device="cuda")
+    smc.layer_norm_backward(dy, x, st, dx=dy, dgamma=dgamma, dbeta=dbeta)
+    tol = (512 / 2 + 16) * E
+    assert float((dbeta.double() / (n * step) - 1).abs().max()) <= tol
+    xh = (x[0].double() - st[0, 0].double()) * st[0, 1].double()
+    assert float((dgamma.double() / (n * step * xh) - 1).abs().max()) <= tol + 8 * E
+
+
 def test_layer_norm_in_place_strided_and_unaligned():
     g = gen(5)
     for dtype in (F32, BF16):
