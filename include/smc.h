@@ -458,7 +458,8 @@ SMC_API int smc_attention(const void* q, const int64_t q_stride[2], const void* 
  * passes.  Other items and heads do not enter).  Scratch (fp32 [n, heads] twice, in
  * fp16 four times and [m, kv_heads] once, and partial sums where the queries are
  * split between blocks) comes from the library's stream-ordered pool.
- * Asynchronous on `stream`.  Errors as smc_attention.
+ * Asynchronous on `stream`.  Errors as smc_attention; SMC_E_SHAPE also where the
+ * rows of both sides and twice the items reach 2^31 - 2^20.
  */
 SMC_API int smc_attention_backward(const void* dout, const int64_t dout_stride[2], const void* q,
                            const int64_t q_stride[2], const void* k, const int64_t k_stride[2], const void* v,

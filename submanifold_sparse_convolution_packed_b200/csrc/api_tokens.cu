@@ -76,6 +76,9 @@ bool apart(const View& a, const View& b, size_t esz) {
          separate(std::gcd(rows, heads), lo.dim, hi.dim);
 }
 
+// Rows, and blocks along a grid's x, with room for the blocks of splits.
+constexpr int64_t kRows = (int64_t{1} << 31) - (1 << 20);
+
 bool known_dtype(int32_t d) { return d == SMC_F32 || d == SMC_BF16 || d == SMC_F16; }
 
 size_t size_of(int32_t d) { return d == SMC_F32 ? 4 : 2; }
@@ -103,7 +106,6 @@ int attention_args(smc::AttnArgs& a, const void* q, const int64_t* qs, const voi
   if (!(scale > 0.f) || std::isinf(scale) || (causal != 0 && causal != 1)) return SMC_E_ARG;
   if (!known_dtype(dtype)) return SMC_E_DTYPE;
   if (heads % kv_heads != 0 || heads / kv_heads > 64 || dim > 128 || kv_heads > 65535) return SMC_E_SHAPE;
-  constexpr int64_t kRows = (int64_t{1} << 31) - (1 << 20);
   if (n * (heads / kv_heads) >= kRows || n >= kRows || m >= kRows || n + m + items >= kRows) return SMC_E_SHAPE;
   if (items > 0 && (!q_off || !k_off || (n > 0 && !q) || (m > 0 && (!k || !v)))) return SMC_E_ARG;
   if (misaligned(q_off, 4) || misaligned(k_off, 4)) return SMC_E_ALIGN;
@@ -329,6 +331,7 @@ int smc_attention_backward(const void* dout, const int64_t dout_stride[2], const
   const int rc = attention_args(a, q, q_stride, k, k_stride, v, v_stride, q_offsets, k_offsets, items, n, m, heads,
                                 kv_heads, dim, scale, causal, dtype);
   if (rc != SMC_OK) return rc;
+  if (n + m + 2ll * items >= kRows) return SMC_E_SHAPE;  // both sides' blocks are one grid
   if (items == 0 || (n == 0 && m == 0)) return SMC_OK;
   if (n > 0 && (!dout || !out || !lse || !dq)) return SMC_E_ARG;
   if (m > 0 && (!dk || !dv)) return SMC_E_ARG;

@@ -300,3 +300,9 @@ def test_stream_of_another_device_is_refused(call, monkeypatch):
     monkeypatch.setattr(_tokens, "_device_of", lambda *tensors: 0)  # as if the tensors were on cuda:0
     with pytest.raises(ValueError, match="stream"):
         call(_StreamOf(1))
+
+
+@pytest.mark.parametrize("items", [(1 << 30) - (1 << 19), (1 << 31) - (1 << 21)])
+def test_attention_backward_refuses_items_beyond_its_grid(items):
+    """Each item may cost a block on the queries' and one on the keys' side."""
+    assert attn_bwd(items=items) == SHAPE
