@@ -467,6 +467,32 @@ def test_attention_many_items_and_splits(case, dtype):
     assert all(torch.equal(x, y) for x, y in zip(got, again))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_attention_tens_of_thousands_of_items(dtype):
+    """More items than a block looks at in several rounds (768 to 2304 of them a
+    round), empty ones among them; sampled against the plain form."""
+    rows = [i * 7 % 6 for i in range(30_011)]
+    g = gen(430)
+    o = torch.tensor([0] + rows).cumsum(0).to(torch.int32).cuda()
+    n = sum(rows)
+    q, k, v, dout = (normal(g, n, 2, 64, dtype=dtype) for _ in range(4))
+    lse = torch.empty(n, 2, device="cuda")
+    out = smc.attention(q, k, v, o, lse=lse)
+    got = smc.attention_backward(dout, q, k, v, out, lse, o)
+    smc.status()
+    ends = o.tolist()
+    for i in [0, 1, 766, 767, 768, 769, 1535, 1536, 2303, 2304, 2305, 6912, 9999, 20_000, 29_999, 30_009, 30_010]:
+        a, b = ends[i], ends[i + 1]
+        if a == b:
+            continue
+        one = offsets_of([b - a])
+        r = attention_ref(q[a:b], k[a:b], v[a:b], one, one, 64 ** -0.5, False)
+        close(out[a:b], r["out"], r["tout"], "out")
+        r = attention_ref(q[a:b], k[a:b], v[a:b], one, one, 64 ** -0.5, False, dout[a:b], out[a:b], lse[a:b])
+        for x, y in zip(("dq", "dk", "dv"), got):
+            close(y[a:b], r[x], r["t" + x], x)
+
+
 # splits of the FMA kernels: groups that do not divide a tile, odd widths, items
 # of different lengths, keys that no query sees
 @pytest.mark.parametrize("ql, kl, h, hk, d, causal, dtype", [
