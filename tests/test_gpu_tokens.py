@@ -615,6 +615,23 @@ def test_attention_bad_offsets_are_cut_and_reported(dtype):
     smc.status()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("n, m, causal", [(0, 1500, False), (1500, 0, True), (0, 5, True), (3, 0, False)])
+def test_attention_with_one_side_empty(n, m, causal, dtype):
+    """No queries, or no keys, in the whole call: gradients of what is there are zero."""
+    g = gen(450)
+    qo, ko = offsets_of([n]), offsets_of([m])
+    q, dout = normal(g, n, 4, 64, dtype=dtype), normal(g, n, 4, 64, dtype=dtype)
+    k, v = normal(g, m, 2, 64, dtype=dtype), normal(g, m, 2, 64, dtype=dtype)
+    lse = torch.full((n, 4), math.nan, device="cuda")
+    out = smc.attention(q, k, v, qo, ko, causal=causal, lse=lse, out=torch.full_like(q, math.nan))
+    assert not out.any() and bool((lse == -math.inf).all())
+    grads = [torch.full_like(x, math.nan) for x in (q, k, v)]
+    smc.attention_backward(dout, q, k, v, out, lse, qo, ko, causal=causal, dq=grads[0], dk=grads[1], dv=grads[2])
+    smc.status()
+    assert all(not x.any() for x in grads)
+
+
 def test_attention_far_rows():
     """Element offsets past 32 bits: rows 2^24 elements apart."""
     g = gen(31)
