@@ -1,6 +1,8 @@
 """Binding of the token-wise layers of include/smc.h: layer norm, rotary
 positions, attention.  As in ``_binding``: argument checks and pointers only,
-every step runs in the library's kernels, and there is no fallback."""
+every step runs in the library's kernels, and there is no fallback.  None of the
+calls is recorded by autograd: results never require gradients, and the
+gradients are calls of their own."""
 from __future__ import annotations
 
 import ctypes
@@ -292,7 +294,11 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.
     scale defaults to D ** -0.5; causal lets the last query see every key.
     `lse` (float32 [N, H]), if given, receives the log sum of exponentials,
     which attention_backward takes.  A query without keys gets zeros; rows
-    outside every item are left as they were (unset in a new tensor)."""
+    outside every item are left as they were (unset in a new tensor).
+    bf16 / fp16 run on the tensor cores where D is a multiple of 8, every tensor
+    starts on 16 bytes and the strides are positive multiples of 8 (one k or v head
+    expanded to all is not: give its dense copy, or fewer kv_heads); anything else
+    is right, but about 24 times slower over long items."""
     (n, h, d, m, hk, items), k_offsets, scale = _attention_sizes(q, k, v, offsets, k_offsets, scale)
     if out is not None:
         _result(out, (n, h, d), q.dtype, q.device, "out")
@@ -321,7 +327,8 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     """Gradients of attention (smc_attention_backward): (dq, dk, dv) for dout
     [N, H, D], with the forward call's arguments, its out and its lse.  The
     gradients of shared key/value heads are summed.  dq, dk, dv may be given,
-    also as views of one packed buffer.  Deterministic."""
+    also as views of one packed buffer.  Deterministic.  The tensor cores take the
+    shapes that attention names, dout and the gradients included."""
     (n, h, d, m, hk, items), k_offsets, scale = _attention_sizes(q, k, v, offsets, k_offsets, scale)
     if dout.shape != q.shape or dout.dtype != q.dtype or out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("dout and out must be [N, H, D] of q's dtype")
@@ -346,7 +353,8 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
         dv = q.new_empty((m, hk, d))
     _check(lib().smc_attention_backward(dout.data_ptr(), _strides(dout), q.data_ptr(), _strides(q), k.data_ptr(),
                                         _strides(k), v.data_ptr(), _strides(v), out.data_ptr(), lse.data_ptr(),
-                                        offsets.data_ptr(), k_offsets.data_ptr(), items, n, m, h, hk, d, scale, 1 if causal else 0, dq.data_ptr(), _strides(dq), dk.data_ptr(),
-                                        _strides(dk), dv.data_ptr(), _strides(dv), _DTYPES[q.dtype],
-                                        _current_stream(dev)), "smc_attention_backward")
+                                        offsets.data_ptr(), k_offsets.data_ptr(), items, n, m, h, hk, d, scale,
+                                        1 if causal else 0, dq.data_ptr(), _strides(dq), dk.data_ptr(), _strides(dk),
+                                        dv.data_ptr(), _strides(dv), _DTYPES[q.dtype], _current_stream(dev)),
+           "smc_attention_backward")
     return dq, dk, dv

@@ -24,7 +24,9 @@
 // machine idle, what passes is split between blocks.  A warp whose rows are not there
 // only loads: one query over 300 keys takes 25 us, 33 us with all warps at work.
 // fp32, items of 3000 and 1200 rows, 8 heads over 4, 32 / 64 / 128 channels:
-// forward 23 / 30 / 31 TFLOP/s, backward 21 / 25 / 25.
+// forward 23 / 30 / 31 TFLOP/s, backward 21 / 25 / 25.  The backward kernel's two blocks
+// to an SM leave 128 registers to a thread, which spills there at up to 64 channels
+// (at 64: fp32 140 bytes, 16-bit types 180).
 #include "attn_join.cuh"
 #include "kernels.h"
 #include "tokens.cuh"

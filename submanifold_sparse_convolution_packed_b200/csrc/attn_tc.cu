@@ -30,9 +30,12 @@
 //
 // What bounds it: at 64 channels the exponentials (16 a clock and SM: 0.71 ms of
 // the first figure), not the products (0.50 ms); a chain's own latency for the rest.
-// Measured: 20,011 rows, 8 heads of 64, bf16: 1.09 ms, 750 TFLOP/s; 512 items of 1 to
+// Measured: 20,011 rows, 8 heads of 64, bf16: 1.09 ms, 750 TFLOP/s, 8 heads of 128:
+// 1.62 to 1.74 ms, 940 to 1010 TFLOP/s (causal 0.90 to 0.96 ms); 512 items of 1 to
 // 512 rows, fp16: 0.26 ms; 8 single queries over 1,000 to 32,768 keys, 16 heads of
-// 128 over 4: 53 us, 4.5 TB/s.
+// 128 over 4: 53 us, 4.5 TB/s.  Registers are short: at 128 channels a thread spills
+// 68 bytes (one tile 44) and reads 148 (108) of them again, at 64 channels 20 (36) and
+// 24 (56).
 #include <type_traits>
 
 #include "attn_join.cuh"
@@ -478,7 +481,12 @@ struct FwdPlan {
 };
 
 // One tile to a CTA where items are short on average: such a CTA's start and
-// end are most of its life, and the others on its SM fill them.
+// end are most of its life, and the others on its SM fill them.  (51,200 rows in
+// items of 256, 512, 1024, 2048, 5000 rows, 8 heads, one tile / two: of 64 channels
+// 76 / 145, 103 / 160, 175 / 210, 304 / 324, 713 / 690 us, of 128 channels 127 / 192,
+// 165 / 228, 255 / 317, 453 / 491, 1095 / 1049 us: the border could lie at 2048 rows.
+// The average misjudges one item of 8000 rows beside 1000 of one row: 551 / 557 and
+// 884 / 720 us.)
 FwdPlan fwd_plan(const AttnArgs& a, int sms) {
   const int group = a.heads / a.kv_heads, qpt = kRows / group;
   FwdPlan s = {};

@@ -15,11 +15,13 @@
 // half a turn are in fp64; only the reduced angle is rounded to fp32, and
 // sincospif takes it from there.  One thread serves one chunk of channels of
 // a row (16 bytes, or one pair where strides or sizes do not allow that) for
-// a run of heads, so the angles are paid once per run.  The bytes are HBM's (82 MB,
-// 12.5 us for 20,011 x 16 x 64 bf16 over three axes), but the angles, fp64 and a
-// sine and cosine each, are work that the first loads only hide in part (21 us where
-// they were issued behind the angles): 19 us there, 4.4 TB/s.  The run of heads is as
-// long as the number of rows allows with the machine full.
+// a run of heads, so the angles are paid once per run.  The bytes (82 MB) take HBM
+// 12.5 us for 20,011 x 16 x 64 bf16 over three axes, the kernel 19 us, 4.4 TB/s:
+// latency, of the angles (fp64, then a sine and cosine) and of the loads, which are
+// issued ahead of them (21 us behind them); HBM is at 27%, the FMA pipe at 18%, the
+// special-function unit at 10% of their peaks.  Half layout with pairs that are not
+// whole 16-byte chunks takes 22 us for a dense x in L2 (interleaved 16 us).  The run of
+// heads is as long as the number of rows allows with the machine full.
 #include "kernels.h"
 #include "tokens.cuh"
 
